@@ -635,6 +635,172 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
                                    const int64_t* strides,
                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Sequence operators: memory over rollouts for the policies and value
+ * functions whose targets the calls above compute.
+ *
+ * Gated recurrence with a matrix state.  Per environment n and head h, with
+ * query and key head h / (heads / kv_heads) and a state S of
+ * [key_dim, value_dim]:
+ *
+ *   S_t = (cut_t ? 0 : exp(log_decay_t) S_{t-1}) + k_t v_t^T
+ *   out_t = scale * S_t^T q_t
+ *
+ * cut_t where reset_t is nonzero (the step starts an episode) or log_decay_t
+ * is -infinity.  S before the first step is initial_state (0 if NULL); it is
+ * dropped where step 0 is cut.
+ *   - Arrays: q, k [N, T, kv_heads, key_dim]; v, out [N, T, heads,
+ *     value_dim]; log_decay [N, T, heads]; reset [N, T] u8 (nullable); all
+ *     of one storage type.  States are float32 in every variant,
+ *     [N, heads, key_dim, value_dim], contiguous: initial_state (nullable)
+ *     in, final_state (nullable: not written) out.
+ *   - strides: NULL (all contiguous), or a HOST array with three strides per
+ *     array -- environment, step, head, in elements, 0 meaning that of a
+ *     contiguous array -- in the order the arrays appear in the signature,
+ *     inputs and outputs alike (forward: q, k, v, log_decay, reset, out;
+ *     backward: grad_out, q, k, v, log_decay, reset, grad_q, grad_k, grad_v,
+ *     grad_log_decay; reset's head stride is ignored).  Elements of a row are
+ *     consecutive.  Views of one projection buffer and time-major arrays are
+ *     read and written in place; outputs must address every element once.
+ *     Strides, bases and dims that keep every row on 16 bytes are fastest.
+ *   - key_dim and value_dim 1 to 128; heads a multiple of kv_heads, at most
+ *     65536; N * heads at most 2^23; N and T as above.
+ *   - Inputs must be finite, log_decay finite or -infinity (and is meant to be
+ *     <= 0: growth is computed as given and may overflow); exact zeros where
+ *     a cut separates two steps, for finite inputs.
+ *   - Sums and states are fp32 (or more); outputs are rounded once.  A call
+ *     gives the same bits every time.
+ *   - workspace: lrs_gated_recurrence_workspace_bytes(...) bytes, 16-byte
+ *     aligned, any contents; NULL with 0 bytes where that is 0.  Nothing in
+ *     it outlives the call's kernels.  Do not pass the estimators' workspace:
+ *     that one must not be modified.
+ *   - Outputs, workspace, states and stream: as for every call above.
+ *
+ * Backward: the gradients of q, k, v and log_decay (of the same storage
+ * type; those of q and k summed over the heads that share them) and of
+ * initial_state (nullable: not written), from grad_out and grad_final_state
+ * (nullable = 0).  grad_log_decay is 0 at cut steps.  The states of the
+ * forward call are computed again; nothing of it has to be kept but its
+ * inputs.
+ *
+ * Step: one step of every environment: q, k [N, kv_heads, key_dim], v, out
+ * [N, heads, value_dim], log_decay [N, heads], reset [N]; strides as above
+ * with the step stride ignored.  next_state may be state itself (updated in
+ * place) and must not overlap it otherwise.                               */
+size_t lrs_gated_recurrence_workspace_bytes(int64_t num_envs, int64_t seq_len, int64_t heads,
+                                            int64_t kv_heads, int64_t key_dim, int64_t value_dim,
+                                            int backward);
+lrs_status lrs_gated_recurrence_f32(int64_t num_envs, int64_t seq_len, int64_t heads, int64_t kv_heads,
+    int64_t key_dim, int64_t value_dim, const float* q, const float* k, const float* v,
+    const float* log_decay, const uint8_t* reset, const float* initial_state, float scale,
+    float* out, float* final_state, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+lrs_status lrs_gated_recurrence_backward_f32(int64_t num_envs, int64_t seq_len, int64_t heads,
+    int64_t kv_heads, int64_t key_dim, int64_t value_dim, const float* grad_out, const float* q,
+    const float* k, const float* v, const float* log_decay, const uint8_t* reset,
+    const float* initial_state, const float* grad_final_state, float scale, float* grad_q,
+    float* grad_k, float* grad_v, float* grad_log_decay, float* grad_initial_state,
+    const int64_t* strides, void* workspace, size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_gated_recurrence_step_f32(int64_t num_envs, int64_t heads, int64_t kv_heads,
+    int64_t key_dim, int64_t value_dim, const float* q, const float* k, const float* v,
+    const float* log_decay, const uint8_t* reset, const float* state, float scale, float* out,
+    float* next_state, const int64_t* strides, hipStream_t stream);
+
+lrs_status lrs_gated_recurrence_bf16(int64_t num_envs, int64_t seq_len, int64_t heads, int64_t kv_heads,
+    int64_t key_dim, int64_t value_dim, const lrs_bf16* q, const lrs_bf16* k, const lrs_bf16* v,
+    const lrs_bf16* log_decay, const uint8_t* reset, const float* initial_state, float scale,
+    lrs_bf16* out, float* final_state, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+lrs_status lrs_gated_recurrence_backward_bf16(int64_t num_envs, int64_t seq_len, int64_t heads,
+    int64_t kv_heads, int64_t key_dim, int64_t value_dim, const lrs_bf16* grad_out, const lrs_bf16* q,
+    const lrs_bf16* k, const lrs_bf16* v, const lrs_bf16* log_decay, const uint8_t* reset,
+    const float* initial_state, const float* grad_final_state, float scale, lrs_bf16* grad_q,
+    lrs_bf16* grad_k, lrs_bf16* grad_v, lrs_bf16* grad_log_decay, float* grad_initial_state,
+    const int64_t* strides, void* workspace, size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_gated_recurrence_step_bf16(int64_t num_envs, int64_t heads, int64_t kv_heads,
+    int64_t key_dim, int64_t value_dim, const lrs_bf16* q, const lrs_bf16* k, const lrs_bf16* v,
+    const lrs_bf16* log_decay, const uint8_t* reset, const float* state, float scale, lrs_bf16* out,
+    float* next_state, const int64_t* strides, hipStream_t stream);
+
+lrs_status lrs_gated_recurrence_f16(int64_t num_envs, int64_t seq_len, int64_t heads, int64_t kv_heads,
+    int64_t key_dim, int64_t value_dim, const lrs_f16* q, const lrs_f16* k, const lrs_f16* v,
+    const lrs_f16* log_decay, const uint8_t* reset, const float* initial_state, float scale,
+    lrs_f16* out, float* final_state, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+lrs_status lrs_gated_recurrence_backward_f16(int64_t num_envs, int64_t seq_len, int64_t heads,
+    int64_t kv_heads, int64_t key_dim, int64_t value_dim, const lrs_f16* grad_out, const lrs_f16* q,
+    const lrs_f16* k, const lrs_f16* v, const lrs_f16* log_decay, const uint8_t* reset,
+    const float* initial_state, const float* grad_final_state, float scale, lrs_f16* grad_q,
+    lrs_f16* grad_k, lrs_f16* grad_v, lrs_f16* grad_log_decay, float* grad_initial_state,
+    const int64_t* strides, void* workspace, size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_gated_recurrence_step_f16(int64_t num_envs, int64_t heads, int64_t kv_heads,
+    int64_t key_dim, int64_t value_dim, const lrs_f16* q, const lrs_f16* k, const lrs_f16* v,
+    const lrs_f16* log_decay, const uint8_t* reset, const float* state, float scale, lrs_f16* out,
+    float* next_state, const int64_t* strides, hipStream_t stream);
+
+/* Norm of queries and keys for each head, with the position rotation in the
+ * same pass.  Per token and head, over the head's dim elements x (w: q_weight
+ * or k_weight [dim]):
+ *
+ *   z = x * w / sqrt(mean(x^2) + eps)
+ *
+ * then the first rotary_dim elements of z are rotated in pairs (a, b) by the
+ * token's position p: (z_a cos - z_b sin, z_b cos + z_a sin), with cos =
+ * table[p][j] and sin = table[p][rotary_dim / 2 + j] for pair j, which is
+ * (j, j + rotary_dim / 2), or (2j, 2j + 1) where interleaved is 1.
+ *   - Arrays: q, q_out [N, T, q_heads, dim]; k, k_out [N, T, k_heads, dim];
+ *     positions [N, T] int32; weights [dim]; table [max_positions,
+ *     rotary_dim] float32 in every variant, contiguous.  Positions outside
+ *     the table give NaN in every output of their token.
+ *   - strides as for the gated recurrence (forward: q, k, positions, q_out,
+ *     k_out; backward: grad_q_out, grad_k_out, q, k, positions, grad_q,
+ *     grad_k).
+ *   - dim 1 to 256; rotary_dim even, 0 (no rotation: table and positions may
+ *     be NULL) to dim; heads 1 to 65536 each; eps >= 0.
+ * Backward: the gradients of q and k, and those of the weights summed over
+ * every token and head in a fixed order (all outputs required); workspace
+ * lrs_qk_norm_rotation_workspace_bytes(...) bytes, any contents.          */
+size_t lrs_qk_norm_rotation_workspace_bytes(int64_t num_envs, int64_t seq_len, int64_t q_heads,
+                                            int64_t k_heads, int64_t dim);
+lrs_status lrs_qk_norm_rotation_f32(int64_t num_envs, int64_t seq_len, int64_t q_heads, int64_t k_heads,
+    int64_t dim, int64_t rotary_dim, const float* q, const float* k, const float* q_weight,
+    const float* k_weight, const float* table, int64_t max_positions, const int32_t* positions,
+    float eps, int interleaved, float* q_out, float* k_out, const int64_t* strides,
+    hipStream_t stream);
+lrs_status lrs_qk_norm_rotation_backward_f32(int64_t num_envs, int64_t seq_len, int64_t q_heads,
+    int64_t k_heads, int64_t dim, int64_t rotary_dim, const float* grad_q_out,
+    const float* grad_k_out, const float* q, const float* k, const float* q_weight,
+    const float* k_weight, const float* table, int64_t max_positions, const int32_t* positions,
+    float eps, int interleaved, float* grad_q, float* grad_k, float* grad_q_weight,
+    float* grad_k_weight, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+
+lrs_status lrs_qk_norm_rotation_bf16(int64_t num_envs, int64_t seq_len, int64_t q_heads, int64_t k_heads,
+    int64_t dim, int64_t rotary_dim, const lrs_bf16* q, const lrs_bf16* k, const lrs_bf16* q_weight,
+    const lrs_bf16* k_weight, const float* table, int64_t max_positions, const int32_t* positions,
+    float eps, int interleaved, lrs_bf16* q_out, lrs_bf16* k_out, const int64_t* strides,
+    hipStream_t stream);
+lrs_status lrs_qk_norm_rotation_backward_bf16(int64_t num_envs, int64_t seq_len, int64_t q_heads,
+    int64_t k_heads, int64_t dim, int64_t rotary_dim, const lrs_bf16* grad_q_out,
+    const lrs_bf16* grad_k_out, const lrs_bf16* q, const lrs_bf16* k, const lrs_bf16* q_weight,
+    const lrs_bf16* k_weight, const float* table, int64_t max_positions, const int32_t* positions,
+    float eps, int interleaved, lrs_bf16* grad_q, lrs_bf16* grad_k, lrs_bf16* grad_q_weight,
+    lrs_bf16* grad_k_weight, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+
+lrs_status lrs_qk_norm_rotation_f16(int64_t num_envs, int64_t seq_len, int64_t q_heads, int64_t k_heads,
+    int64_t dim, int64_t rotary_dim, const lrs_f16* q, const lrs_f16* k, const lrs_f16* q_weight,
+    const lrs_f16* k_weight, const float* table, int64_t max_positions, const int32_t* positions,
+    float eps, int interleaved, lrs_f16* q_out, lrs_f16* k_out, const int64_t* strides,
+    hipStream_t stream);
+lrs_status lrs_qk_norm_rotation_backward_f16(int64_t num_envs, int64_t seq_len, int64_t q_heads,
+    int64_t k_heads, int64_t dim, int64_t rotary_dim, const lrs_f16* grad_q_out,
+    const lrs_f16* grad_k_out, const lrs_f16* q, const lrs_f16* k, const lrs_f16* q_weight,
+    const lrs_f16* k_weight, const float* table, int64_t max_positions, const int32_t* positions,
+    float eps, int interleaved, lrs_f16* grad_q, lrs_f16* grad_k, lrs_f16* grad_q_weight,
+    lrs_f16* grad_k_weight, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+
 /* Diagnostics and tuning (process-wide; not for concurrent use).
  * force_lookback != 0: every later call takes the multi-block carry-
  *   propagation path, even where whole rows fit in one tile.

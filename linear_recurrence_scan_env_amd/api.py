@@ -61,6 +61,19 @@ for _name, _args in list(_SIGS.items()):
     _stem, _sfx = _name.rsplit("_", 1)
     _SIGS[f"{_stem}_tm_{_sfx}"] = _args
 
+# the sequence operators (row strides and any time layout in their strides)
+_SEQ_SIGS = {
+    "lrs_gated_recurrence": [_I64] * 6 + [_P] * 6 + [_F, _P, _P] + _TAIL,
+    "lrs_gated_recurrence_backward": [_I64] * 6 + [_P] * 8 + [_F] + [_P] * 5 + _TAIL,
+    "lrs_gated_recurrence_step": [_I64] * 5 + [_P] * 6 + [_F, _P, _P, _P, _P],
+    "lrs_qk_norm_rotation": [_I64] * 6 + [_P] * 5 + [_I64, _P, _F, ctypes.c_int] + [_P] * 4,
+    "lrs_qk_norm_rotation_backward": [_I64] * 6 + [_P] * 7 + [_I64, _P, _F, ctypes.c_int] +
+                                     [_P] * 4 + _TAIL,
+}
+for _name, _args in _SEQ_SIGS.items():
+    for _sfx in ("f32", "bf16", "f16"):
+        _SIGS[f"{_name}_{_sfx}"] = _args
+
 # storage dtype of the floating-point streams -> entry-point suffix
 _SUFFIX = {torch.float32: "f32", torch.bfloat16: "bf16", torch.float16: "f16"}
 
@@ -112,6 +125,10 @@ def load():
         lib.lrs_last_error.restype = ctypes.c_char_p
         lib.lrs_workspace_bytes.restype = _SZ
         lib.lrs_workspace_bytes.argtypes = [ctypes.c_int, _I64, _I64]
+        lib.lrs_gated_recurrence_workspace_bytes.restype = _SZ
+        lib.lrs_gated_recurrence_workspace_bytes.argtypes = [_I64] * 6 + [ctypes.c_int]
+        lib.lrs_qk_norm_rotation_workspace_bytes.restype = _SZ
+        lib.lrs_qk_norm_rotation_workspace_bytes.argtypes = [_I64] * 5
         lib.lrs_debug_set_schedule.restype = ctypes.c_int
         lib.lrs_debug_set_schedule.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int]
         lib.lrs_debug_set_time_major_waves.argtypes = [ctypes.c_int]

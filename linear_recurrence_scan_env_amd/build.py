@@ -22,10 +22,11 @@ CSRC = os.path.join(PKG, "csrc")
 # One translation unit per group of entry points, compiled in parallel.
 SOURCES = [os.path.join(CSRC, f) for f in ("abi.hip", "noalloc.hip", "floor.hip")] + [
     os.path.join(CSRC, f"{group}{sfx}.hip")
-    for group in ("returns", "offpolicy", "forward", "affine") for sfx in ("", "_bf16", "_f16")]
+    for group in ("returns", "offpolicy", "forward", "affine", "recurrence", "rotation")
+    for sfx in ("", "_bf16", "_f16")]
 HEADERS = [os.path.join(CSRC, f)
            for f in ("launch.hpp", "scan_core.hpp", "estimators.hpp", "entries.hpp",
-                     "timemajor.hpp")] + \
+                     "timemajor.hpp", "sequence.hpp", "recurrence.hpp", "rotation.hpp")] + \
     [os.path.join(ROOT, "include", "lrs.h")]
 DEPS = SOURCES + HEADERS
 LIB = os.path.join(PKG, "liblrs.so")
