@@ -25,6 +25,8 @@
 // k_s . dk_s with all steps from it on; what lies wholly behind t cancels.
 #pragma once
 
+#include <algorithm>
+
 #include "sequence.hpp"
 
 namespace lrs {
@@ -33,8 +35,8 @@ constexpr int kMaxDim = 128;  // largest key and value dimension
 
 // One pass over the sequence.  init: the state before the first step in scan
 // order; last: where the state after the last one goes; both [N, H, key_dim,
-// value_dim] and nullable.  y_scale multiplies y, u_scale what enters the
-// state.  dot (nullable): receives y_i . d_i per [N, H, T]; cross (nullable):
+// value_dim] and nullable.  y_scale multiplies y, p_scale the products a . b,
+// u_scale what enters the state.  dot (nullable): receives y_i . d_i per [N, H, T]; cross (nullable):
 // <final state, meet> per [N, H].
 struct PassArgs {
     SeqView a, b, c, d, y;
@@ -43,7 +45,7 @@ struct PassArgs {
     const float* meet;
     float* dot;
     float* cross;
-    float y_scale, u_scale;
+    float y_scale, p_scale, u_scale;
     int32_t da, dc;  // dims of a and b, of c and y
     uint8_t reverse, transposed, y_f32;
 };
@@ -61,97 +63,432 @@ __device__ __forceinline__ int64_t state_at(const PassArgs& p, int r, int c)
     return p.transposed ? (int64_t)c * p.da + r : (int64_t)r * p.dc + c;
 }
 
-// The step's decay factor, 0 where it is cut.
+// ------------------------------------------------------- matrix instructions
+// All products run as bf16 matrix instructions with fp32 sums.  A value is a
+// sum of bf16 limbs, each the rounding of what the ones before leave: bf16
+// inputs are one limb, f16 inputs two (exact), f32 inputs three.  What is
+// computed in fp32 on the way to another product (weighted products, states)
+// is split as far as its result needs.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
 template <class D>
-__device__ __forceinline__ float decay_of(const RecurrenceArgs& x, int64_t n, int64_t t, int h)
+constexpr int kLimbs = std::is_same<D, bf16_t>::value ? 1 : std::is_same<D, f16_t>::value ? 2 : 3;
+
+template <int L>
+struct Frag {
+    bf16x8 x[L];
+};
+
+template <int L>
+__device__ __forceinline__ Frag<L> split(f32x8 v)
 {
-    const float g = to_f32(*seq_row<D>(x.g, n, t, h));
-    const bool reset = x.reset.p != nullptr && *seq_row<uint8_t>(x.reset, n, t, 0) != 0;
-    return reset ? 0.0f : __expf(g);
+    Frag<L> f;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        f.x[l] = __builtin_convertvector(v, bf16x8);
+        if (l + 1 < L) v -= __builtin_convertvector(f.x[l], f32x8);
+    }
+    return f;
 }
 
-// One block walks one head's sequence step by step; a thread holds one column
-// of the state.
-constexpr int kStage = 16;  // steps staged in LDS at a time
-
-template <class D, int DA>
-__global__ __launch_bounds__(kMaxDim) void recurrence_steps(const RecurrenceArgs x)
+// acc += A^T B over 32 products per lane group, all limb products down to the
+// smaller operand's last limb.
+template <int LA, int LB>
+__device__ __forceinline__ f32x4 mma(const Frag<LA>& a, const Frag<LB>& b, f32x4 acc)
 {
-    __shared__ float sa[kStage][DA], sb[kStage][DA], sf[kStage];
-    __shared__ float part[kMaxDim / kWave];
+    constexpr int level = LA > LB ? LA : LB;
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+#pragma unroll
+        for (int j = 0; j < LB; ++j)
+            if (i + j < level)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x[i], b.x[j], acc, 0, 0, 0);
+    return acc;
+}
+
+// A tile of kChunk steps of up to W elements in LDS, one plane per limb.  The
+// 16-byte units of a row are permuted by its index, so that both ways of
+// reading a fragment (16 rows at one unit; 4 rows at 16 neighbouring columns,
+// transposed) touch every bank once.
+constexpr int kChunk = 64;
+constexpr int kTile = 16;
+
+template <int W, int L>
+struct StepTile {
+    uint16_t e[L][kChunk * W];
+
+    static __device__ __forceinline__ int at(int row, int col)
+    {
+        const int mix = W == 128 ? ((row & 7) << 1) | ((row >> 3) & 1)
+                                 : (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
+        return row * W + (((col >> 3) ^ mix) << 3) + (col & 7);
+    }
+    // A fragment of 16 rows (from `row`) over 32 columns (from `col`): lane l
+    // holds row l % 16, columns 4 (l / 16) + 0..3 and 16 more.  Both operands
+    // of every product use this order of the 32.
+    __device__ __forceinline__ Frag<L> rows(int row, int col, int lane) const
+    {
+        const int r = row + (lane & 15), c = col + (lane >> 4) * 4;
+        Frag<L> f;
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            const s16x4 lo = *reinterpret_cast<const s16x4*>(&e[l][at(r, c)]);
+            const s16x4 hi = *reinterpret_cast<const s16x4*>(&e[l][at(r, c + 16)]);
+            f.x[l] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        return f;
+    }
+    // The transposed fragment: lane l holds column col + l % 16 of the rows
+    // row + 4 (l / 16) + 0..3 and 16 more.  A transposing read hands the 16
+    // lanes of a group four rows of 16 columns, 8 bytes read by each lane.
+    __device__ __forceinline__ Frag<L> columns(int row, int col, int lane) const
+    {
+        const int r = row + (lane >> 4) * 4 + ((lane & 15) >> 2), c = col + (lane & 3) * 4;
+        Frag<L> f;
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][at(r, c)]);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][at(r + 16, c)]);
+            f.x[l] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        return f;
+    }
+};
+
+// Eight elements of a row from column c on, zero beyond `dim`.
+template <class D>
+__device__ __forceinline__ f32x8 load8(const D* row, int c, int dim, bool vec)
+{
+    f32x8 v = {};
+    if (vec && c + 8 <= dim) {
+        if constexpr (sizeof(D) == 4) {
+            const f32x4 a = *reinterpret_cast<const f32x4*>(row + c);
+            const f32x4 b = *reinterpret_cast<const f32x4*>(row + c + 4);
+            v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(row + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;
+                unpack2<D>(w[k], lo, hi);
+                v[2 * k] = lo;
+                v[2 * k + 1] = hi;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k < dim) v[k] = to_f32(row[c + k]);
+    }
+    return v;
+}
+
+// Steps t0 .. t0 + count - 1 of one head into a tile, zero beyond them.
+template <class D, int W>
+__device__ __forceinline__ void stage(StepTile<W, kLimbs<D>>& tile, const SeqView& view, int64_t n, int h,
+                                      int64_t t0, int count, int dim)
+{
+    constexpr int L = kLimbs<D>;
+    const int units = (dim + 31) / 32 * 4;  // what the products read
+    for (int u = threadIdx.x; u < kChunk * units; u += blockDim.x) {
+        const int row = u / units, c = (u % units) * 8;
+        f32x8 v = {};
+        if (row < count) v = load8(seq_row<D>(view, n, t0 + row, h), c, dim, view.vec != 0);
+        const Frag<L> f = split<L>(v);
+#pragma unroll
+        for (int l = 0; l < L; ++l) *reinterpret_cast<bf16x8*>(&tile.e[l][tile.at(row, c)]) = f.x[l];
+    }
+}
+
+// The decays of a chunk of 64 steps, in four tiles of 16.  With p the running
+// sum of log2 decays within a tile (in 64 bits: a strong decay before a weak
+// one would cost an fp32 sum the weak one's digits) and m the running count of
+// its cuts, for steps j < i of one tile D(i, j) = 2^(p_i - p_j) where m_i =
+// m_j, and for steps of tiles B > A, D(i, j) = head_i (tiles between) tail_j,
+// where each factor is at most 1 for log decays up to 0.
+struct ChunkDecay {
+    double p[kChunk];
+    int m[kChunk];
+    float head[kChunk];   // from the start of its tile to this step, inclusive
+    float tail[kChunk];   // from this step, exclusive, to the end of its tile
+    float entry[kChunk];  // from the start of the chunk, inclusive
+    float exit[kChunk];   // to the end of the chunk
+    float whole[4];       // of each tile
+    float total;          // of the chunk
+};
+
+template <class D>
+__device__ __forceinline__ void chunk_decay(ChunkDecay& s, const RecurrenceArgs& x, int64_t n, int h,
+                                            int64_t t0, int count, int lane)
+{
+    double p = 0.0;
+    int m = 0;
+    if (lane < count) {
+        const float g = to_f32(*seq_row<D>(x.g, n, t0 + lane, h));
+        const bool reset = x.reset.p != nullptr && *seq_row<uint8_t>(x.reset, n, t0 + lane, 0) != 0;
+        m = reset || g == -INFINITY;
+        p = m ? 0.0 : (double)g * 1.4426950408889634;
+    }
+    const int i = lane & 15;
+#pragma unroll
+    for (int o = 1; o < kTile; o <<= 1) {
+        const double q = __shfl_up(p, o);
+        const int k = __shfl_up(m, o);
+        if (i >= o) {
+            p += q;
+            m += k;
+        }
+    }
+    const double ptot = __shfl(p, lane | 15);
+    const int mtot = __shfl(m, lane | 15);
+    const float head = m ? 0.0f : exp2f((float)p);
+    const float tail = m != mtot ? 0.0f : exp2f((float)(ptot - p));
+    const float whole = mtot ? 0.0f : exp2f((float)ptot);
+    float w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __shfl(whole, k * kTile);
+    const int tile = lane >> 4;
+    float before = 1.0f, after = 1.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (k < tile) before *= w[k];
+        if (k > tile) after *= w[k];
+    }
+    s.p[lane] = p;
+    s.m[lane] = m;
+    s.head[lane] = head;
+    s.tail[lane] = tail;
+    s.entry[lane] = before * head;
+    s.exit[lane] = after * tail;
+    if (lane < 4) s.whole[lane] = w[lane];
+    if (lane == 0) s.total = w[0] * w[1] * w[2] * w[3];
+}
+
+// A pass by matrix instructions, 64 steps at a time.  A wave holds 32 columns
+// of the state, all its rows, in accumulators; the block's waves share the
+// steps in LDS.  Per chunk, with X, Z the weights from the chunk's start and to
+// its end in scan order:
+//     y^T = S^T a^T X + c^T (D o (a b^T))^T        (S before the chunk)
+//     S   = total S + b^T (Z c)
+// Results of one product leave the matrix unit in the order in which the next
+// one takes its operand (16 columns by 4 consecutive rows per lane group), so
+// a b^T and S go from product to product in registers.
+template <class D, int W>
+struct PassShared {
+    StepTile<W, kLimbs<D>> a, b, c;
+    ChunkDecay decay;
+    float dot[4][kChunk];
+    float cross[4];
+};
+
+template <class D, int W, bool kPrecise>
+__global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
+{
+    constexpr int L = kLimbs<D>;
+    constexpr int LS = L > 1 ? L : (kPrecise ? 2 : 1);  // limbs of a b^T and of the state
+    constexpr int LW = 3;                               // limbs of what enters the state
+    constexpr int K = W / 32;
+    __shared__ PassShared<D, W> sh;
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int group = lane >> 4, col = lane & 15;
     const int pass = blockIdx.x % x.passes;
     const int64_t head = blockIdx.x / x.passes;
     const PassArgs& p = x.pass[pass];
     const int64_t n = head / x.H;
     const int h = (int)(head % x.H);
-    const int col = threadIdx.x;
-    const bool active = col < p.dc;
+    const int c0 = wave * 32;
     const int64_t at = head * p.da * p.dc;
-    float S[DA];
+    const bool back = p.reverse != 0;
+
+    // S[2 k + s][u][r]: row 32 k + 16 s + 4 group + r, column c0 + 16 u + col
+    f32x4 S[2 * K][2];
 #pragma unroll
-    for (int r = 0; r < DA; ++r)
-        S[r] = p.init && active && r < p.da ? p.init[at + state_at(p, r, col)] : 0.0f;
-    for (int64_t done = 0; done < x.T; done += kStage) {
-        const int m = (int)(x.T - done < kStage ? x.T - done : kStage);
-        __syncthreads();
-        for (int e = col; e < kStage * DA; e += blockDim.x) {
-            const int s = e / DA, r = e % DA;
-            const int64_t t = p.reverse ? x.T - 1 - (done + s) : done + s;
-            const bool in = s < m && r < p.da;
-            sa[s][r] = in ? to_f32(seq_row<D>(p.a, n, t, h)[r]) : 0.0f;
-            sb[s][r] = in ? to_f32(seq_row<D>(p.b, n, t, h)[r]) : 0.0f;
-        }
-        if (col < m) sf[col] = decay_of<D>(x, n, p.reverse ? x.T - 1 - (done + col) : done + col, h);
-        __syncthreads();
-        for (int s = 0; s < m; ++s) {
-            const int64_t t = p.reverse ? x.T - 1 - (done + s) : done + s;
-            const float c = active ? to_f32(seq_row<D>(p.c, n, t, h)[col]) * p.u_scale : 0.0f;
-            // against time, the decay of a step applies to what it passes on
-            const float f = p.reverse ? 1.0f : sf[s];
-            float y = 0.0f;
+    for (int k = 0; k < 2 * K; ++k)
 #pragma unroll
-            for (int r = 0; r < DA; ++r) {
-                const float before = f == 0.0f ? 0.0f : S[r] * f;
-                S[r] = fmaf(sb[s][r], c, before);
-                y = fmaf(sa[s][r], S[r], y);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
+                S[k][u][r] = p.init && row < p.da && c < p.dc ? p.init[at + state_at(p, row, c)] : 0.0f;
             }
-            y *= p.y_scale;
-            if (p.reverse)
+
+    const int64_t chunks = (x.T + kChunk - 1) / kChunk;
+    for (int64_t i = 0; i < chunks; ++i) {
+        const int64_t t0 = (back ? chunks - 1 - i : i) * kChunk;
+        const int count = (int)(x.T - t0 < kChunk ? x.T - t0 : kChunk);
+        __syncthreads();
+        if (wave == 0) chunk_decay<D>(sh.decay, x, n, h, t0, count, lane);
+        stage<D, W>(sh.a, p.a, n, h, t0, count, p.da);
+        stage<D, W>(sh.b, p.b, n, h, t0, count, p.da);
+        stage<D, W>(sh.c, p.c, n, h, t0, count, p.dc);
+        __syncthreads();
+
+        // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col;
+        // ab[q][s]: rows (steps) 16 s + 4 group + r, column 16 q + col
+        f32x4 y[4][2] = {}, ab[4][4] = {};
 #pragma unroll
-                for (int r = 0; r < DA; ++r) S[r] = sf[s] == 0.0f ? 0.0f : S[r] * sf[s];
-            if (active) {
-                if (p.y_f32) seq_row_out<float>(p.y, n, t, h)[col] = y;
-                else seq_row_out<D>(p.y, n, t, h)[col] = from_f32<D>(y);
+        for (int k = 0; k < K; ++k) {
+            if (k * 32 >= p.da) break;
+            Frag<LS> s[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                s[u] = split<LS>(__builtin_shufflevector(S[2 * k][u], S[2 * k + 1][u], 0, 1, 2, 3, 4, 5, 6, 7));
+            Frag<L> fb[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) fb[q] = sh.b.rows(q * 16, k * 32, lane);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) y[q][u] = mma(s[u], fa, y[q][u]);
+                // only one side of the diagonal is used: forward steps s <= q
+#pragma unroll
+                for (int s2 = 0; s2 < 4; ++s2)
+                    if (back ? s2 >= q : s2 <= q) ab[q][s2] = mma(fb[s2], fa, ab[q][s2]);
+            }
+        }
+
+        // weights
+        Frag<L> fc[2][2];  // columns c0 + 16 u + l % 16 of 32 steps each
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
+        const float* from = back ? sh.decay.exit : sh.decay.entry;
+        const float* mine = back ? sh.decay.tail : sh.decay.head;
+        const float* theirs = back ? sh.decay.head : sh.decay.tail;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int step = q * 16 + col;
+            const float in = from[step];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) y[q][u] = in == 0.0f ? f32x4{} : y[q][u] * in;
+            float lead = mine[step] * p.p_scale;
+            // tiles from the nearest on, the decay of those between gathered on the way
+#pragma unroll
+            for (int d = 1; d < 4; ++d) {
+                const int s = back ? q + d : q - d;
+                if (s < 0 || s > 3) continue;
+                const f32x4 f = *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]);
+#pragma unroll
+                for (int s2 = 0; s2 < 4; ++s2)
+                    if (s2 == s) ab[q][s2] *= f * lead;
+                lead *= sh.decay.whole[s];
+            }
+            const double pi = sh.decay.p[step];
+            const int mi = sh.decay.m[step];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = q * 16 + group * 4 + r;
+                const double d = back ? sh.decay.p[j] - pi : pi - sh.decay.p[j];
+                const bool in_order = back ? j >= step : j <= step;
+                const float w = in_order && sh.decay.m[j] == mi ? exp2f((float)d) * p.p_scale : 0.0f;
+                ab[q][q][r] = w == 0.0f ? 0.0f : ab[q][q][r] * w;
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (back ? 2 * b + 1 < q : 2 * b > q) continue;
+                const Frag<LS> fp =
+                    split<LS>(__builtin_shufflevector(ab[q][2 * b], ab[q][2 * b + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) y[q][u] = mma(fc[b][u], fp, y[q][u]);
+            }
+        }
+
+        // y out
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int step = q * 16 + col;
+            float dot = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int c = c0 + u * 16 + group * 4;
+                const f32x4 v = y[q][u] * p.y_scale;
+                if (step < count) {
+                    if (p.dot) {
+                        const D* d = seq_row<D>(p.d, n, t0 + step, h);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (c + r < p.dc) dot = fmaf(v[r], to_f32(d[c + r]), dot);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (c + r < p.dc) {
+                            if (p.y_f32) seq_row_out<float>(p.y, n, t0 + step, h)[c + r] = v[r];
+                            else seq_row_out<D>(p.y, n, t0 + step, h)[c + r] = from_f32<D>(v[r]);
+                        }
+                }
             }
             if (p.dot) {
-                float v = active ? y * to_f32(seq_row<D>(p.d, n, t, h)[col]) : 0.0f;
-                for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-                if (col % kWave == 0) part[col / kWave] = v;
-                __syncthreads();
-                if (col == 0) {
-                    float sum = part[0];
-                    for (int w = 1; w < (int)blockDim.x / kWave; ++w) sum += part[w];
-                    p.dot[head * x.T + t] = sum;
-                }
-                __syncthreads();
+                dot += __shfl_xor(dot, 16);
+                dot += __shfl_xor(dot, 32);
+                if (group == 0) sh.dot[wave][step] = dot;
+            }
+        }
+
+        // the state after the chunk
+        const float* to = back ? sh.decay.entry : sh.decay.exit;
+        const float total = sh.decay.total;
+        Frag<LW> fw[2][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(&to[b * 32 + group * 4]);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(&to[b * 32 + 16 + group * 4]);
+            const f32x8 w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * p.u_scale;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                f32x8 v = __builtin_convertvector(fc[b][u].x[0], f32x8);
+#pragma unroll
+                for (int l = 1; l < L; ++l) v += __builtin_convertvector(fc[b][u].x[l], f32x8);
+                fw[b][u] = split<LW>(v * w);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2 * K; ++k) {
+            if (k * 16 >= p.da) break;
+            const Frag<L> fb[2] = {sh.b.columns(0, k * 16, lane), sh.b.columns(32, k * 16, lane)};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                // a cut drops the state, whatever it holds
+                f32x4 v = total == 0.0f ? f32x4{} : S[k][u] * total;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) v = mma(fb[b], fw[b][u], v);
+                S[k][u] = v;
+            }
+        }
+        if (p.dot) {
+            __syncthreads();
+            if (wave == 0 && lane < count) {
+                float sum = 0.0f;
+                for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += sh.dot[w][lane];
+                p.dot[head * x.T + t0 + lane] = sum;
             }
         }
     }
+
     float v = 0.0f;
 #pragma unroll
-    for (int r = 0; r < DA; ++r) {
-        if (!active || r >= p.da) continue;
-        if (p.last) p.last[at + state_at(p, r, col)] = S[r];
-        if (p.cross && p.meet) v = fmaf(S[r], p.meet[at + state_at(p, r, col)], v);
-    }
+    for (int k = 0; k < 2 * K; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
+                if (row >= p.da || c >= p.dc) continue;
+                if (p.last) p.last[at + state_at(p, row, c)] = S[k][u][r];
+                if (p.cross && p.meet) v = fmaf(S[k][u][r], p.meet[at + state_at(p, row, c)], v);
+            }
     if (p.cross) {
         for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+        if (lane == 0) sh.cross[wave] = v;
         __syncthreads();
-        if (col % kWave == 0) part[col / kWave] = v;
-        __syncthreads();
-        if (col == 0) {
-            float sum = part[0];
-            for (int w = 1; w < (int)blockDim.x / kWave; ++w) sum += part[w];
+        if (threadIdx.x == 0) {
+            float sum = 0.0f;
+            for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += sh.cross[w];
             p.cross[head] = sum;
         }
     }
@@ -334,13 +671,30 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
     return p;
 }
 
+// Rows that 16-byte reads may take.
 template <class D>
-lrs_status launch_passes(const char* nm, const RecurrenceArgs& x, int da, int dc, hipStream_t stream)
+void set_vec(SeqView& v, int dim)
+{
+    constexpr int64_t unit = 16 / sizeof(D);
+    v.vec = aligned(v.p, 16) && v.env % unit == 0 && v.step % unit == 0 && v.head % unit == 0;
+    (void)dim;
+}
+
+template <class D, bool kPrecise>
+lrs_status launch_passes(const char* nm, RecurrenceArgs x, hipStream_t stream)
 {
     const uint64_t blocks = (uint64_t)x.N * x.H * x.passes;
-    const int threads = (dc + kWave - 1) / kWave * kWave;
-    return da <= 64 ? launch_seq(nm, recurrence_steps<D, 64>, blocks, threads, stream, x)
-                    : launch_seq(nm, recurrence_steps<D, 128>, blocks, threads, stream, x);
+    int widest = 1, waves = 1;
+    for (int i = 0; i < x.passes; ++i) {
+        PassArgs& p = x.pass[i];
+        set_vec<D>(p.a, p.da);
+        set_vec<D>(p.b, p.da);
+        set_vec<D>(p.c, p.dc);
+        widest = std::max(widest, std::max(p.da, p.dc));
+        waves = std::max(waves, (p.dc + 31) / 32);
+    }
+    return widest <= 64 ? launch_seq(nm, recurrence_pass<D, 64, kPrecise>, blocks, waves * kWave, stream, x)
+                        : launch_seq(nm, recurrence_pass<D, 128, kPrecise>, blocks, waves * kWave, stream, x);
 }
 
 template <class D>
@@ -379,10 +733,11 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     p.init = initial;
     p.last = final_state;
     p.y_scale = scale;
+    p.p_scale = 1.0f;
     p.u_scale = 1.0f;
     p.da = (int32_t)dk;
     p.dc = (int32_t)dv;
-    return launch_passes<D>(nm, x, (int)dk, (int)dv, stream);
+    return launch_passes<D, false>(nm, x, stream);
 }
 
 template <class D>
@@ -420,7 +775,7 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     float* const part_q = reinterpret_cast<float*>(base + plan.dq);
     float* const part_k = reinterpret_cast<float*>(base + plan.dk);
     const auto partial = [&](const float* p) {
-        return SeqView{p, T * H * dk, H * dk, dk, 1};
+        return SeqView{p, T * H * dk, H * dk, dk, 1, 0};
     };
     RecurrenceArgs x{};
     x.g = w[4];
@@ -428,7 +783,7 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     x.N = N;
     x.T = T;
     x.H = (int32_t)H;
-    x.passes = 3;
+    x.passes = 2;
     PassArgs& pq = x.pass[0];  // dq
     pq.a = w[0];
     pq.b = w[3];
@@ -440,6 +795,7 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pq.dot = qdq;
     pq.cross = cross;
     pq.y_scale = scale;
+    pq.p_scale = 1.0f;
     pq.u_scale = 1.0f;
     pq.da = (int32_t)dv;
     pq.dc = (int32_t)dk;
@@ -454,13 +810,17 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pk.init = grad_final;
     pk.dot = kdk;
     pk.y_scale = 1.0f;
+    pk.p_scale = scale;
     pk.u_scale = scale;
     pk.da = (int32_t)dv;
     pk.dc = (int32_t)dk;
     pk.reverse = 1;
     pk.transposed = 1;
     pk.y_f32 = group > 1;
-    PassArgs& pv = x.pass[2];  // dv
+    RecurrenceArgs z = x;
+    z.passes = 1;
+    PassArgs& pv = z.pass[0];  // dv
+    pv = PassArgs{};
     pv.a = w[2];
     pv.b = w[1];
     pv.c = w[0];
@@ -468,12 +828,13 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pv.init = grad_final;
     pv.last = grad_initial;
     pv.y_scale = 1.0f;
+    pv.p_scale = scale;
     pv.u_scale = scale;
     pv.da = (int32_t)dk;
     pv.dc = (int32_t)dv;
     pv.reverse = 1;
-    const int widest = (int)(dk > dv ? dk : dv);
-    LRS_TRY(launch_passes<D>(nm, x, widest, widest, stream));
+    LRS_TRY((launch_passes<D, true>(nm, x, stream)));
+    LRS_TRY((launch_passes<D, false>(nm, z, stream)));
     DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, (int32_t)H};
     LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H), 64, stream, dg));
     if (group > 1) {

@@ -9,11 +9,13 @@
 namespace lrs {
 
 // An array of [env, step, head] rows of consecutive elements.  div: value
-// heads per stored head (head h of the call reads head h / div).
+// heads per stored head (head h of the call reads head h / div).  vec: rows
+// start on 16 bytes.
 struct SeqView {
     const void* p;
     int64_t env, step, head;
     int32_t div;
+    int32_t vec;
 };
 
 template <class D>
@@ -73,7 +75,7 @@ lrs_status check_seq_arrays(const char* nm, int64_t N, int64_t T, const SeqArg (
         const SeqArg& a = args[i];
         if (a.p == nullptr) {
             if (a.required) return fail(LRS_ERR_INVALID_ARG, "%s: %s is required", nm, a.what);
-            views[i] = SeqView{nullptr, 0, 0, 0, 1};
+            views[i] = SeqView{nullptr, 0, 0, 0, 1, 0};
             continue;
         }
         if ((uintptr_t)a.p % a.elem_bytes != 0)
@@ -96,7 +98,7 @@ lrs_status check_seq_arrays(const char* nm, int64_t N, int64_t T, const SeqArg (
         if (a.out && !strides_disjoint(size, st, 3, a.dim))
             return fail(LRS_ERR_INVALID_ARG, "%s: the strides of %s address an element twice", nm,
                         a.what);
-        views[i] = SeqView{a.p, st[0], st[1], st[2], 1};
+        views[i] = SeqView{a.p, st[0], st[1], st[2], 1, 0};
         (a.out ? outs[no++] : ins[ni++]) = Span{a.p, (uint64_t)extent * (uint64_t)a.elem_bytes};
     }
     for (int i = 0; i < nmore; ++i) (i < nmore_out ? outs[no++] : ins[ni++]) = more[i];
