@@ -33,11 +33,13 @@ namespace lrs {
 
 constexpr int kMaxDim = 128;  // largest key and value dimension
 
-// One pass over the sequence.  init: the state before the first step in scan
-// order; last: where the state after the last one goes; both [N, H, key_dim,
-// value_dim] and nullable.  y_scale multiplies y, p_scale the products a . b,
-// u_scale what enters the state.  dot (nullable): receives y_i . d_i per [N, H, T]; cross (nullable):
-// <final state, meet> per [N, H].
+// One pass over the sequence, in segments of seg_len steps that blocks work on
+// side by side.  init: each segment's state before its first step in scan order,
+// [N, H, segments, key_dim, value_dim] (nullable for one segment); last: where
+// the state after the last segment goes, [N, H, key_dim, value_dim], nullable.
+// y_scale multiplies y, p_scale the products a . b, u_scale what enters the
+// state.  dot (nullable): receives y_i . d_i per [N, H, T]; cross (nullable):
+// <state after the segment, meet> per [N, H, segments], meet like init.
 struct PassArgs {
     SeqView a, b, c, d, y;
     const float* init;
@@ -50,11 +52,24 @@ struct PassArgs {
     uint8_t reverse, transposed, y_f32;
 };
 
+// Where the segments of one direction leave their own states (from zero), for
+// the next segment in scan order, and their decays.
+struct CarryArgs {
+    SeqView b, c;
+    float* states;  // [N, H, segments, key_dim, value_dim]
+    float* totals;  // [N, H, segments]
+    const float* init;  // the state before the first segment, nullable
+    float u_scale;
+    int32_t da, dc;
+    uint8_t reverse;
+};
+
 struct RecurrenceArgs {
     SeqView g, reset;
-    int64_t N, T;
-    int32_t H, passes;
-    PassArgs pass[3];
+    int64_t N, T, seg_len;
+    int32_t H, passes, segments;
+    PassArgs pass[2];
+    CarryArgs carry[2];
 };
 
 // Row r (of a's dim) and column c (of y's dim) of a state in memory.
@@ -267,6 +282,45 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& s, const RecurrenceArgs&
     if (lane == 0) s.total = w[0] * w[1] * w[2] * w[3];
 }
 
+// S = total S + b^T (w c) over a chunk of 64 steps; w: the weight of each step,
+// fc: the wave's columns of c.
+template <class D, int W>
+__device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<W, kLimbs<D>>& tb,
+                                          const Frag<kLimbs<D>> (&fc)[2][2], const float* w, float total,
+                                          float scale, int da, int lane)
+{
+    constexpr int L = kLimbs<D>;
+    constexpr int LW = 3;  // limbs of the weighted c: states are fp32, their sums keep 24 bits
+    const int group = lane >> 4;
+    Frag<LW> fw[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(&w[b * 32 + group * 4]);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(&w[b * 32 + 16 + group * 4]);
+        const f32x8 v8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * scale;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            f32x8 v = __builtin_convertvector(fc[b][u].x[0], f32x8);
+#pragma unroll
+            for (int l = 1; l < L; ++l) v += __builtin_convertvector(fc[b][u].x[l], f32x8);
+            fw[b][u] = split<LW>(v * v8);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < W / 16; ++k) {
+        if (k * 16 >= da) break;
+        const Frag<L> fb[2] = {tb.columns(0, k * 16, lane), tb.columns(32, k * 16, lane)};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            // a cut drops the state, whatever it holds
+            f32x4 v = total == 0.0f ? f32x4{} : S[k][u] * total;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) v = mma(fb[b], fw[b][u], v);
+            S[k][u] = v;
+        }
+    }
+}
+
 // A pass by matrix instructions, 64 steps at a time.  A wave holds 32 columns
 // of the state, all its rows, in accumulators; the block's waves share the
 // steps in LDS.  Per chunk, with X, Z the weights from the chunk's start and to
@@ -289,20 +343,22 @@ __global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
 {
     constexpr int L = kLimbs<D>;
     constexpr int LS = L > 1 ? L : (kPrecise ? 2 : 1);  // limbs of a b^T and of the state
-    constexpr int LW = 3;                               // limbs of what enters the state
     constexpr int K = W / 32;
     __shared__ PassShared<D, W> sh;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int group = lane >> 4, col = lane & 15;
-    const int pass = blockIdx.x % x.passes;
-    const int64_t head = blockIdx.x / x.passes;
-    const PassArgs& p = x.pass[pass];
+    const PassArgs& p = x.pass[blockIdx.x % x.passes];
+    const uint32_t block = blockIdx.x / x.passes;
+    const int64_t head = block / x.segments;
+    const int seg = (int)(block % x.segments);
     const int64_t n = head / x.H;
     const int h = (int)(head % x.H);
     const int c0 = wave * 32;
-    const int64_t at = head * p.da * p.dc;
+    const int64_t at = (int64_t)block * p.da * p.dc;
     const bool back = p.reverse != 0;
+    const int64_t first = seg * x.seg_len;
+    const int64_t steps = x.T - first < x.seg_len ? x.T - first : x.seg_len;
 
     // S[2 k + s][u][r]: row 32 k + 16 s + 4 group + r, column c0 + 16 u + col
     f32x4 S[2 * K][2];
@@ -316,10 +372,11 @@ __global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
                 S[k][u][r] = p.init && row < p.da && c < p.dc ? p.init[at + state_at(p, row, c)] : 0.0f;
             }
 
-    const int64_t chunks = (x.T + kChunk - 1) / kChunk;
+    const int64_t chunks = (steps + kChunk - 1) / kChunk;
     for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t t0 = (back ? chunks - 1 - i : i) * kChunk;
-        const int count = (int)(x.T - t0 < kChunk ? x.T - t0 : kChunk);
+        const int64_t done = (back ? chunks - 1 - i : i) * kChunk;
+        const int64_t t0 = first + done;
+        const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
         __syncthreads();
         if (wave == 0) chunk_decay<D>(sh.decay, x, n, h, t0, count, lane);
         stage<D, W>(sh.a, p.a, n, h, t0, count, p.da);
@@ -431,35 +488,8 @@ __global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
         }
 
         // the state after the chunk
-        const float* to = back ? sh.decay.entry : sh.decay.exit;
-        const float total = sh.decay.total;
-        Frag<LW> fw[2][2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(&to[b * 32 + group * 4]);
-            const f32x4 hi = *reinterpret_cast<const f32x4*>(&to[b * 32 + 16 + group * 4]);
-            const f32x8 w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * p.u_scale;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                f32x8 v = __builtin_convertvector(fc[b][u].x[0], f32x8);
-#pragma unroll
-                for (int l = 1; l < L; ++l) v += __builtin_convertvector(fc[b][u].x[l], f32x8);
-                fw[b][u] = split<LW>(v * w);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 2 * K; ++k) {
-            if (k * 16 >= p.da) break;
-            const Frag<L> fb[2] = {sh.b.columns(0, k * 16, lane), sh.b.columns(32, k * 16, lane)};
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                // a cut drops the state, whatever it holds
-                f32x4 v = total == 0.0f ? f32x4{} : S[k][u] * total;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) v = mma(fb[b], fw[b][u], v);
-                S[k][u] = v;
-            }
-        }
+        add_chunk<D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale, p.da,
+                        lane);
         if (p.dot) {
             __syncthreads();
             if (wave == 0 && lane < count) {
@@ -479,7 +509,8 @@ __global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
             for (int r = 0; r < 4; ++r) {
                 const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
                 if (row >= p.da || c >= p.dc) continue;
-                if (p.last) p.last[at + state_at(p, row, c)] = S[k][u][r];
+                if (p.last && seg == (back ? 0 : x.segments - 1))
+                    p.last[head * p.da * p.dc + state_at(p, row, c)] = S[k][u][r];
                 if (p.cross && p.meet) v = fmaf(S[k][u][r], p.meet[at + state_at(p, row, c)], v);
             }
     if (p.cross) {
@@ -489,32 +520,127 @@ __global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
         if (threadIdx.x == 0) {
             float sum = 0.0f;
             for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += sh.cross[w];
-            p.cross[head] = sum;
+            p.cross[block] = sum;
         }
     }
 }
 
-// dg of one head by one wave, 64 steps at a time from the end: a suffix sum of
-// q.dq - k.dk in 64 bits (its terms cancel), started again at each cut, where
-// nothing is carried over and dg is 0.
+// The state that one segment alone leaves (from zero), and its decay, by the
+// same products; the last segment in scan order leaves none that is used.
+template <class D, int W>
+__global__ __launch_bounds__(256) void segment_states(const RecurrenceArgs x)
+{
+    __shared__ struct {
+        StepTile<W, kLimbs<D>> b, c;
+        ChunkDecay decay;
+    } sh;
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int group = lane >> 4, col = lane & 15;
+    const CarryArgs& p = x.carry[blockIdx.x % x.passes];
+    const uint32_t block = blockIdx.x / x.passes;
+    const int64_t head = block / (x.segments - 1);
+    const bool back = p.reverse != 0;
+    const int seg = (int)(block % (x.segments - 1)) + (back ? 1 : 0);
+    const int next = back ? seg - 1 : seg + 1;
+    const int64_t n = head / x.H;
+    const int h = (int)(head % x.H);
+    const int c0 = wave * 32;
+    const int64_t first = seg * x.seg_len;
+    const int64_t steps = x.T - first < x.seg_len ? x.T - first : x.seg_len;
+    f32x4 S[W / 16][2] = {};
+    float total = 1.0f;
+    const int64_t chunks = (steps + kChunk - 1) / kChunk;
+    for (int64_t i = 0; i < chunks; ++i) {
+        const int64_t done = (back ? chunks - 1 - i : i) * kChunk;
+        const int64_t t0 = first + done;
+        const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
+        __syncthreads();
+        if (wave == 0) chunk_decay<D>(sh.decay, x, n, h, t0, count, lane);
+        stage<D, W>(sh.b, p.b, n, h, t0, count, p.da);
+        stage<D, W>(sh.c, p.c, n, h, t0, count, p.dc);
+        __syncthreads();
+        Frag<kLimbs<D>> fc[2][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
+        add_chunk<D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale, p.da,
+                        lane);
+        total *= sh.decay.total;
+    }
+    float* const to = p.states + (head * x.segments + next) * (int64_t)p.da * p.dc;
+#pragma unroll
+    for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
+                if (row < p.da && c < p.dc) to[(int64_t)row * p.dc + c] = S[k][u][r];
+            }
+    if (threadIdx.x == 0) p.totals[head * x.segments + seg] = total;
+}
+
+// Turns the segments' own states into the states before each of them, in scan
+// order: in[s] = own[s - 1] + total[s - 1] in[s - 1].  A thread per element;
+// the loads of kAhead segments are in flight together.
+constexpr int kAhead = 8;
+
+static __global__ __launch_bounds__(256) void join_segments(const RecurrenceArgs x)
+{
+    const CarryArgs& p = x.carry[blockIdx.x % x.passes];
+    const int64_t size = (int64_t)p.da * p.dc;
+    const int64_t e = (int64_t)(blockIdx.x / x.passes) * 256 + threadIdx.x;
+    const int64_t head = e / size, i = e % size;
+    if (head >= x.N * x.H) return;
+    float* const s = p.states + head * x.segments * size + i;
+    const float* const f = p.totals + head * x.segments;
+    const bool back = p.reverse != 0;
+    const auto place = [&](int k) { return back ? x.segments - 1 - k : k; };
+    float v = p.init ? p.init[head * size + i] : 0.0f;
+    s[place(0) * size] = v;
+    for (int k = 1; k < x.segments; k += kAhead) {
+        float own[kAhead], total[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+            if (k + a < x.segments) {
+                own[a] = s[place(k + a) * size];
+                total[a] = f[place(k + a - 1)];
+            }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+            if (k + a < x.segments) {
+                v = total[a] == 0.0f ? own[a] : fmaf(total[a], v, own[a]);
+                s[place(k + a) * size] = v;
+            }
+    }
+}
+
+// dg of one segment of a head by one wave, 64 steps at a time from its end: a
+// suffix sum of q.dq - k.dk in 64 bits (its terms cancel), from <state after
+// the segment, its gradient>, started again at each cut, where nothing is
+// carried over and dg is 0.
 struct DecayGradArgs {
     SeqView g, reset, dg;
     const float *qdq, *kdk, *cross;
-    int64_t N, T;
-    int32_t H;
+    int64_t N, T, seg_len;
+    int32_t H, segments;
 };
 
 template <class D>
 __global__ __launch_bounds__(64) void decay_grad(const DecayGradArgs x)
 {
-    const int64_t head = blockIdx.x, n = head / x.H;
+    const int64_t head = blockIdx.x / x.segments, n = head / x.H;
     const int h = (int)(head % x.H), lane = threadIdx.x;
-    double carry = x.cross[head];
-    for (int64_t end = x.T; end > 0; end -= kWave) {
+    const int64_t first = (int64_t)(blockIdx.x % x.segments) * x.seg_len;
+    const int64_t past = x.T - first < x.seg_len ? x.T : first + x.seg_len;
+    double carry = x.cross[blockIdx.x];
+    for (int64_t end = past; end > first; end -= kWave) {
         const int64_t t = end - 1 - lane;
         double v = 0.0;
         bool cut = false;
-        if (t >= 0) {
+        if (t >= first) {
             v = (double)x.qdq[head * x.T + t] - (double)x.kdk[head * x.T + t];
             const float g = to_f32(*seq_row<D>(x.g, n, t, h));
             cut = __expf(g) == 0.0f || (x.reset.p && *seq_row<uint8_t>(x.reset, n, t, 0) != 0);
@@ -530,7 +656,7 @@ __global__ __launch_bounds__(64) void decay_grad(const DecayGradArgs x)
             }
         }
         if (!stop) v += carry;
-        if (t >= 0) *seq_row_out<D>(x.dg, n, t, h) = from_f32<D>(cut ? 0.0f : (float)v);
+        if (t >= first) *seq_row_out<D>(x.dg, n, t, h) = from_f32<D>(cut ? 0.0f : (float)v);
         carry = __shfl(v, kWave - 1);
         if (__shfl((int)cut, kWave - 1)) carry = 0.0;
     }
@@ -616,7 +742,7 @@ __global__ __launch_bounds__(256) void recurrence_one_step(const StepArgs x)
 
 // ------------------------------------------------------------------ entries
 
-constexpr int64_t kMaxHeads = int64_t(1) << 23;  // num_envs * heads of a call
+constexpr int64_t kMaxHeads = int64_t(1) << 22;  // num_envs * heads of a call
 
 inline lrs_status check_recurrence(const char* nm, int64_t N, int64_t T, int64_t H, int64_t KV,
                                    int64_t dk, int64_t dv, float scale)
@@ -642,30 +768,49 @@ inline lrs_status check_state(const char* nm, const void* p, const char* what)
 
 inline size_t round_up(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Workspace of a call.  Backward: q.dq and k.dk [N, H, T], <S_T, dS_T> [N, H]
+// How a call is cut up, and its workspace.  A pass has a block per head and
+// segment: one segment where the heads alone fill the chip, else as many as
+// give kFillBlocks blocks, of at least kMinSegment steps (a segment costs one
+// more reading of two of its arrays and a state written and read twice).
+// Workspace: the states before each segment and the segments' decays, per
+// direction; backward also q.dq and k.dk [N, H, T], <S, dS> [N, H, segments]
 // and, for shared query and key heads, each value head's dq and dk.
+constexpr int64_t kFillBlocks = 512;
+constexpr int64_t kMinSegment = 256;
+
 struct RecurrencePlan {
-    size_t qdq, kdk, cross, dq, dk, bytes;
+    int64_t seg_len, segments;
+    size_t states[2], totals[2], qdq, kdk, cross, dq, dk, bytes;
 };
 
 inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t KV, int64_t dk,
                                       int64_t dv, bool backward)
 {
-    (void)dv;
     RecurrencePlan p{};
-    if (!backward) return p;
+    const int64_t heads = N * H * (backward ? 2 : 1);
+    int64_t parts = std::min((kFillBlocks + heads - 1) / heads, (T + kMinSegment - 1) / kMinSegment);
+    if (heads >= kFillBlocks) parts = 1;
+    p.seg_len = ((T + parts - 1) / parts + kChunk - 1) / kChunk * kChunk;
+    p.segments = (T + p.seg_len - 1) / p.seg_len;
     size_t at = 0;
-    const auto take = [&](size_t floats) {
+    const auto take = [&](int64_t floats) {
         const size_t here = at;
-        at += round_up(4 * floats);
+        at += round_up(4 * (size_t)floats);
         return here;
     };
-    p.qdq = take((size_t)(N * T * H));
-    p.kdk = take((size_t)(N * T * H));
-    p.cross = take((size_t)(N * H));
-    if (H != KV) {
-        p.dq = take((size_t)(N * T * H * dk));
-        p.dk = take((size_t)(N * T * H * dk));
+    if (p.segments > 1)
+        for (int i = 0; i < (backward ? 2 : 1); ++i) {
+            p.states[i] = take(N * H * p.segments * dk * dv);
+            p.totals[i] = take(N * H * p.segments);
+        }
+    if (backward) {
+        p.qdq = take(N * T * H);
+        p.kdk = take(N * T * H);
+        p.cross = take(N * H * p.segments);
+        if (H != KV) {
+            p.dq = take(N * T * H * dk);
+            p.dk = take(N * T * H * dk);
+        }
     }
     p.bytes = at;
     return p;
@@ -673,28 +818,44 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
 
 // Rows that 16-byte reads may take.
 template <class D>
-void set_vec(SeqView& v, int dim)
+void set_vec(SeqView& v)
 {
     constexpr int64_t unit = 16 / sizeof(D);
     v.vec = aligned(v.p, 16) && v.env % unit == 0 && v.step % unit == 0 && v.head % unit == 0;
-    (void)dim;
 }
 
 template <class D, bool kPrecise>
 lrs_status launch_passes(const char* nm, RecurrenceArgs x, hipStream_t stream)
 {
-    const uint64_t blocks = (uint64_t)x.N * x.H * x.passes;
+    const uint64_t blocks = (uint64_t)x.N * x.H * x.segments * x.passes;
     int widest = 1, waves = 1;
     for (int i = 0; i < x.passes; ++i) {
         PassArgs& p = x.pass[i];
-        set_vec<D>(p.a, p.da);
-        set_vec<D>(p.b, p.da);
-        set_vec<D>(p.c, p.dc);
+        set_vec<D>(p.a);
+        set_vec<D>(p.b);
+        set_vec<D>(p.c);
         widest = std::max(widest, std::max(p.da, p.dc));
         waves = std::max(waves, (p.dc + 31) / 32);
     }
     return widest <= 64 ? launch_seq(nm, recurrence_pass<D, 64, kPrecise>, blocks, waves * kWave, stream, x)
                         : launch_seq(nm, recurrence_pass<D, 128, kPrecise>, blocks, waves * kWave, stream, x);
+}
+
+// The states before every segment, in x.carry's directions.
+template <class D>
+lrs_status launch_carries(const char* nm, RecurrenceArgs x, hipStream_t stream)
+{
+    if (x.segments == 1) return LRS_OK;
+    for (int i = 0; i < x.passes; ++i) {
+        set_vec<D>(x.carry[i].b);
+        set_vec<D>(x.carry[i].c);
+    }
+    const int da = x.carry[0].da, dc = x.carry[0].dc, waves = (dc + 31) / 32;
+    const uint64_t heads = (uint64_t)x.N * x.H, blocks = heads * (x.segments - 1) * x.passes;
+    LRS_TRY(std::max(da, dc) <= 64
+                ? launch_seq(nm, segment_states<D, 64>, blocks, waves * kWave, stream, x)
+                : launch_seq(nm, segment_states<D, 128>, blocks, waves * kWave, stream, x));
+    return launch_seq(nm, join_segments, (heads * da * dc + 255) / 256 * x.passes, 256, stream, x);
 }
 
 template <class D>
@@ -725,6 +886,15 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     x.T = T;
     x.H = (int32_t)H;
     x.passes = 1;
+    x.seg_len = plan.seg_len;
+    x.segments = (int32_t)plan.segments;
+    char* base = static_cast<char*>(ws);
+    if (plan.segments > 1) {
+        CarryArgs& c = x.carry[0];
+        c = CarryArgs{w[1], w[2], reinterpret_cast<float*>(base + plan.states[0]),
+                      reinterpret_cast<float*>(base + plan.totals[0]), initial, 1.0f, (int32_t)dk, (int32_t)dv, 0};
+        initial = c.states;
+    }
     PassArgs& p = x.pass[0];
     p.a = w[0];
     p.b = w[1];
@@ -737,6 +907,7 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     p.u_scale = 1.0f;
     p.da = (int32_t)dk;
     p.dc = (int32_t)dv;
+    LRS_TRY(launch_carries<D>(nm, x, stream));
     return launch_passes<D, false>(nm, x, stream);
 }
 
@@ -784,6 +955,18 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     x.T = T;
     x.H = (int32_t)H;
     x.passes = 2;
+    x.seg_len = plan.seg_len;
+    x.segments = (int32_t)plan.segments;
+    if (plan.segments > 1) {
+        x.carry[0] = CarryArgs{w[2], w[3], reinterpret_cast<float*>(base + plan.states[0]),
+                               reinterpret_cast<float*>(base + plan.totals[0]), initial, 1.0f, (int32_t)dk,
+                               (int32_t)dv, 0};
+        x.carry[1] = CarryArgs{w[1], w[0], reinterpret_cast<float*>(base + plan.states[1]),
+                               reinterpret_cast<float*>(base + plan.totals[1]), grad_final, scale, (int32_t)dk,
+                               (int32_t)dv, 1};
+        initial = x.carry[0].states;
+        grad_final = x.carry[1].states;
+    }
     PassArgs& pq = x.pass[0];  // dq
     pq.a = w[0];
     pq.b = w[3];
@@ -833,10 +1016,12 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pv.da = (int32_t)dk;
     pv.dc = (int32_t)dv;
     pv.reverse = 1;
+    LRS_TRY(launch_carries<D>(nm, x, stream));
     LRS_TRY((launch_passes<D, true>(nm, x, stream)));
     LRS_TRY((launch_passes<D, false>(nm, z, stream)));
-    DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, (int32_t)H};
-    LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H), 64, stream, dg));
+    DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, plan.seg_len, (int32_t)H,
+                     (int32_t)plan.segments};
+    LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H * plan.segments), 64, stream, dg));
     if (group > 1) {
         const int64_t blocks = (N * T * KV * dk + 255) / 256;
         for (int i = 0; i < 2; ++i) {
