@@ -49,7 +49,7 @@ struct PassArgs {
     float* cross;
     float y_scale, p_scale, u_scale;
     int32_t da, dc;  // dims of a and b, of c and y
-    uint8_t reverse, transposed, y_f32;
+    uint8_t transposed, y_f32;
 };
 
 // Where the segments of one direction leave their own states (from zero), for
@@ -67,8 +67,8 @@ struct CarryArgs {
 struct RecurrenceArgs {
     SeqView g, reset;
     int64_t N, T, seg_len;
-    int32_t H, passes, segments;
-    PassArgs pass[2];
+    int32_t H, carries, segments;
+    PassArgs pass[3];
     CarryArgs carry[2];
 };
 
@@ -201,6 +201,17 @@ __device__ __forceinline__ f32x8 load8(const D* row, int c, int dim, bool vec)
     return v;
 }
 
+// The same as one-limb elements, unconverted.
+__device__ __forceinline__ u32x4 load8_raw(const bf16_t* row, int c, int dim, bool vec)
+{
+    if (vec && c + 8 <= dim) return *reinterpret_cast<const u32x4*>(row + c);
+    u32x4 w = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (c + k < dim) w[k / 2] |= (uint32_t)row[c + k].bits << (16 * (k & 1));
+    return w;
+}
+
 // Steps t0 .. t0 + count - 1 of one head into a tile, zero beyond them.
 template <class D, int W>
 __device__ __forceinline__ void stage(StepTile<W, kLimbs<D>>& tile, const SeqView& view, int64_t n, int h,
@@ -210,11 +221,17 @@ __device__ __forceinline__ void stage(StepTile<W, kLimbs<D>>& tile, const SeqVie
     const int units = (dim + 31) / 32 * 4;  // what the products read
     for (int u = threadIdx.x; u < kChunk * units; u += blockDim.x) {
         const int row = u / units, c = (u % units) * 8;
-        f32x8 v = {};
-        if (row < count) v = load8(seq_row<D>(view, n, t0 + row, h), c, dim, view.vec != 0);
-        const Frag<L> f = split<L>(v);
+        if constexpr (L == 1) {
+            u32x4 v = {};
+            if (row < count) v = load8_raw(seq_row<D>(view, n, t0 + row, h), c, dim, view.vec != 0);
+            *reinterpret_cast<u32x4*>(&tile.e[0][tile.at(row, c)]) = v;
+        } else {
+            f32x8 v = {};
+            if (row < count) v = load8(seq_row<D>(view, n, t0 + row, h), c, dim, view.vec != 0);
+            const Frag<L> f = split<L>(v);
 #pragma unroll
-        for (int l = 0; l < L; ++l) *reinterpret_cast<bf16x8*>(&tile.e[l][tile.at(row, c)]) = f.x[l];
+            for (int l = 0; l < L; ++l) *reinterpret_cast<bf16x8*>(&tile.e[l][tile.at(row, c)]) = f.x[l];
+        }
     }
 }
 
@@ -338,25 +355,65 @@ struct PassShared {
     float cross[4];
 };
 
-template <class D, int W, bool kPrecise>
-__global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
+// Four elements of a row from column c on, out of `dim` (one access where the
+// row allows it).
+template <class D>
+__device__ __forceinline__ void store4(D* row, int c, int dim, bool vec, f32x4 v)
+{
+    if (vec) {
+        if (c >= dim) return;
+        if constexpr (sizeof(D) == 4)
+            *reinterpret_cast<f32x4*>(row + c) = v;
+        else
+            *reinterpret_cast<u32x2*>(row + c) = u32x2{pack2<D>(v[0], v[1]), pack2<D>(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (c + r < dim) row[c + r] = from_f32<D>(v[r]);
+    }
+}
+template <class D>
+__device__ __forceinline__ f32x4 load4(const D* row, int c, int dim, bool vec)
+{
+    f32x4 v = {};
+    if (vec) {
+        if (c >= dim) return v;
+        if constexpr (sizeof(D) == 4) {
+            v = *reinterpret_cast<const f32x4*>(row + c);
+        } else {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(row + c);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float lo, hi;
+                unpack2<D>(w[k], lo, hi);
+                v[2 * k] = lo;
+                v[2 * k + 1] = hi;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (c + r < dim) v[r] = to_f32(row[c + r]);
+    }
+    return v;
+}
+
+template <class D, int W, bool back, bool kPrecise>
+__device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs& p, uint32_t block,
+                                         PassShared<D, W>& sh)
 {
     constexpr int L = kLimbs<D>;
     constexpr int LS = L > 1 ? L : (kPrecise ? 2 : 1);  // limbs of a b^T and of the state
     constexpr int K = W / 32;
-    __shared__ PassShared<D, W> sh;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int group = lane >> 4, col = lane & 15;
-    const PassArgs& p = x.pass[blockIdx.x % x.passes];
-    const uint32_t block = blockIdx.x / x.passes;
     const int64_t head = block / x.segments;
     const int seg = (int)(block % x.segments);
     const int64_t n = head / x.H;
     const int h = (int)(head % x.H);
     const int c0 = wave * 32;
     const int64_t at = (int64_t)block * p.da * p.dc;
-    const bool back = p.reverse != 0;
     const int64_t first = seg * x.seg_len;
     const int64_t steps = x.T - first < x.seg_len ? x.T - first : x.seg_len;
 
@@ -384,117 +441,115 @@ __global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
         stage<D, W>(sh.c, p.c, n, h, t0, count, p.dc);
         __syncthreads();
 
-        // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col;
-        // ab[q][s]: rows (steps) 16 s + 4 group + r, column 16 q + col
-        f32x4 y[4][2] = {}, ab[4][4] = {};
+        if (c0 < p.dc) {
+            // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col;
+            // ab[q][s]: rows (steps) 16 s + 4 group + r, column 16 q + col
+            f32x4 y[4][2] = {}, ab[4][4] = {};
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (k * 32 >= p.da) break;
-            Frag<LS> s[2];
+            for (int k = 0; k < K; ++k) {
+                if (k * 32 >= p.da) break;
+                Frag<LS> s[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                s[u] = split<LS>(__builtin_shufflevector(S[2 * k][u], S[2 * k + 1][u], 0, 1, 2, 3, 4, 5, 6, 7));
-            Frag<L> fb[4];
+                for (int u = 0; u < 2; ++u)
+                    s[u] = split<LS>(__builtin_shufflevector(S[2 * k][u], S[2 * k + 1][u], 0, 1, 2, 3, 4, 5, 6, 7));
+                Frag<L> fb[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) fb[q] = sh.b.rows(q * 16, k * 32, lane);
+                for (int q = 0; q < 4; ++q) fb[q] = sh.b.rows(q * 16, k * 32, lane);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
+                for (int q = 0; q < 4; ++q) {
+                    const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) y[q][u] = mma(s[u], fa, y[q][u]);
-                // only one side of the diagonal is used: forward steps s <= q
+                    for (int u = 0; u < 2; ++u) y[q][u] = mma(s[u], fa, y[q][u]);
+                    // only one side of the diagonal is used: forward steps s <= q
 #pragma unroll
-                for (int s2 = 0; s2 < 4; ++s2)
-                    if (back ? s2 >= q : s2 <= q) ab[q][s2] = mma(fb[s2], fa, ab[q][s2]);
-            }
-        }
-
-        // weights
-        Frag<L> fc[2][2];  // columns c0 + 16 u + l % 16 of 32 steps each
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
-        const float* from = back ? sh.decay.exit : sh.decay.entry;
-        const float* mine = back ? sh.decay.tail : sh.decay.head;
-        const float* theirs = back ? sh.decay.head : sh.decay.tail;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int step = q * 16 + col;
-            const float in = from[step];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) y[q][u] = in == 0.0f ? f32x4{} : y[q][u] * in;
-            float lead = mine[step] * p.p_scale;
-            // tiles from the nearest on, the decay of those between gathered on the way
-#pragma unroll
-            for (int d = 1; d < 4; ++d) {
-                const int s = back ? q + d : q - d;
-                if (s < 0 || s > 3) continue;
-                const f32x4 f = *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]);
-#pragma unroll
-                for (int s2 = 0; s2 < 4; ++s2)
-                    if (s2 == s) ab[q][s2] *= f * lead;
-                lead *= sh.decay.whole[s];
-            }
-            const double pi = sh.decay.p[step];
-            const int mi = sh.decay.m[step];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = q * 16 + group * 4 + r;
-                const double d = back ? sh.decay.p[j] - pi : pi - sh.decay.p[j];
-                const bool in_order = back ? j >= step : j <= step;
-                const float w = in_order && sh.decay.m[j] == mi ? exp2f((float)d) * p.p_scale : 0.0f;
-                ab[q][q][r] = w == 0.0f ? 0.0f : ab[q][q][r] * w;
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (back ? 2 * b + 1 < q : 2 * b > q) continue;
-                const Frag<LS> fp =
-                    split<LS>(__builtin_shufflevector(ab[q][2 * b], ab[q][2 * b + 1], 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                for (int u = 0; u < 2; ++u) y[q][u] = mma(fc[b][u], fp, y[q][u]);
-            }
-        }
-
-        // y out
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int step = q * 16 + col;
-            float dot = 0.0f;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int c = c0 + u * 16 + group * 4;
-                const f32x4 v = y[q][u] * p.y_scale;
-                if (step < count) {
-                    if (p.dot) {
-                        const D* d = seq_row<D>(p.d, n, t0 + step, h);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (c + r < p.dc) dot = fmaf(v[r], to_f32(d[c + r]), dot);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (c + r < p.dc) {
-                            if (p.y_f32) seq_row_out<float>(p.y, n, t0 + step, h)[c + r] = v[r];
-                            else seq_row_out<D>(p.y, n, t0 + step, h)[c + r] = from_f32<D>(v[r]);
-                        }
+                    for (int s2 = 0; s2 < 4; ++s2)
+                        if (back ? s2 >= q : s2 <= q) ab[q][s2] = mma(fb[s2], fa, ab[q][s2]);
                 }
             }
-            if (p.dot) {
-                dot += __shfl_xor(dot, 16);
-                dot += __shfl_xor(dot, 32);
-                if (group == 0) sh.dot[wave][step] = dot;
-            }
-        }
 
-        // the state after the chunk
-        add_chunk<D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale, p.da,
-                        lane);
-        if (p.dot) {
+            // weights
+            Frag<L> fc[2][2];  // columns c0 + 16 u + l % 16 of 32 steps each
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
+            const float* from = back ? sh.decay.exit : sh.decay.entry;
+            const float* mine = back ? sh.decay.tail : sh.decay.head;
+            const float* theirs = back ? sh.decay.head : sh.decay.tail;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int step = q * 16 + col;
+                const float in = from[step];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) y[q][u] = in == 0.0f ? f32x4{} : y[q][u] * in;
+                float lead = mine[step] * p.p_scale;
+                // tiles from the nearest on, the decay of those between gathered on the way
+#pragma unroll
+                for (int d = 1; d < 4; ++d) {
+                    const int s = back ? q + d : q - d;
+                    if (s < 0 || s > 3) continue;
+                    const f32x4 f = *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]);
+#pragma unroll
+                    for (int s2 = 0; s2 < 4; ++s2)
+                        if (s2 == s) ab[q][s2] *= f * lead;
+                    lead *= sh.decay.whole[s];
+                }
+                const double pi = sh.decay.p[step];
+                const int mi = sh.decay.m[step];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = q * 16 + group * 4 + r;
+                    const double d = back ? sh.decay.p[j] - pi : pi - sh.decay.p[j];
+                    const bool in_order = back ? j >= step : j <= step;
+                    const float w = in_order && sh.decay.m[j] == mi ? exp2f((float)d) * p.p_scale : 0.0f;
+                    ab[q][q][r] = w == 0.0f ? 0.0f : ab[q][q][r] * w;
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (back ? 2 * b + 1 < q : 2 * b > q) continue;
+                    const Frag<LS> fp =
+                        split<LS>(__builtin_shufflevector(ab[q][2 * b], ab[q][2 * b + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) y[q][u] = mma(fc[b][u], fp, y[q][u]);
+                }
+            }
+
+            // y out
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int step = q * 16 + col;
+                float dot = 0.0f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int c = c0 + u * 16 + group * 4;
+                    const f32x4 v = y[q][u] * p.y_scale;
+                    if (step < count) {
+                        if (kPrecise) {
+                            const f32x4 d = load4<D>(seq_row<D>(p.d, n, t0 + step, h), c, p.dc, p.d.vec != 0) * v;
+                            dot += (d[0] + d[1]) + (d[2] + d[3]);
+                        }
+                        if (kPrecise && p.y_f32)
+                            store4<float>(seq_row_out<float>(p.y, n, t0 + step, h), c, p.dc, p.y.vec != 0, v);
+                        else
+                            store4<D>(seq_row_out<D>(p.y, n, t0 + step, h), c, p.dc, p.y.vec != 0, v);
+                    }
+                }
+                if (kPrecise) {
+                    dot += __shfl_xor(dot, 16);
+                    dot += __shfl_xor(dot, 32);
+                    if (group == 0) sh.dot[wave][step] = dot;
+                }
+            }
+
+            // the state after the chunk
+            add_chunk<D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale, p.da,
+                            lane);
+        }
+        if (kPrecise) {
             __syncthreads();
             if (wave == 0 && lane < count) {
                 float sum = 0.0f;
-                for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += sh.dot[w][lane];
+                for (int w = 0; w * 32 < p.dc; ++w) sum += sh.dot[w][lane];
                 p.dot[head * x.T + t0 + lane] = sum;
             }
         }
@@ -525,10 +580,29 @@ __global__ __launch_bounds__(256) void recurrence_pass(const RecurrenceArgs x)
     }
 }
 
+template <class D, int W>
+__global__ __launch_bounds__(2 * W, 2) void recurrence_forward(const RecurrenceArgs x)
+{
+    __shared__ PassShared<D, W> sh;
+    run_pass<D, W, false, false>(x, x.pass[0], blockIdx.x, sh);
+}
+
+// The three passes of the backward call: dq and dk with q.dq and k.dk to a
+// precision that their differences keep, and dv.
+template <class D, int W>
+__global__ __launch_bounds__(2 * W, 2) void recurrence_backward(const RecurrenceArgs x)
+{
+    __shared__ PassShared<D, W> sh;
+    const uint32_t block = blockIdx.x / 3, pass = blockIdx.x % 3;
+    if (pass == 0) run_pass<D, W, false, true>(x, x.pass[0], block, sh);
+    else if (pass == 1) run_pass<D, W, true, true>(x, x.pass[1], block, sh);
+    else run_pass<D, W, true, false>(x, x.pass[2], block, sh);
+}
+
 // The state that one segment alone leaves (from zero), and its decay, by the
 // same products; the last segment in scan order leaves none that is used.
 template <class D, int W>
-__global__ __launch_bounds__(256) void segment_states(const RecurrenceArgs x)
+__global__ __launch_bounds__(2 * W) void segment_states(const RecurrenceArgs x)
 {
     __shared__ struct {
         StepTile<W, kLimbs<D>> b, c;
@@ -537,8 +611,8 @@ __global__ __launch_bounds__(256) void segment_states(const RecurrenceArgs x)
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int group = lane >> 4, col = lane & 15;
-    const CarryArgs& p = x.carry[blockIdx.x % x.passes];
-    const uint32_t block = blockIdx.x / x.passes;
+    const CarryArgs& p = x.carry[blockIdx.x % x.carries];
+    const uint32_t block = blockIdx.x / x.carries;
     const int64_t head = block / (x.segments - 1);
     const bool back = p.reverse != 0;
     const int seg = (int)(block % (x.segments - 1)) + (back ? 1 : 0);
@@ -560,6 +634,7 @@ __global__ __launch_bounds__(256) void segment_states(const RecurrenceArgs x)
         stage<D, W>(sh.b, p.b, n, h, t0, count, p.da);
         stage<D, W>(sh.c, p.c, n, h, t0, count, p.dc);
         __syncthreads();
+        if (c0 >= p.dc) continue;
         Frag<kLimbs<D>> fc[2][2];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -579,6 +654,7 @@ __global__ __launch_bounds__(256) void segment_states(const RecurrenceArgs x)
                 const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
                 if (row < p.da && c < p.dc) to[(int64_t)row * p.dc + c] = S[k][u][r];
             }
+    // (wave 0 always has columns, and with them the whole decay)
     if (threadIdx.x == 0) p.totals[head * x.segments + seg] = total;
 }
 
@@ -587,11 +663,12 @@ __global__ __launch_bounds__(256) void segment_states(const RecurrenceArgs x)
 // the loads of kAhead segments are in flight together.
 constexpr int kAhead = 8;
 
-static __global__ __launch_bounds__(256) void join_segments(const RecurrenceArgs x)
+template <class D>
+__global__ __launch_bounds__(256) void join_segments(const RecurrenceArgs x)
 {
-    const CarryArgs& p = x.carry[blockIdx.x % x.passes];
+    const CarryArgs& p = x.carry[blockIdx.x % x.carries];
     const int64_t size = (int64_t)p.da * p.dc;
-    const int64_t e = (int64_t)(blockIdx.x / x.passes) * 256 + threadIdx.x;
+    const int64_t e = (int64_t)(blockIdx.x / x.carries) * 256 + threadIdx.x;
     const int64_t head = e / size, i = e % size;
     if (head >= x.N * x.H) return;
     float* const s = p.states + head * x.segments * size + i;
@@ -787,7 +864,7 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
                                       int64_t dv, bool backward)
 {
     RecurrencePlan p{};
-    const int64_t heads = N * H * (backward ? 2 : 1);
+    const int64_t heads = N * H * (backward ? 3 : 1);
     int64_t parts = std::min((kFillBlocks + heads - 1) / heads, (T + kMinSegment - 1) / kMinSegment);
     if (heads >= kFillBlocks) parts = 1;
     p.seg_len = ((T + parts - 1) / parts + kChunk - 1) / kChunk * kChunk;
@@ -816,29 +893,23 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
     return p;
 }
 
-// Rows that 16-byte reads may take.
-template <class D>
-void set_vec(SeqView& v)
+// Whether rows start where accesses of `unit` elements may.
+inline void set_vec(SeqView& v, int unit, int elem_bytes)
 {
-    constexpr int64_t unit = 16 / sizeof(D);
-    v.vec = aligned(v.p, 16) && v.env % unit == 0 && v.step % unit == 0 && v.head % unit == 0;
+    v.vec = aligned(v.p, (uintptr_t)(unit * elem_bytes)) && v.env % unit == 0 && v.step % unit == 0 &&
+            v.head % unit == 0;
 }
 
-template <class D, bool kPrecise>
-lrs_status launch_passes(const char* nm, RecurrenceArgs x, hipStream_t stream)
+template <class D>
+void set_vec(PassArgs& p)
 {
-    const uint64_t blocks = (uint64_t)x.N * x.H * x.segments * x.passes;
-    int widest = 1, waves = 1;
-    for (int i = 0; i < x.passes; ++i) {
-        PassArgs& p = x.pass[i];
-        set_vec<D>(p.a);
-        set_vec<D>(p.b);
-        set_vec<D>(p.c);
-        widest = std::max(widest, std::max(p.da, p.dc));
-        waves = std::max(waves, (p.dc + 31) / 32);
-    }
-    return widest <= 64 ? launch_seq(nm, recurrence_pass<D, 64, kPrecise>, blocks, waves * kWave, stream, x)
-                        : launch_seq(nm, recurrence_pass<D, 128, kPrecise>, blocks, waves * kWave, stream, x);
+    constexpr int s = sizeof(D), unit = 16 / s;
+    set_vec(p.a, unit, s);
+    set_vec(p.b, unit, s);
+    set_vec(p.c, unit, s);
+    set_vec(p.d, 4, s);
+    set_vec(p.y, 4, p.y_f32 ? 4 : s);
+    if (p.dc % 4 != 0) p.d.vec = p.y.vec = 0;
 }
 
 // The states before every segment, in x.carry's directions.
@@ -846,16 +917,15 @@ template <class D>
 lrs_status launch_carries(const char* nm, RecurrenceArgs x, hipStream_t stream)
 {
     if (x.segments == 1) return LRS_OK;
-    for (int i = 0; i < x.passes; ++i) {
-        set_vec<D>(x.carry[i].b);
-        set_vec<D>(x.carry[i].c);
+    for (int i = 0; i < x.carries; ++i) {
+        set_vec(x.carry[i].b, 16 / sizeof(D), sizeof(D));
+        set_vec(x.carry[i].c, 16 / sizeof(D), sizeof(D));
     }
-    const int da = x.carry[0].da, dc = x.carry[0].dc, waves = (dc + 31) / 32;
-    const uint64_t heads = (uint64_t)x.N * x.H, blocks = heads * (x.segments - 1) * x.passes;
-    LRS_TRY(std::max(da, dc) <= 64
-                ? launch_seq(nm, segment_states<D, 64>, blocks, waves * kWave, stream, x)
-                : launch_seq(nm, segment_states<D, 128>, blocks, waves * kWave, stream, x));
-    return launch_seq(nm, join_segments, (heads * da * dc + 255) / 256 * x.passes, 256, stream, x);
+    const int da = x.carry[0].da, dc = x.carry[0].dc;
+    const uint64_t heads = (uint64_t)x.N * x.H, blocks = heads * (x.segments - 1) * x.carries;
+    LRS_TRY(std::max(da, dc) <= 64 ? launch_seq(nm, segment_states<D, 64>, blocks, 128, stream, x)
+                                   : launch_seq(nm, segment_states<D, 128>, blocks, 256, stream, x));
+    return launch_seq(nm, join_segments<D>, (heads * da * dc + 255) / 256 * x.carries, 256, stream, x);
 }
 
 template <class D>
@@ -885,7 +955,7 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     x.N = N;
     x.T = T;
     x.H = (int32_t)H;
-    x.passes = 1;
+    x.carries = 1;
     x.seg_len = plan.seg_len;
     x.segments = (int32_t)plan.segments;
     char* base = static_cast<char*>(ws);
@@ -908,7 +978,10 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     p.da = (int32_t)dk;
     p.dc = (int32_t)dv;
     LRS_TRY(launch_carries<D>(nm, x, stream));
-    return launch_passes<D, false>(nm, x, stream);
+    set_vec<D>(p);
+    const uint64_t blocks = (uint64_t)(N * H * plan.segments);
+    return std::max(dk, dv) <= 64 ? launch_seq(nm, recurrence_forward<D, 64>, blocks, 128, stream, x)
+                                  : launch_seq(nm, recurrence_forward<D, 128>, blocks, 256, stream, x);
 }
 
 template <class D>
@@ -954,7 +1027,7 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     x.N = N;
     x.T = T;
     x.H = (int32_t)H;
-    x.passes = 2;
+    x.carries = 2;
     x.seg_len = plan.seg_len;
     x.segments = (int32_t)plan.segments;
     if (plan.segments > 1) {
@@ -997,13 +1070,9 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pk.u_scale = scale;
     pk.da = (int32_t)dv;
     pk.dc = (int32_t)dk;
-    pk.reverse = 1;
     pk.transposed = 1;
     pk.y_f32 = group > 1;
-    RecurrenceArgs z = x;
-    z.passes = 1;
-    PassArgs& pv = z.pass[0];  // dv
-    pv = PassArgs{};
+    PassArgs& pv = x.pass[2];  // dv
     pv.a = w[2];
     pv.b = w[1];
     pv.c = w[0];
@@ -1015,10 +1084,11 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pv.u_scale = scale;
     pv.da = (int32_t)dk;
     pv.dc = (int32_t)dv;
-    pv.reverse = 1;
     LRS_TRY(launch_carries<D>(nm, x, stream));
-    LRS_TRY((launch_passes<D, true>(nm, x, stream)));
-    LRS_TRY((launch_passes<D, false>(nm, z, stream)));
+    for (PassArgs& p : x.pass) set_vec<D>(p);
+    const uint64_t blocks = (uint64_t)(N * H * plan.segments) * 3;
+    LRS_TRY(std::max(dk, dv) <= 64 ? launch_seq(nm, recurrence_backward<D, 64>, blocks, 128, stream, x)
+                                   : launch_seq(nm, recurrence_backward<D, 128>, blocks, 256, stream, x));
     DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, plan.seg_len, (int32_t)H,
                      (int32_t)plan.segments};
     LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H * plan.segments), 64, stream, dg));
