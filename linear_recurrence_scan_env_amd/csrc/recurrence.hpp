@@ -86,6 +86,7 @@ __device__ __forceinline__ int64_t state_at(const PassArgs& p, int r, int c)
 // is split as far as its result needs.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 template <class D>
@@ -123,34 +124,34 @@ __device__ __forceinline__ f32x4 mma(const Frag<LA>& a, const Frag<LB>& b, f32x4
     return acc;
 }
 
-// A tile of kChunk steps of up to W elements in LDS, one plane per limb.  The
-// 16-byte units of a row are permuted by its index, so that both ways of
-// reading a fragment (16 rows at one unit; 4 rows at 16 neighbouring columns,
-// transposed) touch every bank once.
+// A tile of kChunk steps of up to W elements in LDS, one plane per limb.  Rows
+// are an odd number of 16-byte units long, and the rows of each 16 are laid out
+// 0, 8, 1, 9, ..., so that both ways of reading a fragment (16 rows at one
+// unit; 8 rows at two neighbouring units, transposed) touch every bank once,
+// at addresses that differ from lane to lane by one offset only.
 constexpr int kChunk = 64;
 constexpr int kTile = 16;
 
 template <int W, int L>
 struct StepTile {
-    uint16_t e[L][kChunk * W];
+    static constexpr int kRow = W + 8;
+    uint16_t e[L][kChunk * kRow];
 
     static __device__ __forceinline__ int at(int row, int col)
     {
-        const int mix = W == 128 ? ((row & 7) << 1) | ((row >> 3) & 1)
-                                 : (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
-        return row * W + (((col >> 3) ^ mix) << 3) + (col & 7);
+        return ((row & ~15) | ((row & 7) << 1) | ((row >> 3) & 1)) * kRow + col;
     }
     // A fragment of 16 rows (from `row`) over 32 columns (from `col`): lane l
     // holds row l % 16, columns 4 (l / 16) + 0..3 and 16 more.  Both operands
     // of every product use this order of the 32.
     __device__ __forceinline__ Frag<L> rows(int row, int col, int lane) const
     {
-        const int r = row + (lane & 15), c = col + (lane >> 4) * 4;
+        const int mine = at(lane & 15, (lane >> 4) * 4), to = row * kRow + col;
         Frag<L> f;
 #pragma unroll
         for (int l = 0; l < L; ++l) {
-            const s16x4 lo = *reinterpret_cast<const s16x4*>(&e[l][at(r, c)]);
-            const s16x4 hi = *reinterpret_cast<const s16x4*>(&e[l][at(r, c + 16)]);
+            const s16x4 lo = *reinterpret_cast<const s16x4*>(&e[l][mine + to]);
+            const s16x4 hi = *reinterpret_cast<const s16x4*>(&e[l][mine + to + 16]);
             f.x[l] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
         return f;
@@ -160,80 +161,128 @@ struct StepTile {
     // lanes of a group four rows of 16 columns, 8 bytes read by each lane.
     __device__ __forceinline__ Frag<L> columns(int row, int col, int lane) const
     {
-        const int r = row + (lane >> 4) * 4 + ((lane & 15) >> 2), c = col + (lane & 3) * 4;
+        const int mine = at((lane >> 4) * 4 + ((lane & 15) >> 2), (lane & 3) * 4), to = row * kRow + col;
         Frag<L> f;
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][at(r, c)]);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][at(r + 16, c)]);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][mine + to]);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][mine + to + 16 * kRow]);
             f.x[l] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
         return f;
     }
 };
 
-// Eight elements of a row from column c on, zero beyond `dim`.
+// Eight elements of a row from column c on as they are stored, zero beyond
+// `dim`; `vec`: the bytes that an access may take (16, 4 or one element).
 template <class D>
-__device__ __forceinline__ f32x8 load8(const D* row, int c, int dim, bool vec)
+struct Raw8 {
+    u32x4 w[sizeof(D) / 2];
+};
+
+template <class D>
+__device__ __forceinline__ Raw8<D> load8(const D* row, int c, int dim, int vec)
 {
-    f32x8 v = {};
-    if (vec && c + 8 <= dim) {
-        if constexpr (sizeof(D) == 4) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(row + c);
-            const f32x4 b = *reinterpret_cast<const f32x4*>(row + c + 4);
-            v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(row + c);
+    Raw8<D> v = {};
+    if (vec == 16 && c + 8 <= dim) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float lo, hi;
-                unpack2<D>(w[k], lo, hi);
-                v[2 * k] = lo;
-                v[2 * k + 1] = hi;
-            }
-        }
+        for (int k = 0; k < (int)sizeof(D) / 2; ++k)
+            v.w[k] = *reinterpret_cast<const u32x4*>(row + c + k * (16 / sizeof(D)));
+    } else if (sizeof(D) == 4 || vec >= 4) {
+        const uint32_t* const words = reinterpret_cast<const uint32_t*>(row + c);
+        constexpr int per = 4 / sizeof(D);
+#pragma unroll
+        for (int k = 0; k < 8 / per; ++k)
+            if (c + k * per < dim) v.w[k / 4][k % 4] = words[k];
     } else {
+        const uint16_t* const halves = reinterpret_cast<const uint16_t*>(row + c);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (c + k < dim) v[k] = to_f32(row[c + k]);
+            if (c + k < dim) v.w[0][k / 2] |= (uint32_t)halves[k] << (16 * (k & 1));
     }
     return v;
 }
 
-// The same as one-limb elements, unconverted.
-__device__ __forceinline__ u32x4 load8_raw(const bf16_t* row, int c, int dim, bool vec)
-{
-    if (vec && c + 8 <= dim) return *reinterpret_cast<const u32x4*>(row + c);
-    u32x4 w = {};
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (c + k < dim) w[k / 2] |= (uint32_t)row[c + k].bits << (16 * (k & 1));
-    return w;
-}
-
-// Steps t0 .. t0 + count - 1 of one head into a tile, zero beyond them.
 template <class D, int W>
-__device__ __forceinline__ void stage(StepTile<W, kLimbs<D>>& tile, const SeqView& view, int64_t n, int h,
-                                      int64_t t0, int count, int dim)
+__device__ __forceinline__ void put8(StepTile<W, kLimbs<D>>& tile, int at, const Raw8<D>& v)
 {
-    constexpr int L = kLimbs<D>;
-    const int units = (dim + 31) / 32 * 4;  // what the products read
-    for (int u = threadIdx.x; u < kChunk * units; u += blockDim.x) {
-        const int row = u / units, c = (u % units) * 8;
-        if constexpr (L == 1) {
-            u32x4 v = {};
-            if (row < count) v = load8_raw(seq_row<D>(view, n, t0 + row, h), c, dim, view.vec != 0);
-            *reinterpret_cast<u32x4*>(&tile.e[0][tile.at(row, c)]) = v;
+    if constexpr (kLimbs<D> == 1) {
+        *reinterpret_cast<u32x4*>(&tile.e[0][at]) = v.w[0];
+    } else {
+        f32x8 e;
+        if constexpr (sizeof(D) == 4) {
+            e = __builtin_bit_cast(f32x8, v);
         } else {
-            f32x8 v = {};
-            if (row < count) v = load8(seq_row<D>(view, n, t0 + row, h), c, dim, view.vec != 0);
-            const Frag<L> f = split<L>(v);
 #pragma unroll
-            for (int l = 0; l < L; ++l) *reinterpret_cast<bf16x8*>(&tile.e[l][tile.at(row, c)]) = f.x[l];
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;
+                unpack2<D>(v.w[0][k], lo, hi);
+                e[2 * k] = lo;
+                e[2 * k + 1] = hi;
+            }
         }
+        const Frag<kLimbs<D>> f = split<kLimbs<D>>(e);
+#pragma unroll
+        for (int l = 0; l < kLimbs<D>; ++l) *reinterpret_cast<bf16x8*>(&tile.e[l][at]) = f.x[l];
     }
 }
+
+// One head's steps of an array, from the first of a segment on.
+template <class D>
+struct Rows {
+    D* p;
+    int64_t step;
+    int32_t dim, vec;
+
+    __device__ __forceinline__ Rows(const SeqView& v, int64_t n, int64_t t, int h, int dim)
+        : p(seq_row_out<D>(v, n, t, h)), step(v.step), dim(dim), vec(v.vec)
+    {
+    }
+};
+
+// A block of 2 W threads moves 64 steps of one head's array into a tile in two
+// halves: fetch() starts the loads (four of a thread's 16-byte units, 16 steps
+// apart), put() writes what arrived to LDS, zero beyond dim.  Steps beyond
+// `count` read the last one again: their weights are zero.  kWide: every row is
+// on 16 bytes and dim a multiple of 8, and 64 steps lie within 2 GiB, so that
+// one 32-bit offset per lane and access is all the addressing there is; nothing
+// then branches around the loads, which would make the wave wait for them where
+// the branches join.
+template <class D, int W, bool kWide>
+struct Staged {
+    Raw8<D> r[4];
+
+    __device__ __forceinline__ void fetch(const Rows<D>& rows, int64_t t, int count)
+    {
+        const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+        const D* const from = rows.p + t * rows.step;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at_row = min(row + 16 * k, count - 1);
+            if constexpr (kWide) {
+                const uint32_t at = (uint32_t)at_row * (uint32_t)rows.step + (c < rows.dim ? c : 0);
+#pragma unroll
+                for (int j = 0; j < (int)sizeof(D) / 2; ++j)
+                    r[k].w[j] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(from) +
+                                                                (at * (uint32_t)sizeof(D) + 16u * j));
+            } else {
+                r[k] = Raw8<D>{};
+                if (c < rows.dim) r[k] = load8(from + at_row * rows.step, c, rows.dim, rows.vec);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(StepTile<W, kLimbs<D>>& tile, const Rows<D>& rows) const
+    {
+        const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            Raw8<D> v = r[k];
+            if (kWide && c >= rows.dim) v = Raw8<D>{};
+            put8<D, W>(tile, tile.at(row, c) + 16 * k * tile.kRow, v);
+        }
+    }
+};
 
 // The decays of a chunk of 64 steps, in four tiles of 16.  With p the running
 // sum of log2 decays within a tile (in 64 bits: a strong decay before a weak
@@ -248,22 +297,45 @@ struct ChunkDecay {
     float tail[kChunk];   // from this step, exclusive, to the end of its tile
     float entry[kChunk];  // from the start of the chunk, inclusive
     float exit[kChunk];   // to the end of the chunk
-    float whole[4];       // of each tile
+    float between[4][4];  // of the tiles between two
     float total;          // of the chunk
 };
 
+// The log decay and the reset mask of a lane's step, as they are stored, loaded
+// like the steps themselves.
 template <class D>
-__device__ __forceinline__ void chunk_decay(ChunkDecay& s, const RecurrenceArgs& x, int64_t n, int h,
-                                            int64_t t0, int count, int lane)
-{
-    double p = 0.0;
-    int m = 0;
-    if (lane < count) {
-        const float g = to_f32(*seq_row<D>(x.g, n, t0 + lane, h));
-        const bool reset = x.reset.p != nullptr && *seq_row<uint8_t>(x.reset, n, t0 + lane, 0) != 0;
-        m = reset || g == -INFINITY;
-        p = m ? 0.0 : (double)g * 1.4426950408889634;
+struct DecayRows {
+    const D* g;
+    const uint8_t* reset;
+    int64_t g_step, reset_step;
+    bool resets;
+    D next_g;
+    uint8_t next_reset;
+
+    __device__ __forceinline__ DecayRows(const RecurrenceArgs& x, int64_t n, int64_t t, int h)
+        : g(seq_row<D>(x.g, n, t, h)), g_step(x.g.step), resets(x.reset.p != nullptr)
+    {
+        reset = resets ? seq_row<uint8_t>(x.reset, n, t, 0) : reinterpret_cast<const uint8_t*>(g);
+        reset_step = resets ? x.reset.step : 0;
     }
+    __device__ __forceinline__ void fetch(int64_t t, int count, int lane)
+    {
+        t += min(lane, count - 1);
+        next_g = g[t * g_step];
+        next_reset = reset[t * reset_step];
+    }
+    // -infinity where the step is cut
+    __device__ __forceinline__ float value() const
+    {
+        return resets && next_reset != 0 ? -INFINITY : to_f32(next_g);
+    }
+};
+
+__device__ __forceinline__ void chunk_decay(ChunkDecay& s, float g, int count, int lane)
+{
+    const bool in = lane < count;
+    int m = in && g == -INFINITY;
+    double p = m || !in ? 0.0 : (double)g * 1.4426950408889634;
     const int i = lane & 15;
 #pragma unroll
     for (int o = 1; o < kTile; o <<= 1) {
@@ -276,9 +348,9 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& s, const RecurrenceArgs&
     }
     const double ptot = __shfl(p, lane | 15);
     const int mtot = __shfl(m, lane | 15);
-    const float head = m ? 0.0f : exp2f((float)p);
-    const float tail = m != mtot ? 0.0f : exp2f((float)(ptot - p));
-    const float whole = mtot ? 0.0f : exp2f((float)ptot);
+    const float head = m ? 0.0f : __builtin_amdgcn_exp2f((float)p);
+    const float tail = m != mtot ? 0.0f : __builtin_amdgcn_exp2f((float)(ptot - p));
+    const float whole = mtot ? 0.0f : __builtin_amdgcn_exp2f((float)ptot);
     float w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = __shfl(whole, k * kTile);
@@ -290,24 +362,37 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& s, const RecurrenceArgs&
         if (k > tile) after *= w[k];
     }
     s.p[lane] = p;
-    s.m[lane] = m;
-    s.head[lane] = head;
-    s.tail[lane] = tail;
-    s.entry[lane] = before * head;
-    s.exit[lane] = after * tail;
-    if (lane < 4) s.whole[lane] = w[lane];
+    s.m[lane] = in ? m : -1;  // steps beyond the end have no part in anything
+    s.head[lane] = in ? head : 0.0f;
+    s.tail[lane] = in ? tail : 0.0f;
+    s.entry[lane] = in ? before * head : 0.0f;
+    s.exit[lane] = in ? after * tail : 0.0f;
+    if (lane < 16) {
+        float f = 1.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((k > (lane & 3)) != (k >= (lane >> 2)) && k != (lane & 3) && k != (lane >> 2)) f *= w[k];
+        s.between[lane >> 2][lane & 3] = f;
+    }
     if (lane == 0) s.total = w[0] * w[1] * w[2] * w[3];
 }
 
 // S = total S + b^T (w c) over a chunk of 64 steps; w: the weight of each step,
-// fc: the wave's columns of c.
-template <class D, int W>
+// fc: the wave's columns of c.  The weighted c is fp32: two limbs keep 16 of its
+// bits, enough for what is made of S in 16-bit results and their differences; a
+// state that is itself a result takes a third (LW = 3, all 24).
+template <class D>
+constexpr int kStateLimbs(bool exact)
+{
+    return kLimbs<D> > 1 || exact ? 3 : 2;
+}
+
+template <int LW, class D, int W>
 __device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<W, kLimbs<D>>& tb,
                                           const Frag<kLimbs<D>> (&fc)[2][2], const float* w, float total,
                                           float scale, int da, int lane)
 {
     constexpr int L = kLimbs<D>;
-    constexpr int LW = 3;  // limbs of the weighted c: states are fp32, their sums keep 24 bits
     const int group = lane >> 4;
     Frag<LW> fw[2][2];
 #pragma unroll
@@ -323,6 +408,7 @@ __device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<
             fw[b][u] = split<LW>(v * v8);
         }
     }
+    const float f = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, total)));
 #pragma unroll
     for (int k = 0; k < W / 16; ++k) {
         if (k * 16 >= da) break;
@@ -330,7 +416,7 @@ __device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             // a cut drops the state, whatever it holds
-            f32x4 v = total == 0.0f ? f32x4{} : S[k][u] * total;
+            f32x4 v = f == 0.0f ? f32x4{} : S[k][u] * f;
 #pragma unroll
             for (int b = 0; b < 2; ++b) v = mma(fb[b], fw[b][u], v);
             S[k][u] = v;
@@ -340,19 +426,28 @@ __device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<
 
 // A pass by matrix instructions, 64 steps at a time.  A wave holds 32 columns
 // of the state, all its rows, in accumulators; the block's waves share the
-// steps in LDS.  Per chunk, with X, Z the weights from the chunk's start and to
-// its end in scan order:
+// steps, and the products a b^T of which each computes its part, in LDS.  Per
+// chunk, with X, Z the weights from the chunk's start and to its end in scan
+// order:
 //     y^T = S^T a^T X + c^T (D o (a b^T))^T        (S before the chunk)
 //     S   = total S + b^T (Z c)
-// Results of one product leave the matrix unit in the order in which the next
-// one takes its operand (16 columns by 4 consecutive rows per lane group), so
-// a b^T and S go from product to product in registers.
-template <class D, int W>
+// Results of a product leave the matrix unit with 4 consecutive rows of one of
+// 16 columns per lane, and operands are read in that order of their summed
+// index, so S feeds the next product from the registers that it is kept in.
+template <class D, int W, int LS>
 struct PassShared {
+    // the products take a's place where LDS does not hold both
+    static constexpr bool kOverlay = 3 * sizeof(StepTile<W, kLimbs<D>>) + sizeof(StepTile<64, LS>) > 160000;
     StepTile<W, kLimbs<D>> a, b, c;
+    StepTile<64, LS> own_ab[kOverlay ? 0 : 1];
     ChunkDecay decay;
-    float dot[4][kChunk];
-    float cross[4];
+    float dot[W / 32][kChunk];
+    float cross[W / 32];
+
+    __device__ __forceinline__ StepTile<64, LS>& ab()
+    {
+        return kOverlay ? *reinterpret_cast<StepTile<64, LS>*>(&a) : own_ab[0];
+    }
 };
 
 // Four elements of a row from column c on, out of `dim` (one access where the
@@ -398,13 +493,20 @@ __device__ __forceinline__ f32x4 load4(const D* row, int c, int dim, bool vec)
     return v;
 }
 
-template <class D, int W, bool back, bool kPrecise>
+// Limbs of a b^T and of the state as operands: as many as the inputs have, and
+// at least two where q.dq and k.dk are wanted.
+template <class D>
+constexpr int kOperandLimbs(bool precise)
+{
+    return kLimbs<D> > 1 ? kLimbs<D> : (precise ? 2 : 1);
+}
+
+template <class D, int W, bool kWide, bool back, bool kPrecise, int LW, int LS>
 __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs& p, uint32_t block,
-                                         PassShared<D, W>& sh)
+                                         PassShared<D, W, LS>& sh)
 {
     constexpr int L = kLimbs<D>;
-    constexpr int LS = L > 1 ? L : (kPrecise ? 2 : 1);  // limbs of a b^T and of the state
-    constexpr int K = W / 32;
+    constexpr int K = W / 32, kWaves = W / 32;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int group = lane >> 4, col = lane & 15;
@@ -416,6 +518,25 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     const int64_t at = (int64_t)block * p.da * p.dc;
     const int64_t first = seg * x.seg_len;
     const int64_t steps = x.T - first < x.seg_len ? x.T - first : x.seg_len;
+    const int chunks = (int)((steps + kChunk - 1) / kChunk);
+
+    const Rows<D> ra(p.a, n, first, h, p.da), rb(p.b, n, first, h, p.da), rc(p.c, n, first, h, p.dc);
+    const Rows<D> rd(kPrecise ? p.d : p.c, n, first, h, p.dc);
+    DecayRows<D> decays(x, n, first, h);
+    const bool y_f32 = kPrecise && p.y_f32;
+    char* const y_base = y_f32 ? reinterpret_cast<char*>(seq_row_out<float>(p.y, n, first, h))
+                               : reinterpret_cast<char*>(seq_row_out<D>(p.y, n, first, h));
+    const int64_t y_step = p.y.step;
+    Staged<D, W, kWide> ga, gb, gc;
+    const auto fetch = [&](int i) {
+        const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
+        const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
+        decays.fetch(done, count, lane);
+        ga.fetch(ra, done, count);
+        gb.fetch(rb, done, count);
+        gc.fetch(rc, done, count);
+    };
+    fetch(0);
 
     // S[2 k + s][u][r]: row 32 k + 16 s + 4 group + r, column c0 + 16 u + col
     f32x4 S[2 * K][2];
@@ -429,22 +550,59 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 S[k][u][r] = p.init && row < p.da && c < p.dc ? p.init[at + state_at(p, row, c)] : 0.0f;
             }
 
-    const int64_t chunks = (steps + kChunk - 1) / kChunk;
-    for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t done = (back ? chunks - 1 - i : i) * kChunk;
-        const int64_t t0 = first + done;
+    for (int i = 0; i < chunks; ++i) {
+        const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
         const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
+        ga.put(sh.a, ra);
+        gb.put(sh.b, rb);
+        gc.put(sh.c, rc);
+        if (wave == 0) chunk_decay(sh.decay, decays.value(), count, lane);
         __syncthreads();
-        if (wave == 0) chunk_decay<D>(sh.decay, x, n, h, t0, count, lane);
-        stage<D, W>(sh.a, p.a, n, h, t0, count, p.da);
-        stage<D, W>(sh.b, p.b, n, h, t0, count, p.da);
-        stage<D, W>(sh.c, p.c, n, h, t0, count, p.dc);
-        __syncthreads();
+        if (i + 1 < chunks) fetch(i + 1);
 
+        // the wave's strips of a b^T, weighted: tile s has rows (steps of b) 16 s + 4 group + r,
+        // columns (steps of a) 16 q + col; only one side of the diagonal is not zero
+        f32x4 ab[4 / kWaves][4];
+#pragma unroll
+        for (int j = 0; j < 4 / kWaves; ++j) {
+            const int q = j == 0 ? wave : 3 - wave;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) ab[j][s] = f32x4{};
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (k * 32 >= p.da) break;
+                const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    if (back ? s >= q : s <= q) ab[j][s] = mma(sh.b.rows(s * 16, k * 32, lane), fa, ab[j][s]);
+            }
+            const int step = q * 16 + col;
+            const float mine = (back ? sh.decay.tail : sh.decay.head)[step] * p.p_scale;
+            const double pi = sh.decay.p[step];
+            const int mi = sh.decay.m[step];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (s == q) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int o = s * 16 + group * 4 + r;
+                        const float d = (float)(back ? sh.decay.p[o] - pi : pi - sh.decay.p[o]);
+                        const bool in = (back ? o >= step : o <= step) && sh.decay.m[o] == mi;
+                        // (the exponential of -infinity is 0; no branch)
+                        const float w = __builtin_amdgcn_exp2f(in ? d : -INFINITY) * p.p_scale;
+                        ab[j][s][r] = in ? ab[j][s][r] * w : 0.0f;
+                    }
+                } else if (back ? s > q : s < q) {
+                    const float* const theirs = back ? sh.decay.head : sh.decay.tail;
+                    ab[j][s] *= *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]) *
+                                (mine * sh.decay.between[q][s]);
+                }
+            }
+        }
+
+        // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col
+        f32x4 y[4][2] = {};
         if (c0 < p.dc) {
-            // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col;
-            // ab[q][s]: rows (steps) 16 s + 4 group + r, column 16 q + col
-            f32x4 y[4][2] = {}, ab[4][4] = {};
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (k * 32 >= p.da) break;
@@ -452,69 +610,62 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     s[u] = split<LS>(__builtin_shufflevector(S[2 * k][u], S[2 * k + 1][u], 0, 1, 2, 3, 4, 5, 6, 7));
-                Frag<L> fb[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) fb[q] = sh.b.rows(q * 16, k * 32, lane);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) y[q][u] = mma(s[u], fa, y[q][u]);
-                    // only one side of the diagonal is used: forward steps s <= q
-#pragma unroll
-                    for (int s2 = 0; s2 < 4; ++s2)
-                        if (back ? s2 >= q : s2 <= q) ab[q][s2] = mma(fb[s2], fa, ab[q][s2]);
                 }
             }
+        }
+        if constexpr (PassShared<D, W, LS>::kOverlay) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4 / kWaves; ++j) {
+            const int q = j == 0 ? wave : 3 - wave;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const Frag<LS> f =
+                    split<LS>(__builtin_shufflevector(ab[j][2 * b], ab[j][2 * b + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+                StepTile<64, LS>& to = sh.ab();
+#pragma unroll
+                for (int l = 0; l < LS; ++l) {
+                    const s16x8 e = __builtin_bit_cast(s16x8, f.x[l]);
+                    const int here = to.at(col, group * 4) + q * 16 * to.kRow + b * 32;
+                    *reinterpret_cast<s16x4*>(&to.e[l][here]) = __builtin_shufflevector(e, e, 0, 1, 2, 3);
+                    *reinterpret_cast<s16x4*>(&to.e[l][here + 16]) = __builtin_shufflevector(e, e, 4, 5, 6, 7);
+                }
+            }
+        }
+        __syncthreads();
 
-            // weights
+        if (c0 < p.dc) {
+            f32x4 d[4][2];
+            if constexpr (kPrecise)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        d[q][u] = load4<D>(rd.p + (done + min(q * 16 + col, count - 1)) * rd.step,
+                                           c0 + u * 16 + group * 4, p.dc, kWide || rd.vec != 0);
             Frag<L> fc[2][2];  // columns c0 + 16 u + l % 16 of 32 steps each
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
-            const float* from = back ? sh.decay.exit : sh.decay.entry;
-            const float* mine = back ? sh.decay.tail : sh.decay.head;
-            const float* theirs = back ? sh.decay.head : sh.decay.tail;
+            const float* const from = back ? sh.decay.exit : sh.decay.entry;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int step = q * 16 + col;
-                const float in = from[step];
+                const float in = from[q * 16 + col];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) y[q][u] = in == 0.0f ? f32x4{} : y[q][u] * in;
-                float lead = mine[step] * p.p_scale;
-                // tiles from the nearest on, the decay of those between gathered on the way
-#pragma unroll
-                for (int d = 1; d < 4; ++d) {
-                    const int s = back ? q + d : q - d;
-                    if (s < 0 || s > 3) continue;
-                    const f32x4 f = *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]);
-#pragma unroll
-                    for (int s2 = 0; s2 < 4; ++s2)
-                        if (s2 == s) ab[q][s2] *= f * lead;
-                    lead *= sh.decay.whole[s];
-                }
-                const double pi = sh.decay.p[step];
-                const int mi = sh.decay.m[step];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = q * 16 + group * 4 + r;
-                    const double d = back ? sh.decay.p[j] - pi : pi - sh.decay.p[j];
-                    const bool in_order = back ? j >= step : j <= step;
-                    const float w = in_order && sh.decay.m[j] == mi ? exp2f((float)d) * p.p_scale : 0.0f;
-                    ab[q][q][r] = w == 0.0f ? 0.0f : ab[q][q][r] * w;
-                }
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     if (back ? 2 * b + 1 < q : 2 * b > q) continue;
-                    const Frag<LS> fp =
-                        split<LS>(__builtin_shufflevector(ab[q][2 * b], ab[q][2 * b + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    const Frag<LS> f = sh.ab().rows(q * 16, b * 32, lane);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) y[q][u] = mma(fc[b][u], fp, y[q][u]);
+                    for (int u = 0; u < 2; ++u) y[q][u] = mma(fc[b][u], f, y[q][u]);
                 }
             }
-
-            // y out
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int step = q * 16 + col;
@@ -523,38 +674,38 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 for (int u = 0; u < 2; ++u) {
                     const int c = c0 + u * 16 + group * 4;
                     const f32x4 v = y[q][u] * p.y_scale;
+                    if constexpr (kPrecise) {
+                        const f32x4 e = d[q][u] * v;
+                        dot += (e[0] + e[1]) + (e[2] + e[3]);
+                    }
                     if (step < count) {
-                        if (kPrecise) {
-                            const f32x4 d = load4<D>(seq_row<D>(p.d, n, t0 + step, h), c, p.dc, p.d.vec != 0) * v;
-                            dot += (d[0] + d[1]) + (d[2] + d[3]);
-                        }
-                        if (kPrecise && p.y_f32)
-                            store4<float>(seq_row_out<float>(p.y, n, t0 + step, h), c, p.dc, p.y.vec != 0, v);
+                        const int64_t at_row = (done + step) * y_step;
+                        if (y_f32)
+                            store4<float>(reinterpret_cast<float*>(y_base) + at_row, c, p.dc,
+                                          kWide || p.y.vec != 0, v);
                         else
-                            store4<D>(seq_row_out<D>(p.y, n, t0 + step, h), c, p.dc, p.y.vec != 0, v);
+                            store4<D>(reinterpret_cast<D*>(y_base) + at_row, c, p.dc, kWide || p.y.vec != 0, v);
                     }
                 }
-                if (kPrecise) {
+                if constexpr (kPrecise) {
                     dot += __shfl_xor(dot, 16);
                     dot += __shfl_xor(dot, 32);
                     if (group == 0) sh.dot[wave][step] = dot;
                 }
             }
-
             // the state after the chunk
-            add_chunk<D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale, p.da,
-                            lane);
+            add_chunk<LW, D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale,
+                                p.da, lane);
         }
-        if (kPrecise) {
-            __syncthreads();
-            if (wave == 0 && lane < count) {
-                float sum = 0.0f;
-                for (int w = 0; w * 32 < p.dc; ++w) sum += sh.dot[w][lane];
-                p.dot[head * x.T + t0 + lane] = sum;
-            }
+        __syncthreads();
+        if (kPrecise && wave == 0 && lane < count) {
+            float sum = 0.0f;
+            for (int w = 0; w * 32 < p.dc; ++w) sum += sh.dot[w][lane];
+            p.dot[head * x.T + first + done + lane] = sum;
         }
     }
 
+    if (p.last == nullptr && p.cross == nullptr) return;
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < 2 * K; ++k)
@@ -574,34 +725,43 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
         __syncthreads();
         if (threadIdx.x == 0) {
             float sum = 0.0f;
-            for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += sh.cross[w];
+            for (int w = 0; w < kWaves; ++w) sum += sh.cross[w];
             p.cross[block] = sum;
         }
     }
 }
 
-template <class D, int W>
-__global__ __launch_bounds__(2 * W, 2) void recurrence_forward(const RecurrenceArgs x)
+// Two waves per SIMD where the steps' tiles leave room in LDS for them.
+template <class D>
+constexpr int kPassWaves = kLimbs<D> == 1 ? 2 : 1;
+
+template <class D, int W, bool kWide, bool kExact>
+__global__ __launch_bounds__(2 * W, kPassWaves<D>) void recurrence_forward(const RecurrenceArgs x)
 {
-    __shared__ PassShared<D, W> sh;
-    run_pass<D, W, false, false>(x, x.pass[0], blockIdx.x, sh);
+    constexpr int LS = kOperandLimbs<D>(false);
+    __shared__ PassShared<D, W, LS> sh;
+    run_pass<D, W, kWide, false, false, kStateLimbs<D>(kExact), LS>(x, x.pass[0], blockIdx.x, sh);
 }
 
 // The three passes of the backward call: dq and dk with q.dq and k.dk to a
 // precision that their differences keep, and dv.
-template <class D, int W>
-__global__ __launch_bounds__(2 * W, 2) void recurrence_backward(const RecurrenceArgs x)
+template <class D, int W, bool kWide, bool kExact>
+__global__ __launch_bounds__(2 * W, kPassWaves<D>) void recurrence_backward(const RecurrenceArgs x)
 {
-    __shared__ PassShared<D, W> sh;
+    constexpr int LS = kOperandLimbs<D>(true), LV = kOperandLimbs<D>(false);
+    __shared__ union {
+        PassShared<D, W, LS> precise;
+        PassShared<D, W, LV> plain;
+    } sh;
     const uint32_t block = blockIdx.x / 3, pass = blockIdx.x % 3;
-    if (pass == 0) run_pass<D, W, false, true>(x, x.pass[0], block, sh);
-    else if (pass == 1) run_pass<D, W, true, true>(x, x.pass[1], block, sh);
-    else run_pass<D, W, true, false>(x, x.pass[2], block, sh);
+    if (pass == 0) run_pass<D, W, kWide, false, true, kStateLimbs<D>(false), LS>(x, x.pass[0], block, sh.precise);
+    else if (pass == 1) run_pass<D, W, kWide, true, true, kStateLimbs<D>(false), LS>(x, x.pass[1], block, sh.precise);
+    else run_pass<D, W, kWide, true, false, kStateLimbs<D>(kExact), LV>(x, x.pass[2], block, sh.plain);
 }
 
 // The state that one segment alone leaves (from zero), and its decay, by the
 // same products; the last segment in scan order leaves none that is used.
-template <class D, int W>
+template <class D, int W, bool kWide, bool kExact>
 __global__ __launch_bounds__(2 * W) void segment_states(const RecurrenceArgs x)
 {
     __shared__ struct {
@@ -624,24 +784,35 @@ __global__ __launch_bounds__(2 * W) void segment_states(const RecurrenceArgs x)
     const int64_t steps = x.T - first < x.seg_len ? x.T - first : x.seg_len;
     f32x4 S[W / 16][2] = {};
     float total = 1.0f;
-    const int64_t chunks = (steps + kChunk - 1) / kChunk;
-    for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t done = (back ? chunks - 1 - i : i) * kChunk;
-        const int64_t t0 = first + done;
+    const int chunks = (int)((steps + kChunk - 1) / kChunk);
+    const Rows<D> rb(p.b, n, first, h, p.da), rc(p.c, n, first, h, p.dc);
+    DecayRows<D> decays(x, n, first, h);
+    Staged<D, W, kWide> gb, gc;
+    const auto fetch = [&](int i) {
+        const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
         const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
+        decays.fetch(done, count, lane);
+        gb.fetch(rb, done, count);
+        gc.fetch(rc, done, count);
+    };
+    fetch(0);
+    for (int i = 0; i < chunks; ++i) {
+        const int64_t left = steps - (int64_t)(back ? chunks - 1 - i : i) * kChunk;
+        const int count = (int)(left < kChunk ? left : kChunk);
+        if (i > 0) __syncthreads();
+        gb.put(sh.b, rb);
+        gc.put(sh.c, rc);
+        if (wave == 0) chunk_decay(sh.decay, decays.value(), count, lane);
         __syncthreads();
-        if (wave == 0) chunk_decay<D>(sh.decay, x, n, h, t0, count, lane);
-        stage<D, W>(sh.b, p.b, n, h, t0, count, p.da);
-        stage<D, W>(sh.c, p.c, n, h, t0, count, p.dc);
-        __syncthreads();
+        if (i + 1 < chunks) fetch(i + 1);
         if (c0 >= p.dc) continue;
         Frag<kLimbs<D>> fc[2][2];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
-        add_chunk<D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale, p.da,
-                        lane);
+        add_chunk<kStateLimbs<D>(kExact), D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit,
+                                                sh.decay.total, p.u_scale, p.da, lane);
         total *= sh.decay.total;
     }
     float* const to = p.states + (head * x.segments + next) * (int64_t)p.da * p.dc;
@@ -893,38 +1064,64 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
     return p;
 }
 
-// Whether rows start where accesses of `unit` elements may.
-inline void set_vec(SeqView& v, int unit, int elem_bytes)
+// Whether every row starts on a multiple of `unit` elements.
+inline bool rows_on(const SeqView& v, int unit, int elem_bytes)
 {
-    v.vec = aligned(v.p, (uintptr_t)(unit * elem_bytes)) && v.env % unit == 0 && v.step % unit == 0 &&
-            v.head % unit == 0;
+    return aligned(v.p, (uintptr_t)(unit * elem_bytes)) && v.env % unit == 0 && v.step % unit == 0 &&
+           v.head % unit == 0;
 }
 
+// The bytes that one access to a row of `dim` elements may take, in load8.
 template <class D>
-void set_vec(PassArgs& p)
+void set_vec(SeqView& v, int dim)
 {
-    constexpr int s = sizeof(D), unit = 16 / s;
-    set_vec(p.a, unit, s);
-    set_vec(p.b, unit, s);
-    set_vec(p.c, unit, s);
-    set_vec(p.d, 4, s);
-    set_vec(p.y, 4, p.y_f32 ? 4 : s);
-    if (p.dc % 4 != 0) p.d.vec = p.y.vec = 0;
+    constexpr int s = sizeof(D);
+    v.vec = rows_on(v, 16 / s, s) && dim % 8 == 0 ? 16 : rows_on(v, 4 / s, s) && dim % (4 / s) == 0 ? 4 : s;
 }
+
+// Whether one 32-bit offset reaches 64 steps of the array.
+template <class D>
+bool steps_near(const SeqView& v)
+{
+    return v.step <= (int64_t(1) << 31) / (kChunk * (int64_t)sizeof(D)) - kMaxDim;
+}
+
+// Sets how the pass's arrays are accessed; true if kWide accesses serve them.
+template <class D>
+bool set_vec(PassArgs& p)
+{
+    bool wide = true;
+    for (SeqView* v : {&p.a, &p.b, &p.c}) {
+        set_vec<D>(*v, v == &p.c ? p.dc : p.da);
+        wide = wide && v->vec == 16 && steps_near<D>(*v);
+    }
+    p.d.vec = p.dc % 4 == 0 && rows_on(p.d, 4, sizeof(D));
+    p.y.vec = p.dc % 4 == 0 && rows_on(p.y, 4, p.y_f32 ? 4 : sizeof(D));
+    return wide && p.y.vec && (p.d.p == nullptr || p.d.vec);
+}
+
+// The kernel for a call's width and accesses, and whether a state is a result of
+// the call (kExact differs from not only where inputs are one limb).
+#define LRS_PICK_EXACT(kernel, D, W, wide, exact)                                             \
+    ((exact) || kLimbs<D> > 1 ? ((wide) ? kernel<D, W, true, true> : kernel<D, W, false, true>) \
+                              : ((wide) ? kernel<D, W, true, kLimbs<D> != 1>                    \
+                                        : kernel<D, W, false, kLimbs<D> != 1>))
+#define LRS_PICK(kernel, D, widest, wide, exact)                   \
+    ((widest) <= 64 ? LRS_PICK_EXACT(kernel, D, 64, wide, exact)   \
+                    : LRS_PICK_EXACT(kernel, D, 128, wide, exact))
 
 // The states before every segment, in x.carry's directions.
 template <class D>
-lrs_status launch_carries(const char* nm, RecurrenceArgs x, hipStream_t stream)
+lrs_status launch_carries(const char* nm, RecurrenceArgs& x, bool wide, bool exact, hipStream_t stream)
 {
     if (x.segments == 1) return LRS_OK;
     for (int i = 0; i < x.carries; ++i) {
-        set_vec(x.carry[i].b, 16 / sizeof(D), sizeof(D));
-        set_vec(x.carry[i].c, 16 / sizeof(D), sizeof(D));
+        set_vec<D>(x.carry[i].b, x.carry[i].da);
+        set_vec<D>(x.carry[i].c, x.carry[i].dc);
     }
-    const int da = x.carry[0].da, dc = x.carry[0].dc;
+    const int da = x.carry[0].da, dc = x.carry[0].dc, widest = std::max(da, dc);
     const uint64_t heads = (uint64_t)x.N * x.H, blocks = heads * (x.segments - 1) * x.carries;
-    LRS_TRY(std::max(da, dc) <= 64 ? launch_seq(nm, segment_states<D, 64>, blocks, 128, stream, x)
-                                   : launch_seq(nm, segment_states<D, 128>, blocks, 256, stream, x));
+    LRS_TRY(launch_seq(nm, LRS_PICK(segment_states, D, widest, wide, exact), blocks, widest <= 64 ? 128 : 256, stream, x));
     return launch_seq(nm, join_segments<D>, (heads * da * dc + 255) / 256 * x.carries, 256, stream, x);
 }
 
@@ -977,11 +1174,12 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     p.u_scale = 1.0f;
     p.da = (int32_t)dk;
     p.dc = (int32_t)dv;
-    LRS_TRY(launch_carries<D>(nm, x, stream));
-    set_vec<D>(p);
-    const uint64_t blocks = (uint64_t)(N * H * plan.segments);
-    return std::max(dk, dv) <= 64 ? launch_seq(nm, recurrence_forward<D, 64>, blocks, 128, stream, x)
-                                  : launch_seq(nm, recurrence_forward<D, 128>, blocks, 256, stream, x);
+    const int widest = (int)std::max(dk, dv);
+    const bool wide = set_vec<D>(p);
+    const bool exact = final_state != nullptr;
+    LRS_TRY(launch_carries<D>(nm, x, wide, exact, stream));
+    return launch_seq(nm, LRS_PICK(recurrence_forward, D, widest, wide, exact), (uint64_t)(N * H * plan.segments),
+                      widest <= 64 ? 128 : 256, stream, x);
 }
 
 template <class D>
@@ -1084,11 +1282,13 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pv.u_scale = scale;
     pv.da = (int32_t)dk;
     pv.dc = (int32_t)dv;
-    LRS_TRY(launch_carries<D>(nm, x, stream));
-    for (PassArgs& p : x.pass) set_vec<D>(p);
-    const uint64_t blocks = (uint64_t)(N * H * plan.segments) * 3;
-    LRS_TRY(std::max(dk, dv) <= 64 ? launch_seq(nm, recurrence_backward<D, 64>, blocks, 128, stream, x)
-                                   : launch_seq(nm, recurrence_backward<D, 128>, blocks, 256, stream, x));
+    const int widest = (int)std::max(dk, dv);
+    bool wide = true;
+    for (PassArgs& p : x.pass) wide = set_vec<D>(p) && wide;
+    const bool exact = grad_initial != nullptr;
+    LRS_TRY(launch_carries<D>(nm, x, wide, exact, stream));
+    LRS_TRY(launch_seq(nm, LRS_PICK(recurrence_backward, D, widest, wide, exact), (uint64_t)(N * H * plan.segments) * 3,
+                       widest <= 64 ? 128 : 256, stream, x));
     DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, plan.seg_len, (int32_t)H,
                      (int32_t)plan.segments};
     LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H * plan.segments), 64, stream, dg));

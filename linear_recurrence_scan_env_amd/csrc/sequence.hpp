@@ -9,8 +9,8 @@
 namespace lrs {
 
 // An array of [env, step, head] rows of consecutive elements.  div: value
-// heads per stored head (head h of the call reads head h / div).  vec: rows
-// start on 16 bytes.
+// heads per stored head (head h of the call reads head h / div).  vec: how
+// wide an access to its rows may be, as its kernel counts it.
 struct SeqView {
     const void* p;
     int64_t env, step, head;
