@@ -135,7 +135,7 @@ constexpr int kTile = 16;
 template <int W, int L>
 struct StepTile {
     static constexpr int kRow = W + 8;
-    uint16_t e[L][kChunk * kRow];
+    alignas(16) uint16_t e[L][kChunk * kRow];
 
     static __device__ __forceinline__ int at(int row, int col)
     {
@@ -277,9 +277,12 @@ struct Staged {
         const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            Raw8<D> v = r[k];
-            if (kWide && c >= rows.dim) v = Raw8<D>{};
-            put8<D, W>(tile, tile.at(row, c) + 16 * k * tile.kRow, v);
+            if (kWide && rows.dim < W) {
+                const Raw8<D> v = c < rows.dim ? r[k] : Raw8<D>{};
+                put8<D, W>(tile, tile.at(row, c) + 16 * k * tile.kRow, v);
+            } else {
+                put8<D, W>(tile, tile.at(row, c) + 16 * k * tile.kRow, r[k]);
+            }
         }
     }
 };
@@ -323,6 +326,10 @@ struct DecayRows {
         t += min(lane, count - 1);
         next_g = g[t * g_step];
         next_reset = reset[t * reset_step];
+    }
+    __device__ __forceinline__ bool cut(int64_t t) const
+    {
+        return (resets && reset[t * reset_step] != 0) || to_f32(g[t * g_step]) == -INFINITY;
     }
     // -infinity where the step is cut
     __device__ __forceinline__ float value() const
@@ -415,8 +422,7 @@ __device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<
         const Frag<L> fb[2] = {tb.columns(0, k * 16, lane), tb.columns(32, k * 16, lane)};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            // a cut drops the state, whatever it holds
-            f32x4 v = f == 0.0f ? f32x4{} : S[k][u] * f;
+            f32x4 v = S[k][u] * f;
 #pragma unroll
             for (int b = 0; b < 2; ++b) v = mma(fb[b], fw[b][u], v);
             S[k][u] = v;
@@ -523,10 +529,12 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     const Rows<D> ra(p.a, n, first, h, p.da), rb(p.b, n, first, h, p.da), rc(p.c, n, first, h, p.dc);
     const Rows<D> rd(kPrecise ? p.d : p.c, n, first, h, p.dc);
     DecayRows<D> decays(x, n, first, h);
+    // (partial gradients of shared heads are fp32)
     const bool y_f32 = kPrecise && p.y_f32;
+    const int y_bytes = y_f32 ? 4 : (int)sizeof(D);
     char* const y_base = y_f32 ? reinterpret_cast<char*>(seq_row_out<float>(p.y, n, first, h))
                                : reinterpret_cast<char*>(seq_row_out<D>(p.y, n, first, h));
-    const int64_t y_step = p.y.step;
+    const int64_t y_step = p.y.step * y_bytes;
     Staged<D, W, kWide> ga, gb, gc;
     const auto fetch = [&](int i) {
         const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
@@ -538,7 +546,9 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     };
     fetch(0);
 
-    // S[2 k + s][u][r]: row 32 k + 16 s + 4 group + r, column c0 + 16 u + col
+    // S[2 k + s][u][r]: row 32 k + 16 s + 4 group + r, column c0 + 16 u + col; a state that
+    // the first step drops is not read, whatever it holds
+    const float* const init = p.init == nullptr || (!back && decays.cut(0)) ? nullptr : p.init;
     f32x4 S[2 * K][2];
 #pragma unroll
     for (int k = 0; k < 2 * K; ++k)
@@ -547,12 +557,13 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
-                S[k][u][r] = p.init && row < p.da && c < p.dc ? p.init[at + state_at(p, row, c)] : 0.0f;
+                S[k][u][r] = init && row < p.da && c < p.dc ? init[at + state_at(p, row, c)] : 0.0f;
             }
 
     for (int i = 0; i < chunks; ++i) {
         const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
         const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
+        char* const y_chunk = y_base + done * y_step;
         ga.put(sh.a, ra);
         gb.put(sh.b, rb);
         gc.put(sh.c, rc);
@@ -645,7 +656,9 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
-                        d[q][u] = load4<D>(rd.p + (done + min(q * 16 + col, count - 1)) * rd.step,
+                        d[q][u] = load4<D>(kWide ? rd.p + done * rd.step + (uint32_t)min(q * 16 + col, count - 1) *
+                                                                               (uint32_t)rd.step
+                                                 : rd.p + (done + min(q * 16 + col, count - 1)) * rd.step,
                                            c0 + u * 16 + group * 4, p.dc, kWide || rd.vec != 0);
             Frag<L> fc[2][2];  // columns c0 + 16 u + l % 16 of 32 steps each
 #pragma unroll
@@ -657,7 +670,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
             for (int q = 0; q < 4; ++q) {
                 const float in = from[q * 16 + col];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) y[q][u] = in == 0.0f ? f32x4{} : y[q][u] * in;
+                for (int u = 0; u < 2; ++u) y[q][u] *= in;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     if (back ? 2 * b + 1 < q : 2 * b > q) continue;
@@ -679,12 +692,12 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                         dot += (e[0] + e[1]) + (e[2] + e[3]);
                     }
                     if (step < count) {
-                        const int64_t at_row = (done + step) * y_step;
+                        char* const to = kWide ? y_chunk + (uint32_t)step * (uint32_t)y_step
+                                               : y_chunk + step * y_step;
                         if (y_f32)
-                            store4<float>(reinterpret_cast<float*>(y_base) + at_row, c, p.dc,
-                                          kWide || p.y.vec != 0, v);
+                            store4<float>(reinterpret_cast<float*>(to), c, p.dc, kWide || p.y.vec != 0, v);
                         else
-                            store4<D>(reinterpret_cast<D*>(y_base) + at_row, c, p.dc, kWide || p.y.vec != 0, v);
+                            store4<D>(reinterpret_cast<D*>(to), c, p.dc, kWide || p.y.vec != 0, v);
                     }
                 }
                 if constexpr (kPrecise) {
@@ -762,7 +775,7 @@ __global__ __launch_bounds__(2 * W, kPassWaves<D>) void recurrence_backward(cons
 // The state that one segment alone leaves (from zero), and its decay, by the
 // same products; the last segment in scan order leaves none that is used.
 template <class D, int W, bool kWide, bool kExact>
-__global__ __launch_bounds__(2 * W) void segment_states(const RecurrenceArgs x)
+__global__ __launch_bounds__(2 * W, kPassWaves<D>) void segment_states(const RecurrenceArgs x)
 {
     __shared__ struct {
         StepTile<W, kLimbs<D>> b, c;
@@ -1080,10 +1093,9 @@ void set_vec(SeqView& v, int dim)
 }
 
 // Whether one 32-bit offset reaches 64 steps of the array.
-template <class D>
-bool steps_near(const SeqView& v)
+inline bool steps_near(const SeqView& v)
 {
-    return v.step <= (int64_t(1) << 31) / (kChunk * (int64_t)sizeof(D)) - kMaxDim;
+    return v.step <= (int64_t(1) << 31) / (kChunk * 4) - kMaxDim;
 }
 
 // Sets how the pass's arrays are accessed; true if kWide accesses serve them.
@@ -1093,11 +1105,11 @@ bool set_vec(PassArgs& p)
     bool wide = true;
     for (SeqView* v : {&p.a, &p.b, &p.c}) {
         set_vec<D>(*v, v == &p.c ? p.dc : p.da);
-        wide = wide && v->vec == 16 && steps_near<D>(*v);
+        wide = wide && v->vec == 16 && steps_near(*v);
     }
     p.d.vec = p.dc % 4 == 0 && rows_on(p.d, 4, sizeof(D));
     p.y.vec = p.dc % 4 == 0 && rows_on(p.y, 4, p.y_f32 ? 4 : sizeof(D));
-    return wide && p.y.vec && (p.d.p == nullptr || p.d.vec);
+    return wide && p.y.vec && steps_near(p.y) && (p.d.p == nullptr || (p.d.vec && steps_near(p.d)));
 }
 
 // The kernel for a call's width and accesses, and whether a state is a result of
