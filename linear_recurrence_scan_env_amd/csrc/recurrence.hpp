@@ -1077,13 +1077,6 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
     return p;
 }
 
-// Whether every row starts on a multiple of `unit` elements.
-inline bool rows_on(const SeqView& v, int unit, int elem_bytes)
-{
-    return aligned(v.p, (uintptr_t)(unit * elem_bytes)) && v.env % unit == 0 && v.step % unit == 0 &&
-           v.head % unit == 0;
-}
-
 // The bytes that one access to a row of `dim` elements may take, in load8.
 template <class D>
 void set_vec(SeqView& v, int dim)

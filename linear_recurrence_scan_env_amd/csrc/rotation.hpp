@@ -134,6 +134,184 @@ __global__ __launch_bounds__(kNormWaves * kWave) void norm_rotation(const NormAr
     }
 }
 
+// The same for rows on 16 bytes, by lanes that hold one 16-byte unit of V
+// elements each: G lanes (a power of two) span a row, so a wave holds 64 / G
+// rows.  They are heads of one token where it has that many, else of a few
+// consecutive tokens; a lane keeps its columns' weights, and its token's angles
+// for all the heads that it walks over, in registers.  Each wave walks over
+// consecutive tokens of its own.  With kNormAhead rows in flight per lane the
+// loads are what bounds it.
+template <class D>
+constexpr int kUnit = 16 / sizeof(D);
+constexpr int kNormAhead = 4;
+
+template <class D>
+__device__ __forceinline__ void unpack(const u32x4& w, float (&v)[kUnit<D>])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(D) == 4) v[k] = __uint_as_float(w[k]);
+        else unpack2<D>(w[k], v[2 * k], v[2 * k + 1]);
+    }
+}
+template <class D>
+__device__ __forceinline__ u32x4 pack(const float (&v)[kUnit<D>])
+{
+    u32x4 w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(D) == 4) w[k] = __float_as_uint(v[k]);
+        else w[k] = pack2<D>(v[2 * k], v[2 * k + 1]);
+    }
+    return w;
+}
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp_add(float v)
+{
+    const int i = __builtin_bit_cast(int, v);
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, kCtrl, 0xf, 0xf, true));
+}
+
+// The sum over the G lanes of a row, in each of them.
+template <int G>
+__device__ __forceinline__ float row_sum(float v)
+{
+    if constexpr (G >= 2) v = dpp_add<0xb1>(v);    // quad_perm 1 0 3 2
+    if constexpr (G >= 4) v = dpp_add<0x4e>(v);    // quad_perm 2 3 0 1
+    if constexpr (G >= 8) v = dpp_add<0x141>(v);   // row_half_mirror
+    if constexpr (G >= 16) v = dpp_add<0x140>(v);  // row_mirror
+    if constexpr (G >= 32) v += __shfl_xor(v, 16);
+    if constexpr (G >= 64) v += __shfl_xor(v, 32);
+    return v;
+}
+
+template <class D, int G, bool kPairs, bool kBackward>
+__global__ __launch_bounds__(kNormWaves * kWave) void norm_rotation_wide(const NormArgs x)
+{
+    constexpr int V = kUnit<D>, kRows = kWave / G;
+    __shared__ float sums[kBackward ? kNormWaves : 1][kBackward ? G * V : 1];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const bool keys = blockIdx.x >= x.side[0].blocks;
+    const NormSide& s = x.side[keys ? 1 : 0];
+    const uint32_t block = keys ? blockIdx.x - x.side[0].blocks : blockIdx.x;
+    const int c = (lane & (G - 1)) * V, half = x.rot / 2;
+    const bool in_dim = c < x.dim, turned = c < x.rot;
+    // heads side by side, then tokens
+    int across = 1;
+    while (across < kRows && across < s.heads) across <<= 1;
+    const int tokens = kRows / across, sub = lane / G / across, h0 = lane / G % across;
+    const int64_t waves = (int64_t)s.blocks * kNormWaves, all = x.N * x.T;
+    const int64_t per = ((all + waves - 1) / waves + tokens - 1) / tokens * tokens;
+    const int64_t begin = (block * (int64_t)kNormWaves + wave) * per;
+    const int64_t end = begin + per < all ? begin + per : all;
+
+    float w[V], dw[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        w[e] = in_dim ? to_f32(static_cast<const D*>(s.w)[c + e]) : 0.0f;
+        dw[e] = 0.0f;
+    }
+    const float share = 1.0f / (float)x.dim;
+    const int mate = kPairs ? lane : lane + (c < half ? half : -half) / V;
+
+    int64_t n = (begin + sub) / x.T, t = (begin + sub) % x.T;
+    for (int64_t tok = begin + sub; tok - sub < end; tok += tokens) {
+        const bool live = tok < end && in_dim;
+        float cos[V], sin[V];  // of a lane's elements, the sign of its part in the sine
+        bool known = true;
+        if (x.rot > 0) {
+            const int64_t p = live ? *seq_row<int32_t>(x.positions, n, t, 0) : 0;
+            known = p >= 0 && p < x.max_positions;
+            const float* const angle = x.table + (known ? p : 0) * x.rot;
+            const int j = turned ? (kPairs ? c / 2 : (c < half ? c : c - half)) : 0;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int k = kPairs ? j + e / 2 : j + e;
+                cos[e] = turned ? angle[k] : 1.0f;
+                const float si = turned ? angle[half + k] : 0.0f;
+                const bool first = kPairs ? e % 2 == 0 : c < half;
+                sin[e] = first != kBackward ? -si : si;
+            }
+        }
+        const D* const xs = seq_row<D>(s.x, n, t, 0);
+        const D* const gs = kBackward ? seq_row<D>(s.dy, n, t, 0) : nullptr;
+        D* const ys = seq_row_out<D>(s.y, n, t, 0);
+        for (int h = h0; h - h0 < s.heads; h += across * kNormAhead) {
+            u32x4 raw[kNormAhead], grad[kNormAhead];
+#pragma unroll
+            for (int a = 0; a < kNormAhead; ++a) {
+                raw[a] = grad[a] = u32x4{};
+                if (live && h + a * across < s.heads) {
+                    raw[a] = *reinterpret_cast<const u32x4*>(xs + (h + a * across) * s.x.head + c);
+                    if (kBackward) grad[a] = *reinterpret_cast<const u32x4*>(gs + (h + a * across) * s.dy.head + c);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < kNormAhead; ++a) {
+                if (h - h0 + a * across >= s.heads) break;  // (the wave's)
+                float v[V], u[V], sum = 0.0f;
+                unpack<D>(raw[a], v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum = fmaf(v[e], v[e], sum);
+                const float scale = rsqrtf(row_sum<G>(sum) * share + x.eps);
+                if constexpr (kBackward) unpack<D>(grad[a], u);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    v[e] *= scale;
+                    if constexpr (!kBackward) u[e] = v[e] * w[e];
+                }
+                if (x.rot > 0) {
+                    float z[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) z[e] = kPairs ? u[e ^ 1] : __shfl(u[e], mate);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) u[e] = turned ? fmaf(u[e], cos[e], sin[e] * z[e]) : u[e];
+                }
+                if (!known) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) u[e] = __builtin_nanf("");
+                }
+                if constexpr (kBackward) {
+                    float dot = 0.0f;
+                    const bool mine = live && h + a * across < s.heads;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        if (mine) dw[e] = fmaf(u[e], v[e], dw[e]);
+                        u[e] *= w[e];
+                        dot = fmaf(u[e], v[e], dot);
+                    }
+                    dot = row_sum<G>(dot) * share;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) u[e] = scale * (u[e] - v[e] * dot);
+                }
+                if (live && h + a * across < s.heads)
+                    *reinterpret_cast<u32x4*>(ys + (h + a * across) * s.y.head + c) = pack<D>(u);
+            }
+        }
+        t += tokens;
+        while (t >= x.T) {
+            t -= x.T;
+            ++n;
+        }
+    }
+    if constexpr (kBackward) {
+        // over the rows of a wave, then the waves of the block
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int o = G; o < kWave; o <<= 1) dw[e] += __shfl_xor(dw[e], o);
+            if (lane < G) sums[wave][c + e] = dw[e];
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < x.dim; e += kNormWaves * kWave) {
+            float sum = 0.0f;
+            for (int k = 0; k < kNormWaves; ++k) sum += sums[k][e];
+            s.part[(int64_t)block * x.dim + e] = sum;
+        }
+    }
+}
+
 // dw from the blocks' sums, in a fixed order: one block per element of dim.
 struct WeightSumArgs {
     const float* part[2];
@@ -191,6 +369,31 @@ inline uint32_t norm_blocks(int64_t rows, uint32_t most)
     return (uint32_t)(b < (int64_t)most ? b : (int64_t)most);
 }
 
+// The kernel: 16-byte units where the rows allow them (and rotated pairs lie in
+// whole units), with as many lanes to a row as it has units.
+template <class D, bool kBackward>
+lrs_status launch_norm(const char* nm, const NormArgs& x, hipStream_t stream)
+{
+    constexpr int V = kUnit<D>, s = sizeof(D);
+    bool wide = x.dim % V == 0 && (x.interleaved ? x.rot % V == 0 : x.rot % (2 * V) == 0);
+    for (const NormSide& side : x.side)
+        wide = wide && rows_on(side.x, V, s) && rows_on(side.y, V, s) &&
+               (!kBackward || rows_on(side.dy, V, s));
+    void (*kernel)(NormArgs) = norm_rotation<D, kBackward>;
+    if (wide) {
+#define LRS_NORM(G) \
+    (x.interleaved ? norm_rotation_wide<D, G, true, kBackward> : norm_rotation_wide<D, G, false, kBackward>)
+        const int units = x.dim / V;
+        if (units <= 4) kernel = LRS_NORM(4);
+        else if (units <= 8) kernel = LRS_NORM(8);
+        else if (units <= 16) kernel = LRS_NORM(16);
+        else if (units <= 32) kernel = LRS_NORM(32);
+        else if constexpr (s == 4) kernel = LRS_NORM(64);
+#undef LRS_NORM
+    }
+    return launch_seq(nm, kernel, (uint64_t)x.side[0].blocks + x.side[1].blocks, kNormWaves * kWave, stream, x);
+}
+
 inline size_t norm_workspace(int64_t N, int64_t T, int64_t HQ, int64_t HK, int64_t dim)
 {
     return ((size_t)norm_blocks(N * T * HQ, kNormMaxBlocksGrad) +
@@ -230,8 +433,7 @@ lrs_status norm_rotation_entry(const char* nm, int64_t N, int64_t T, int64_t HQ,
     x.rot = (int32_t)rot;
     x.eps = eps;
     x.interleaved = interleaved;
-    return launch_seq(nm, norm_rotation<D, false>, x.side[0].blocks + x.side[1].blocks,
-                      kNormWaves * kWave, stream, x);
+    return launch_norm<D, false>(nm, x, stream);
 }
 
 template <class D>
@@ -276,7 +478,7 @@ lrs_status norm_rotation_backward_entry(const char* nm, int64_t N, int64_t T, in
     x.rot = (int32_t)rot;
     x.eps = eps;
     x.interleaved = interleaved;
-    LRS_TRY(launch_seq(nm, norm_rotation<D, true>, (uint64_t)bq + bk, kNormWaves * kWave, stream, x));
+    LRS_TRY((launch_norm<D, true>(nm, x, stream)));
     const WeightSumArgs sum{{x.side[0].part, x.side[1].part}, {grad_qw, grad_kw}, {bq, bk}, (int32_t)dim};
     return launch_seq(nm, weight_sum<D>, (uint64_t)(2 * dim), 256, stream, sum);
 }

@@ -115,6 +115,13 @@ inline lrs_status check_workspace(const char* nm, size_t need, const void* ws, s
     return LRS_OK;
 }
 
+// Whether every row starts on a multiple of `unit` elements.
+inline bool rows_on(const SeqView& v, int unit, int elem_bytes)
+{
+    return aligned(v.p, (uintptr_t)(unit * elem_bytes)) && v.env % unit == 0 && v.step % unit == 0 &&
+           v.head % unit == 0;
+}
+
 // Launches `kernel` and returns the launch's own status.
 template <class... P>
 lrs_status launch_seq(const char* nm, void (*kernel)(P...), uint64_t blocks, int threads,
