@@ -86,11 +86,21 @@ __device__ __forceinline__ int64_t state_at(const PassArgs& p, int r, int c)
 // is split as far as its result needs.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 template <class D>
 constexpr int kLimbs = std::is_same<D, bf16_t>::value ? 1 : std::is_same<D, f16_t>::value ? 2 : 3;
+
+// Tiles of 16 columns that a wave holds of the state (W: its padded dimension,
+// 64 or 128), and the threads of a block.  Two tiles halve the reads of the
+// shared fragments per product; one tile leaves room for twice the waves, which
+// is worth more where several limbs fill LDS and registers: 4096 x 128, f16,
+// 439 us with two and 338 with one; 32768 steps of bf16, W = 128, 219 and 271.
+template <class D, int W>
+constexpr int kCols = W == 128 && kLimbs<D> == 1 ? 2 : 1;
+template <class D, int W>
+constexpr int kThreads = 4 * W / kCols<D, W>;
 
 template <int L>
 struct Frag {
@@ -123,6 +133,12 @@ __device__ __forceinline__ f32x4 mma(const Frag<LA>& a, const Frag<LB>& b, f32x4
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x[i], b.x[j], acc, 0, 0, 0);
     return acc;
 }
+
+// What a wave holds of the state, and the columns of c that go with it.
+template <class D, int W>
+using StateTiles = f32x4[W / 16][kCols<D, W>];
+template <class D, int W>
+using ColumnFrags = Frag<kLimbs<D>>[2][kCols<D, W>];
 
 // A tile of kChunk steps of up to W elements in LDS, one plane per limb.  Rows
 // are an odd number of 16-byte units long, and the rows of each 16 are laid out
@@ -241,9 +257,8 @@ struct Rows {
     }
 };
 
-// A block of 2 W threads moves 64 steps of one head's array into a tile in two
-// halves: fetch() starts the loads (four of a thread's 16-byte units, 16 steps
-// apart), put() writes what arrived to LDS, zero beyond dim.  Steps beyond
+// A block moves 64 steps of one head's array into a tile in two halves: fetch()
+// starts the loads (of a thread's 16-byte units), put() writes what arrived to LDS, zero beyond dim.  Steps beyond
 // `count` read the last one again: their weights are zero.  kWide: every row is
 // on 16 bytes and dim a multiple of 8, and 64 steps lie within 2 GiB, so that
 // one 32-bit offset per lane and access is all the addressing there is; nothing
@@ -251,15 +266,16 @@ struct Rows {
 // the branches join.
 template <class D, int W, bool kWide>
 struct Staged {
-    Raw8<D> r[4];
+    static constexpr int kUnits = 2 * kCols<D, W>, kApart = kChunk / kUnits;
+    Raw8<D> r[kUnits];
 
     __device__ __forceinline__ void fetch(const Rows<D>& rows, int64_t t, int count)
     {
         const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
         const D* const from = rows.p + t * rows.step;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int at_row = min(row + 16 * k, count - 1);
+        for (int k = 0; k < kUnits; ++k) {
+            const int at_row = min(row + kApart * k, count - 1);
             if constexpr (kWide) {
                 const uint32_t at = (uint32_t)at_row * (uint32_t)rows.step + (c < rows.dim ? c : 0);
 #pragma unroll
@@ -276,12 +292,12 @@ struct Staged {
     {
         const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kUnits; ++k) {
             if (kWide && rows.dim < W) {
                 const Raw8<D> v = c < rows.dim ? r[k] : Raw8<D>{};
-                put8<D, W>(tile, tile.at(row, c) + 16 * k * tile.kRow, v);
+                put8<D, W>(tile, tile.at(row, c) + kApart * k * tile.kRow, v);
             } else {
-                put8<D, W>(tile, tile.at(row, c) + 16 * k * tile.kRow, r[k]);
+                put8<D, W>(tile, tile.at(row, c) + kApart * k * tile.kRow, r[k]);
             }
         }
     }
@@ -395,20 +411,20 @@ constexpr int kStateLimbs(bool exact)
 }
 
 template <int LW, class D, int W>
-__device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<W, kLimbs<D>>& tb,
-                                          const Frag<kLimbs<D>> (&fc)[2][2], const float* w, float total,
+__device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W, kLimbs<D>>& tb,
+                                          const ColumnFrags<D, W>& fc, const float* w, float total,
                                           float scale, int da, int lane)
 {
-    constexpr int L = kLimbs<D>;
+    constexpr int L = kLimbs<D>, U = kCols<D, W>;
     const int group = lane >> 4;
-    Frag<LW> fw[2][2];
+    Frag<LW> fw[2][U];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const f32x4 lo = *reinterpret_cast<const f32x4*>(&w[b * 32 + group * 4]);
         const f32x4 hi = *reinterpret_cast<const f32x4*>(&w[b * 32 + 16 + group * 4]);
         const f32x8 v8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * scale;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
             f32x8 v = __builtin_convertvector(fc[b][u].x[0], f32x8);
 #pragma unroll
             for (int l = 1; l < L; ++l) v += __builtin_convertvector(fc[b][u].x[l], f32x8);
@@ -421,7 +437,7 @@ __device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<
         if (k * 16 >= da) break;
         const Frag<L> fb[2] = {tb.columns(0, k * 16, lane), tb.columns(32, k * 16, lane)};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
             f32x4 v = S[k][u] * f;
 #pragma unroll
             for (int b = 0; b < 2; ++b) v = mma(fb[b], fw[b][u], v);
@@ -430,7 +446,7 @@ __device__ __forceinline__ void add_chunk(f32x4 (&S)[W / 16][2], const StepTile<
     }
 }
 
-// A pass by matrix instructions, 64 steps at a time.  A wave holds 32 columns
+// A pass by matrix instructions, 64 steps at a time.  A wave holds 16 or 32 columns
 // of the state, all its rows, in accumulators; the block's waves share the
 // steps, and the products a b^T of which each computes its part, in LDS.  Per
 // chunk, with X, Z the weights from the chunk's start and to its end in scan
@@ -447,8 +463,8 @@ struct PassShared {
     StepTile<W, kLimbs<D>> a, b, c;
     StepTile<64, LS> own_ab[kOverlay ? 0 : 1];
     ChunkDecay decay;
-    float dot[W / 32][kChunk];
-    float cross[W / 32];
+    float dot[W / 16][kChunk];
+    float cross[W / 16];
 
     __device__ __forceinline__ StepTile<64, LS>& ab()
     {
@@ -474,29 +490,44 @@ __device__ __forceinline__ void store4(D* row, int c, int dim, bool vec, f32x4 v
     }
 }
 template <class D>
-__device__ __forceinline__ f32x4 load4(const D* row, int c, int dim, bool vec)
+struct alignas(4 * sizeof(D)) Raw4 {
+    uint32_t w[sizeof(D)];
+};
+template <class D>
+__device__ __forceinline__ Raw4<D> load4(const D* row, int c, int dim, bool vec)
 {
-    f32x4 v = {};
+    Raw4<D> v = {};
     if (vec) {
-        if (c >= dim) return v;
-        if constexpr (sizeof(D) == 4) {
-            v = *reinterpret_cast<const f32x4*>(row + c);
-        } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(row + c);
+        v = *reinterpret_cast<const Raw4<D>*>(row + (c < dim ? c : 0));
+        if (c >= dim) v = Raw4<D>{};
+    } else if constexpr (sizeof(D) == 4) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float lo, hi;
-                unpack2<D>(w[k], lo, hi);
-                v[2 * k] = lo;
-                v[2 * k + 1] = hi;
-            }
-        }
+        for (int r = 0; r < 4; ++r)
+            if (c + r < dim) v.w[r] = __float_as_uint(row[c + r]);
     } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            if (c + r < dim) v[r] = to_f32(row[c + r]);
+            if (c + r < dim) v.w[r / 2] |= (uint32_t)row[c + r].bits << (16 * (r & 1));
     }
     return v;
+}
+template <class D>
+__device__ __forceinline__ f32x4 unpack4(const Raw4<D>& v)
+{
+    f32x4 f;
+    if constexpr (sizeof(D) == 4) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[r] = __uint_as_float(v.w[r]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float lo, hi;
+            unpack2<D>(v.w[k], lo, hi);
+            f[2 * k] = lo;
+            f[2 * k + 1] = hi;
+        }
+    }
+    return f;
 }
 
 // Limbs of a b^T and of the state as operands: as many as the inputs have, and
@@ -512,7 +543,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                                          PassShared<D, W, LS>& sh)
 {
     constexpr int L = kLimbs<D>;
-    constexpr int K = W / 32, kWaves = W / 32;
+    constexpr int K = W / 32, U = kCols<D, W>, kWaves = W / 16 / U;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int group = lane >> 4, col = lane & 15;
@@ -520,7 +551,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     const int seg = (int)(block % x.segments);
     const int64_t n = head / x.H;
     const int h = (int)(head % x.H);
-    const int c0 = wave * 32;
+    const int c0 = wave * 16 * kCols<D, W>;
     const int64_t at = (int64_t)block * p.da * p.dc;
     const int64_t first = seg * x.seg_len;
     const int64_t steps = x.T - first < x.seg_len ? x.T - first : x.seg_len;
@@ -546,14 +577,14 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     };
     fetch(0);
 
-    // S[2 k + s][u][r]: row 32 k + 16 s + 4 group + r, column c0 + 16 u + col; a state that
-    // the first step drops is not read, whatever it holds
+    // S[k][u][r]: row 16 k + 4 group + r, column c0 + 16 u + col; a state that the first step drops is
+    // not read, whatever it holds
     const float* const init = p.init == nullptr || (!back && decays.cut(0)) ? nullptr : p.init;
-    f32x4 S[2 * K][2];
+    StateTiles<D, W> S;
 #pragma unroll
     for (int k = 0; k < 2 * K; ++k)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
@@ -571,29 +602,33 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
         __syncthreads();
         if (i + 1 < chunks) fetch(i + 1);
 
-        // the wave's strips of a b^T, weighted: tile s has rows (steps of b) 16 s + 4 group + r,
+        // the wave's tiles of a b^T, weighted: tile j has rows (steps of b) 16 s + 4 group + r and
         // columns (steps of a) 16 q + col; only one side of the diagonal is not zero
-        f32x4 ab[4 / kWaves][4];
+        constexpr int kParts = kWaves / 4;
+        const int q0 = wave % 4;
+        f32x4 ab[4 / kParts];
+        {
+            const int step = q0 * 16 + col;
 #pragma unroll
-        for (int j = 0; j < 4 / kWaves; ++j) {
-            const int q = j == 0 ? wave : 3 - wave;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) ab[j][s] = f32x4{};
+            for (int j = 0; j < 4 / kParts; ++j) ab[j] = f32x4{};
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (k * 32 >= p.da) break;
-                const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
+                const Frag<L> fa = sh.a.rows(q0 * 16, k * 32, lane);
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    if (back ? s >= q : s <= q) ab[j][s] = mma(sh.b.rows(s * 16, k * 32, lane), fa, ab[j][s]);
+                for (int j = 0; j < 4 / kParts; ++j) {
+                    const int s = j * kParts + wave / 4;
+                    if (back ? s >= q0 : s <= q0) ab[j] = mma(sh.b.rows(s * 16, k * 32, lane), fa, ab[j]);
+                }
             }
-            const int step = q * 16 + col;
             const float mine = (back ? sh.decay.tail : sh.decay.head)[step] * p.p_scale;
             const double pi = sh.decay.p[step];
             const int mi = sh.decay.m[step];
+            const float* const theirs = back ? sh.decay.head : sh.decay.tail;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (s == q) {
+            for (int j = 0; j < 4 / kParts; ++j) {
+                const int s = j * kParts + wave / 4;
+                if (s == q0) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int o = s * 16 + group * 4 + r;
@@ -601,99 +636,95 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                         const bool in = (back ? o >= step : o <= step) && sh.decay.m[o] == mi;
                         // (the exponential of -infinity is 0; no branch)
                         const float w = __builtin_amdgcn_exp2f(in ? d : -INFINITY) * p.p_scale;
-                        ab[j][s][r] = in ? ab[j][s][r] * w : 0.0f;
+                        ab[j][r] = in ? ab[j][r] * w : 0.0f;
                     }
-                } else if (back ? s > q : s < q) {
-                    const float* const theirs = back ? sh.decay.head : sh.decay.tail;
-                    ab[j][s] *= *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]) *
-                                (mine * sh.decay.between[q][s]);
+                } else if (back ? s > q0 : s < q0) {
+                    ab[j] *= *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]) *
+                             (mine * sh.decay.between[q0][s]);
                 }
             }
         }
 
         // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col
-        f32x4 y[4][2] = {};
+        f32x4 y[4][U] = {};
         if (c0 < p.dc) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (k * 32 >= p.da) break;
-                Frag<LS> s[2];
+                Frag<LS> s[U];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < U; ++u)
                     s[u] = split<LS>(__builtin_shufflevector(S[2 * k][u], S[2 * k + 1][u], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) y[q][u] = mma(s[u], fa, y[q][u]);
+                    for (int u = 0; u < U; ++u) y[q][u] = mma(s[u], fa, y[q][u]);
                 }
             }
         }
         if constexpr (PassShared<D, W, LS>::kOverlay) __syncthreads();
+        {
+            StepTile<64, LS>& to = sh.ab();
 #pragma unroll
-        for (int j = 0; j < 4 / kWaves; ++j) {
-            const int q = j == 0 ? wave : 3 - wave;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const Frag<LS> f =
-                    split<LS>(__builtin_shufflevector(ab[j][2 * b], ab[j][2 * b + 1], 0, 1, 2, 3, 4, 5, 6, 7));
-                StepTile<64, LS>& to = sh.ab();
+            for (int j = 0; j < 4 / kParts; ++j) {
+                const int here = to.at(col, group * 4) + q0 * 16 * to.kRow + (j * kParts + wave / 4) * 16;
+                f32x4 v = ab[j];
 #pragma unroll
                 for (int l = 0; l < LS; ++l) {
-                    const s16x8 e = __builtin_bit_cast(s16x8, f.x[l]);
-                    const int here = to.at(col, group * 4) + q * 16 * to.kRow + b * 32;
-                    *reinterpret_cast<s16x4*>(&to.e[l][here]) = __builtin_shufflevector(e, e, 0, 1, 2, 3);
-                    *reinterpret_cast<s16x4*>(&to.e[l][here + 16]) = __builtin_shufflevector(e, e, 4, 5, 6, 7);
+                    const bf16x4 e = __builtin_convertvector(v, bf16x4);
+                    *reinterpret_cast<bf16x4*>(&to.e[l][here]) = e;
+                    if (l + 1 < LS) v -= __builtin_convertvector(e, f32x4);
                 }
             }
         }
         __syncthreads();
 
         if (c0 < p.dc) {
-            f32x4 d[4][2];
+            Raw4<D> d[4][U];
             if constexpr (kPrecise)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 4; ++q) {
+                    const int step = min(q * 16 + col, count - 1);
+                    const D* const row = kWide ? rd.p + done * rd.step + (uint32_t)step * (uint32_t)rd.step
+                                               : rd.p + (done + step) * rd.step;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        d[q][u] = load4<D>(kWide ? rd.p + done * rd.step + (uint32_t)min(q * 16 + col, count - 1) *
-                                                                               (uint32_t)rd.step
-                                                 : rd.p + (done + min(q * 16 + col, count - 1)) * rd.step,
-                                           c0 + u * 16 + group * 4, p.dc, kWide || rd.vec != 0);
-            Frag<L> fc[2][2];  // columns c0 + 16 u + l % 16 of 32 steps each
+                    for (int u = 0; u < U; ++u)
+                        d[q][u] = load4<D>(row, c0 + u * 16 + group * 4, p.dc, kWide || rd.vec != 0);
+                }
+            ColumnFrags<D, W> fc;  // columns c0 + 16 u + l % 16 of 32 steps each
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
+                for (int u = 0; u < U; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
             const float* const from = back ? sh.decay.exit : sh.decay.entry;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float in = from[q * 16 + col];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) y[q][u] *= in;
+                for (int u = 0; u < U; ++u) y[q][u] *= in;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     if (back ? 2 * b + 1 < q : 2 * b > q) continue;
                     const Frag<LS> f = sh.ab().rows(q * 16, b * 32, lane);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) y[q][u] = mma(fc[b][u], f, y[q][u]);
+                    for (int u = 0; u < U; ++u) y[q][u] = mma(fc[b][u], f, y[q][u]);
                 }
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int step = q * 16 + col;
                 float dot = 0.0f;
+                char* const to = kWide ? y_chunk + (uint32_t)step * (uint32_t)y_step : y_chunk + step * y_step;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < U; ++u) {
                     const int c = c0 + u * 16 + group * 4;
                     const f32x4 v = y[q][u] * p.y_scale;
                     if constexpr (kPrecise) {
-                        const f32x4 e = d[q][u] * v;
+                        const f32x4 e = unpack4<D>(d[q][u]) * v;
                         dot += (e[0] + e[1]) + (e[2] + e[3]);
                     }
                     if (step < count) {
-                        char* const to = kWide ? y_chunk + (uint32_t)step * (uint32_t)y_step
-                                               : y_chunk + step * y_step;
                         if (y_f32)
                             store4<float>(reinterpret_cast<float*>(to), c, p.dc, kWide || p.y.vec != 0, v);
                         else
@@ -713,7 +744,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
         __syncthreads();
         if (kPrecise && wave == 0 && lane < count) {
             float sum = 0.0f;
-            for (int w = 0; w * 32 < p.dc; ++w) sum += sh.dot[w][lane];
+            for (int w = 0; w * 16 * U < p.dc; ++w) sum += sh.dot[w][lane];
             p.dot[head * x.T + first + done + lane] = sum;
         }
     }
@@ -723,7 +754,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
     for (int k = 0; k < 2 * K; ++k)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
@@ -744,12 +775,12 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     }
 }
 
-// Two waves per SIMD where the steps' tiles leave room in LDS for them.
-template <class D>
-constexpr int kPassWaves = kLimbs<D> == 1 ? 2 : 1;
+// Waves per SIMD: as many blocks as LDS holds the steps' tiles of.
+template <class D, int W>
+constexpr int kPassWaves = W == 128 ? 2 : 4 - kLimbs<D>;
 
 template <class D, int W, bool kWide, bool kExact>
-__global__ __launch_bounds__(2 * W, kPassWaves<D>) void recurrence_forward(const RecurrenceArgs x)
+__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_forward(const RecurrenceArgs x)
 {
     constexpr int LS = kOperandLimbs<D>(false);
     __shared__ PassShared<D, W, LS> sh;
@@ -759,7 +790,7 @@ __global__ __launch_bounds__(2 * W, kPassWaves<D>) void recurrence_forward(const
 // The three passes of the backward call: dq and dk with q.dq and k.dk to a
 // precision that their differences keep, and dv.
 template <class D, int W, bool kWide, bool kExact>
-__global__ __launch_bounds__(2 * W, kPassWaves<D>) void recurrence_backward(const RecurrenceArgs x)
+__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_backward(const RecurrenceArgs x)
 {
     constexpr int LS = kOperandLimbs<D>(true), LV = kOperandLimbs<D>(false);
     __shared__ union {
@@ -775,7 +806,7 @@ __global__ __launch_bounds__(2 * W, kPassWaves<D>) void recurrence_backward(cons
 // The state that one segment alone leaves (from zero), and its decay, by the
 // same products; the last segment in scan order leaves none that is used.
 template <class D, int W, bool kWide, bool kExact>
-__global__ __launch_bounds__(2 * W, kPassWaves<D>) void segment_states(const RecurrenceArgs x)
+__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_states(const RecurrenceArgs x)
 {
     __shared__ struct {
         StepTile<W, kLimbs<D>> b, c;
@@ -792,10 +823,11 @@ __global__ __launch_bounds__(2 * W, kPassWaves<D>) void segment_states(const Rec
     const int next = back ? seg - 1 : seg + 1;
     const int64_t n = head / x.H;
     const int h = (int)(head % x.H);
-    const int c0 = wave * 32;
+    const int c0 = wave * 16 * kCols<D, W>;
     const int64_t first = seg * x.seg_len;
     const int64_t steps = x.T - first < x.seg_len ? x.T - first : x.seg_len;
-    f32x4 S[W / 16][2] = {};
+    constexpr int U = kCols<D, W>;
+    StateTiles<D, W> S = {};
     float total = 1.0f;
     const int chunks = (int)((steps + kChunk - 1) / kChunk);
     const Rows<D> rb(p.b, n, first, h, p.da), rc(p.c, n, first, h, p.dc);
@@ -819,11 +851,11 @@ __global__ __launch_bounds__(2 * W, kPassWaves<D>) void segment_states(const Rec
         __syncthreads();
         if (i + 1 < chunks) fetch(i + 1);
         if (c0 >= p.dc) continue;
-        Frag<kLimbs<D>> fc[2][2];
+        ColumnFrags<D, W> fc;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
+            for (int u = 0; u < U; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
         add_chunk<kStateLimbs<D>(kExact), D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit,
                                                 sh.decay.total, p.u_scale, p.da, lane);
         total *= sh.decay.total;
@@ -832,7 +864,7 @@ __global__ __launch_bounds__(2 * W, kPassWaves<D>) void segment_states(const Rec
 #pragma unroll
     for (int k = 0; k < W / 16; ++k)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
@@ -1126,7 +1158,7 @@ lrs_status launch_carries(const char* nm, RecurrenceArgs& x, bool wide, bool exa
     }
     const int da = x.carry[0].da, dc = x.carry[0].dc, widest = std::max(da, dc);
     const uint64_t heads = (uint64_t)x.N * x.H, blocks = heads * (x.segments - 1) * x.carries;
-    LRS_TRY(launch_seq(nm, LRS_PICK(segment_states, D, widest, wide, exact), blocks, widest <= 64 ? 128 : 256, stream, x));
+    LRS_TRY(launch_seq(nm, LRS_PICK(segment_states, D, widest, wide, exact), blocks, (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x));
     return launch_seq(nm, join_segments<D>, (heads * da * dc + 255) / 256 * x.carries, 256, stream, x);
 }
 
@@ -1184,7 +1216,7 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     const bool exact = final_state != nullptr;
     LRS_TRY(launch_carries<D>(nm, x, wide, exact, stream));
     return launch_seq(nm, LRS_PICK(recurrence_forward, D, widest, wide, exact), (uint64_t)(N * H * plan.segments),
-                      widest <= 64 ? 128 : 256, stream, x);
+                      (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x);
 }
 
 template <class D>
@@ -1293,7 +1325,7 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     const bool exact = grad_initial != nullptr;
     LRS_TRY(launch_carries<D>(nm, x, wide, exact, stream));
     LRS_TRY(launch_seq(nm, LRS_PICK(recurrence_backward, D, widest, wide, exact), (uint64_t)(N * H * plan.segments) * 3,
-                       widest <= 64 ? 128 : 256, stream, x));
+                       (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x));
     DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, plan.seg_len, (int32_t)H,
                      (int32_t)plan.segments};
     LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H * plan.segments), 64, stream, dg));
