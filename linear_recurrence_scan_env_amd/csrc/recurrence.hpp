@@ -37,8 +37,8 @@ constexpr int kMaxDim = 128;  // largest key and value dimension
 // side by side.  init: each segment's state before its first step in scan order,
 // [N, H, segments, key_dim, value_dim] (nullable for one segment); last: where
 // the state after the last segment goes, [N, H, key_dim, value_dim], nullable.
-// y_scale multiplies y, p_scale the products a . b, u_scale what enters the
-// state.  dot (nullable): receives y_i . d_i per [N, H, T]; cross (nullable):
+// y_scale multiplies what y has of the state, p_scale what it has of the products
+// a . b, u_scale what enters the state.  dot (nullable): receives y_i . d_i per [N, H, T]; cross (nullable):
 // <state after the segment, meet> per [N, H, segments], meet like init.
 struct PassArgs {
     SeqView a, b, c, d, y;
@@ -96,7 +96,7 @@ constexpr int kLimbs = std::is_same<D, bf16_t>::value ? 1 : std::is_same<D, f16_
 // 64 or 128), and the threads of a block.  Two tiles halve the reads of the
 // shared fragments per product; one tile leaves room for twice the waves, which
 // is worth more where several limbs fill LDS and registers: 4096 x 128, f16,
-// 439 us with two and 338 with one; 32768 steps of bf16, W = 128, 219 and 271.
+// 439 us with two and 338 with one; 32768 steps of bf16, W = 128, 204 and 239.
 template <class D, int W>
 constexpr int kCols = W == 128 && kLimbs<D> == 1 ? 2 : 1;
 template <class D, int W>
@@ -107,16 +107,53 @@ struct Frag {
     bf16x8 x[L];
 };
 
+// The limbs of two values, each a packed pair.
+template <int L>
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t (&w)[L])
+{
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        w[l] = pack2<bf16_t>(v0, v1);
+        if (l + 1 < L) {
+            v0 -= __uint_as_float(w[l] << 16);
+            v1 -= __uint_as_float(w[l] & 0xffff0000u);
+        }
+    }
+}
+
 template <int L>
 __device__ __forceinline__ Frag<L> split(f32x8 v)
 {
+    u32x4 x[L];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t w[L];
+        split2<L>(v[2 * k], v[2 * k + 1], w);
+#pragma unroll
+        for (int l = 0; l < L; ++l) x[l][k] = w[l];
+    }
     Frag<L> f;
 #pragma unroll
-    for (int l = 0; l < L; ++l) {
-        f.x[l] = __builtin_convertvector(v, bf16x8);
-        if (l + 1 < L) v -= __builtin_convertvector(f.x[l], f32x8);
-    }
+    for (int l = 0; l < L; ++l) f.x[l] = __builtin_bit_cast(bf16x8, x[l]);
     return f;
+}
+
+// The values of a fragment.
+template <int L>
+__device__ __forceinline__ f32x8 joined(const Frag<L>& f)
+{
+    f32x8 v;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        const u32x4 w = __builtin_bit_cast(u32x4, f.x[l]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+            v[2 * k] = l == 0 ? lo : v[2 * k] + lo;
+            v[2 * k + 1] = l == 0 ? hi : v[2 * k + 1] + hi;
+        }
+    }
+    return v;
 }
 
 // acc += A^T B over 32 products per lane group, all limb products down to the
@@ -138,14 +175,18 @@ __device__ __forceinline__ f32x4 mma(const Frag<LA>& a, const Frag<LB>& b, f32x4
 template <class D, int W>
 using StateTiles = f32x4[W / 16][kCols<D, W>];
 template <class D, int W>
-using ColumnFrags = Frag<kLimbs<D>>[2][kCols<D, W>];
+using ColumnFrags = Frag<kLimbs<D>>[kCols<D, W>];
 
-// A tile of kChunk steps of up to W elements in LDS, one plane per limb.  Rows
-// are an odd number of 16-byte units long, and the rows of each 16 are laid out
-// 0, 8, 1, 9, ..., so that both ways of reading a fragment (16 rows at one
-// unit; 8 rows at two neighbouring units, transposed) touch every bank once,
-// at addresses that differ from lane to lane by one offset only.
-constexpr int kChunk = 64;
+// A tile of kChunk steps of up to W elements in LDS, one plane per limb.  The 32
+// values that a matrix instruction sums over are taken in order, eight to a
+// group of 16 lanes, by both operands.  Rows are an odd number of 16-byte units
+// long, and the rows of each 16 are laid out 0, 4, 1, 5, ... and 8 below, so
+// that a fragment by rows (16 rows at one unit) and one by columns (rows 0..3
+// and 8..11 at two neighbouring units, transposed) touch every bank once; and
+// every fragment lies at a constant distance from one address per lane, which
+// is worth registers: pairs of 8-byte reads, whose distances are limited, took
+// 40 registers of addresses.
+constexpr int kChunk = 32;
 constexpr int kTile = 16;
 
 template <int W, int L>
@@ -155,40 +196,42 @@ struct StepTile {
 
     static __device__ __forceinline__ int at(int row, int col)
     {
-        return ((row & ~15) | ((row & 7) << 1) | ((row >> 3) & 1)) * kRow + col;
+        return ((row & ~15) | (row & 8) | ((row & 3) << 1) | ((row >> 2) & 1)) * kRow + col;
     }
     // A fragment of 16 rows (from `row`) over 32 columns (from `col`): lane l
-    // holds row l % 16, columns 4 (l / 16) + 0..3 and 16 more.  Both operands
-    // of every product use this order of the 32.
+    // holds row l % 16, columns 8 (l / 16) + 0..7.
     __device__ __forceinline__ Frag<L> rows(int row, int col, int lane) const
     {
-        const int mine = at(lane & 15, (lane >> 4) * 4), to = row * kRow + col;
+        const int mine = at(lane & 15, (lane >> 4) * 8), to = row * kRow + col;
         Frag<L> f;
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-            const s16x4 lo = *reinterpret_cast<const s16x4*>(&e[l][mine + to]);
-            const s16x4 hi = *reinterpret_cast<const s16x4*>(&e[l][mine + to + 16]);
-            f.x[l] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
+        for (int l = 0; l < L; ++l) f.x[l] = *reinterpret_cast<const bf16x8*>(&e[l][mine + to]);
         return f;
     }
-    // The transposed fragment: lane l holds column col + l % 16 of the rows
-    // row + 4 (l / 16) + 0..3 and 16 more.  A transposing read hands the 16
-    // lanes of a group four rows of 16 columns, 8 bytes read by each lane.
+    // The transposed fragment over the 32 rows from `row`: lane l holds rows
+    // 8 (l / 16) + 0..7 of column col + l % 16, or, kEights, of column
+    // col + 8 (l % 16 / 4) + l % 4 (with col and col + 4 a pair that covers 32
+    // columns in eights).  A transposing read hands the 16 lanes of a group
+    // four rows of four groups of 4 columns, 8 bytes read by each lane.
+    template <bool kEights = false>
     __device__ __forceinline__ Frag<L> columns(int row, int col, int lane) const
     {
-        const int mine = at((lane >> 4) * 4 + ((lane & 15) >> 2), (lane & 3) * 4), to = row * kRow + col;
+        const int mine = at((lane >> 4) * 8 + ((lane & 15) >> 2), (lane & 3) * (kEights ? 8 : 4));
+        const int to = row * kRow + col, four = at(4, 0);
         Frag<L> f;
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][mine + to]);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][mine + to + 16 * kRow]);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)&e[l][mine + to + four]);
             f.x[l] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
         return f;
     }
 };
+
+// The rows of the state that a wave holds in tile k: four from here on.
+__device__ __forceinline__ int state_row(int k, int group) { return (k >> 1) * 32 + group * 8 + (k & 1) * 4; }
 
 // Eight elements of a row from column c on as they are stored, zero beyond
 // `dim`; `vec`: the bytes that an access may take (16, 4 or one element).
@@ -257,16 +300,16 @@ struct Rows {
     }
 };
 
-// A block moves 64 steps of one head's array into a tile in two halves: fetch()
+// A block moves a chunk of one head's array into a tile in two halves: fetch()
 // starts the loads (of a thread's 16-byte units), put() writes what arrived to LDS, zero beyond dim.  Steps beyond
 // `count` read the last one again: their weights are zero.  kWide: every row is
-// on 16 bytes and dim a multiple of 8, and 64 steps lie within 2 GiB, so that
+// on 16 bytes and dim a multiple of 8, and a chunk lies within 2 GiB, so that
 // one 32-bit offset per lane and access is all the addressing there is; nothing
 // then branches around the loads, which would make the wave wait for them where
 // the branches join.
 template <class D, int W, bool kWide>
 struct Staged {
-    static constexpr int kUnits = 2 * kCols<D, W>, kApart = kChunk / kUnits;
+    static constexpr int kApart = kThreads<D, W> / (W / 8), kUnits = kChunk / kApart;
     Raw8<D> r[kUnits];
 
     __device__ __forceinline__ void fetch(const Rows<D>& rows, int64_t t, int count)
@@ -291,23 +334,122 @@ struct Staged {
     __device__ __forceinline__ void put(StepTile<W, kLimbs<D>>& tile, const Rows<D>& rows) const
     {
         const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+        if (!kWide || c < rows.dim)
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            if (kWide && rows.dim < W) {
-                const Raw8<D> v = c < rows.dim ? r[k] : Raw8<D>{};
-                put8<D, W>(tile, tile.at(row, c) + kApart * k * tile.kRow, v);
-            } else {
-                put8<D, W>(tile, tile.at(row, c) + kApart * k * tile.kRow, r[k]);
-            }
-        }
+            for (int k = 0; k < kUnits; ++k) put8<D, W>(tile, tile.at(row, c) + kApart * k * tile.kRow, r[k]);
+    }
+    // The columns beyond dim, once: put() leaves them alone where kWide.
+    static __device__ __forceinline__ void clear(StepTile<W, kLimbs<D>>& tile, const Rows<D>& rows)
+    {
+        const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+        if (kWide && c >= rows.dim)
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k)
+                put8<D, W>(tile, tile.at(row, c) + kApart * k * tile.kRow, Raw8<D>{});
     }
 };
 
-// The decays of a chunk of 64 steps, in four tiles of 16.  With p the running
+// A chunk's results on their way from the accumulators to memory by whole rows:
+// put() leaves a wave's part in LDS, 16-bit values in one plane of a tile, fp32
+// ones by halves in two; take() reads what the thread itself will overwrite by
+// its next Staged::put(), and store() writes it out.  Stores go out before the
+// next loads start: the wait for the loads would otherwise be one for the
+// stores as well, which are slower to be acknowledged (a pass of 32768 steps of
+// 16 heads took 150 us where they came between).
+template <class D, int W, bool kWide>
+struct Result {
+    static constexpr int kUnits = Staged<D, W, kWide>::kUnits, kApart = Staged<D, W, kWide>::kApart;
+    using Tile = StepTile<W, kLimbs<D>>;
+    u32x4 lo[kUnits], hi[sizeof(D) == 4 ? kUnits : 1];
+
+    static __device__ __forceinline__ void put(uint16_t* low, uint16_t* high, int at, f32x4 v, bool f32)
+    {
+        if (f32) {
+            const uint32_t w[4] = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                   __float_as_uint(v[3])};
+            *reinterpret_cast<u32x2*>(&low[at]) = u32x2{__builtin_amdgcn_perm(w[1], w[0], 0x05040100),
+                                                        __builtin_amdgcn_perm(w[3], w[2], 0x05040100)};
+            *reinterpret_cast<u32x2*>(&high[at]) = u32x2{__builtin_amdgcn_perm(w[1], w[0], 0x07060302),
+                                                         __builtin_amdgcn_perm(w[3], w[2], 0x07060302)};
+        } else if constexpr (sizeof(D) == 2) {
+            *reinterpret_cast<u32x2*>(&low[at]) = u32x2{pack2<D>(v[0], v[1]), pack2<D>(v[2], v[3])};
+        }
+    }
+    // Elements c .. c + 7 of a row of `dim` from w.
+    template <class E>
+    static __device__ __forceinline__ void store8(char* to, const Raw8<E>& v, int c, int dim, int vec)
+    {
+        to += c * (int)sizeof(E);
+        if (kWide || (vec == 16 && c + 8 <= dim)) {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(E) / 2; ++j) reinterpret_cast<u32x4*>(to)[j] = v.w[j];
+        } else if (sizeof(E) == 4 || vec >= 4) {
+            constexpr int per = 4 / sizeof(E);
+#pragma unroll
+            for (int j = 0; j < 8 / per; ++j)
+                if (c + per * j < dim) reinterpret_cast<uint32_t*>(to)[j] = v.w[j / 4][j % 4];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < dim)
+                    reinterpret_cast<uint16_t*>(to)[j] = (uint16_t)(v.w[0][j / 2] >> (16 * (j & 1)));
+        }
+    }
+    __device__ __forceinline__ void take(const uint16_t* low, const uint16_t* high)
+    {
+        const int at = Tile::at(threadIdx.x / (W / 8), threadIdx.x % (W / 8) * 8);
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            lo[k] = *reinterpret_cast<const u32x4*>(&low[at + kApart * k * Tile::kRow]);
+            if constexpr (sizeof(D) == 4) hi[k] = *reinterpret_cast<const u32x4*>(&high[at + kApart * k * Tile::kRow]);
+        }
+    }
+    __device__ __forceinline__ void store(char* y, int64_t step, int count, int dim, int vec) const
+    {
+        const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+        if (c >= dim) return;
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const int at = row + kApart * k;
+            if (at >= count) continue;
+            char* const to = kWide ? y + (uint32_t)at * (uint32_t)step : y + at * step;
+            if constexpr (sizeof(D) == 4) store8<float>(to, both(lo[k], hi[k]), c, dim, vec);
+            else store8<D>(to, Raw8<D>{{lo[k]}}, c, dim, vec);
+        }
+    }
+    // take() and store() of fp32 results where D is not fp32, in one.
+    static __device__ __forceinline__ void move(const uint16_t* low, const uint16_t* high, char* y, int64_t step,
+                                                int count, int dim, int vec)
+    {
+        const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+        const int at = Tile::at(row, c);
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const u32x4 l = *reinterpret_cast<const u32x4*>(&low[at + kApart * k * Tile::kRow]);
+            const u32x4 h = *reinterpret_cast<const u32x4*>(&high[at + kApart * k * Tile::kRow]);
+            if (c < dim && row + kApart * k < count)
+                store8<float>(kWide ? y + (uint32_t)(row + kApart * k) * (uint32_t)step
+                                    : y + (row + kApart * k) * step,
+                              both(l, h), c, dim, vec);
+        }
+    }
+    static __device__ __forceinline__ Raw8<float> both(const u32x4& l, const u32x4& h)
+    {
+        Raw8<float> v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v.w[j / 2][j % 2 * 2] = __builtin_amdgcn_perm(h[j], l[j], 0x05040100);
+            v.w[j / 2][j % 2 * 2 + 1] = __builtin_amdgcn_perm(h[j], l[j], 0x07060302);
+        }
+        return v;
+    }
+};
+
+// The decays of a chunk of 32 steps, in two tiles of 16.  With p the running
 // sum of log2 decays within a tile (in 64 bits: a strong decay before a weak
 // one would cost an fp32 sum the weak one's digits) and m the running count of
 // its cuts, for steps j < i of one tile D(i, j) = 2^(p_i - p_j) where m_i =
-// m_j, and for steps of tiles B > A, D(i, j) = head_i (tiles between) tail_j,
+// m_j, and for steps of the second and the first tile D(i, j) = head_i tail_j,
 // where each factor is at most 1 for log decays up to 0.
 struct ChunkDecay {
     double p[kChunk];
@@ -316,7 +458,6 @@ struct ChunkDecay {
     float tail[kChunk];   // from this step, exclusive, to the end of its tile
     float entry[kChunk];  // from the start of the chunk, inclusive
     float exit[kChunk];   // to the end of the chunk
-    float between[4][4];  // of the tiles between two
     float total;          // of the chunk
 };
 
@@ -354,53 +495,62 @@ struct DecayRows {
     }
 };
 
+// The value of the lane kShift below in the row of 16 lanes, `none` where there
+// is none (a register move: the reads of a shuffle through LDS would be a chunk's
+// longest chain).
+template <int kShift>
+__device__ __forceinline__ int row_below(int v, int none)
+{
+    return __builtin_amdgcn_update_dpp(none, v, 0x110 + kShift, 0xf, 0xf, false);
+}
+template <int kShift>
+__device__ __forceinline__ void row_scan(double& p, int& m)
+{
+    const uint64_t bits = __builtin_bit_cast(uint64_t, p);
+    const uint32_t lo = row_below<kShift>((int)(uint32_t)bits, 0), hi = row_below<kShift>((int)(bits >> 32), 0);
+    p += __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    m += row_below<kShift>(m, 0);
+}
+
 __device__ __forceinline__ void chunk_decay(ChunkDecay& s, float g, int count, int lane)
 {
     const bool in = lane < count;
     int m = in && g == -INFINITY;
     double p = m || !in ? 0.0 : (double)g * 1.4426950408889634;
-    const int i = lane & 15;
+    static_assert(kTile == 16, "rows of 16 lanes");
+    row_scan<1>(p, m);
+    row_scan<2>(p, m);
+    row_scan<4>(p, m);
+    row_scan<8>(p, m);
+    const bool second = lane >= kTile;
+    const uint64_t bits = __builtin_bit_cast(uint64_t, p);
+    double ptot[2];
+    int mtot[2];
+    float w[2];
 #pragma unroll
-    for (int o = 1; o < kTile; o <<= 1) {
-        const double q = __shfl_up(p, o);
-        const int k = __shfl_up(m, o);
-        if (i >= o) {
-            p += q;
-            m += k;
-        }
+    for (int k = 0; k < 2; ++k) {
+        const int end = k * kTile + kTile - 1;
+        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)bits, end);
+        const uint32_t hi = __builtin_amdgcn_readlane((int)(bits >> 32), end);
+        ptot[k] = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+        mtot[k] = __builtin_amdgcn_readlane(m, end);
+        w[k] = mtot[k] ? 0.0f : __builtin_amdgcn_exp2f((float)ptot[k]);
     }
-    const double ptot = __shfl(p, lane | 15);
-    const int mtot = __shfl(m, lane | 15);
     const float head = m ? 0.0f : __builtin_amdgcn_exp2f((float)p);
-    const float tail = m != mtot ? 0.0f : __builtin_amdgcn_exp2f((float)(ptot - p));
-    const float whole = mtot ? 0.0f : __builtin_amdgcn_exp2f((float)ptot);
-    float w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = __shfl(whole, k * kTile);
-    const int tile = lane >> 4;
-    float before = 1.0f, after = 1.0f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (k < tile) before *= w[k];
-        if (k > tile) after *= w[k];
+    const float tail =
+        m != (second ? mtot[1] : mtot[0]) ? 0.0f : __builtin_amdgcn_exp2f((float)((second ? ptot[1] : ptot[0]) - p));
+    if (lane < kChunk) {
+        s.p[lane] = p;
+        s.m[lane] = in ? m : -1;  // steps beyond the end have no part in anything
+        s.head[lane] = in ? head : 0.0f;
+        s.tail[lane] = in ? tail : 0.0f;
+        s.entry[lane] = in ? (second ? w[0] * head : head) : 0.0f;
+        s.exit[lane] = in ? (second ? tail : w[1] * tail) : 0.0f;
     }
-    s.p[lane] = p;
-    s.m[lane] = in ? m : -1;  // steps beyond the end have no part in anything
-    s.head[lane] = in ? head : 0.0f;
-    s.tail[lane] = in ? tail : 0.0f;
-    s.entry[lane] = in ? before * head : 0.0f;
-    s.exit[lane] = in ? after * tail : 0.0f;
-    if (lane < 16) {
-        float f = 1.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if ((k > (lane & 3)) != (k >= (lane >> 2)) && k != (lane & 3) && k != (lane >> 2)) f *= w[k];
-        s.between[lane >> 2][lane & 3] = f;
-    }
-    if (lane == 0) s.total = w[0] * w[1] * w[2] * w[3];
+    if (lane == 0) s.total = w[0] * w[1];
 }
 
-// S = total S + b^T (w c) over a chunk of 64 steps; w: the weight of each step,
+// S = total S + b^T (w c) over a chunk; w: the weight of each step,
 // fc: the wave's columns of c.  The weighted c is fp32: two limbs keep 16 of its
 // bits, enough for what is made of S in 16-bit results and their differences; a
 // state that is itself a result takes a third (LW = 3, all 24).
@@ -417,36 +567,23 @@ __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W,
 {
     constexpr int L = kLimbs<D>, U = kCols<D, W>;
     const int group = lane >> 4;
-    Frag<LW> fw[2][U];
+    Frag<LW> fw[U];
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(&w[group * 8]);
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(&w[group * 8 + 4]);
+    const f32x8 w8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * scale;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(&w[b * 32 + group * 4]);
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(&w[b * 32 + 16 + group * 4]);
-        const f32x8 v8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * scale;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            f32x8 v = __builtin_convertvector(fc[b][u].x[0], f32x8);
-#pragma unroll
-            for (int l = 1; l < L; ++l) v += __builtin_convertvector(fc[b][u].x[l], f32x8);
-            fw[b][u] = split<LW>(v * v8);
-        }
-    }
+    for (int u = 0; u < U; ++u) fw[u] = split<LW>(joined<L>(fc[u]) * w8);
     const float f = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, total)));
 #pragma unroll
     for (int k = 0; k < W / 16; ++k) {
-        if (k * 16 >= da) break;
-        const Frag<L> fb[2] = {tb.columns(0, k * 16, lane), tb.columns(32, k * 16, lane)};
+        if (state_row(k, 0) >= da) break;  // (da: W where the whole width is to be unrolled)
+        const Frag<L> fb = tb.template columns<true>(0, state_row(k, 0), lane);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            f32x4 v = S[k][u] * f;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) v = mma(fb[b], fw[b][u], v);
-            S[k][u] = v;
-        }
+        for (int u = 0; u < U; ++u) S[k][u] = mma(fb, fw[u], S[k][u] * f);
     }
 }
 
-// A pass by matrix instructions, 64 steps at a time.  A wave holds 16 or 32 columns
+// A pass by matrix instructions, 32 steps at a time.  A wave holds 16 or 32 columns
 // of the state, all its rows, in accumulators; the block's waves share the
 // steps, and the products a b^T of which each computes its part, in LDS.  Per
 // chunk, with X, Z the weights from the chunk's start and to its end in scan
@@ -454,41 +591,19 @@ __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W,
 //     y^T = S^T a^T X + c^T (D o (a b^T))^T        (S before the chunk)
 //     S   = total S + b^T (Z c)
 // Results of a product leave the matrix unit with 4 consecutive rows of one of
-// 16 columns per lane, and operands are read in that order of their summed
-// index, so S feeds the next product from the registers that it is kept in.
+// 16 columns per lane; a wave's tiles of S take their rows in fours of every 8,
+// so that two of them are an operand and S feeds the next product from the
+// registers that it is kept in.
 template <class D, int W, int LS>
 struct PassShared {
-    // the products take a's place where LDS does not hold both
-    static constexpr bool kOverlay = 3 * sizeof(StepTile<W, kLimbs<D>>) + sizeof(StepTile<64, LS>) > 160000;
     StepTile<W, kLimbs<D>> a, b, c;
-    StepTile<64, LS> own_ab[kOverlay ? 0 : 1];
-    ChunkDecay decay;
+    StepTile<kChunk, LS> ab;
+    ChunkDecay decays[2];  // this chunk's, and the next one's as it is made
     float dot[W / 16][kChunk];
     float cross[W / 16];
-
-    __device__ __forceinline__ StepTile<64, LS>& ab()
-    {
-        return kOverlay ? *reinterpret_cast<StepTile<64, LS>*>(&a) : own_ab[0];
-    }
 };
 
-// Four elements of a row from column c on, out of `dim` (one access where the
-// row allows it).
-template <class D>
-__device__ __forceinline__ void store4(D* row, int c, int dim, bool vec, f32x4 v)
-{
-    if (vec) {
-        if (c >= dim) return;
-        if constexpr (sizeof(D) == 4)
-            *reinterpret_cast<f32x4*>(row + c) = v;
-        else
-            *reinterpret_cast<u32x2*>(row + c) = u32x2{pack2<D>(v[0], v[1]), pack2<D>(v[2], v[3])};
-    } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (c + r < dim) row[c + r] = from_f32<D>(v[r]);
-    }
-}
+// Four elements of a row from column c on, out of `dim`.
 template <class D>
 struct alignas(4 * sizeof(D)) Raw4 {
     uint32_t w[sizeof(D)];
@@ -566,18 +681,37 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     char* const y_base = y_f32 ? reinterpret_cast<char*>(seq_row_out<float>(p.y, n, first, h))
                                : reinterpret_cast<char*>(seq_row_out<D>(p.y, n, first, h));
     const int64_t y_step = p.y.step * y_bytes;
+    // where results wait in LDS: a wave's own columns of c, and for the high halves of fp32 ones
+    // a second plane, or a where there is none (a is not read any more then)
+    uint16_t* const low = sh.c.e[0];
+    uint16_t* const high = L > 1 ? sh.c.e[L > 1 ? 1 : 0] : sh.a.e[0];
+    const bool f32 = sizeof(D) == 4 || y_f32;
     Staged<D, W, kWide> ga, gb, gc;
     const auto fetch = [&](int i) {
         const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
         const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
-        decays.fetch(done, count, lane);
         ga.fetch(ra, done, count);
         gb.fetch(rb, done, count);
         gc.fetch(rc, done, count);
     };
+    // the decays are loaded two chunks ahead, and made ready one ahead
+    const auto fetch_decay = [&](int i) {
+        const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
+        decays.fetch(done, (int)(steps - done < kChunk ? steps - done : kChunk), lane);
+    };
+    const auto make_decay = [&](int i) {
+        const int64_t left = steps - (int64_t)(back ? chunks - 1 - i : i) * kChunk;
+        chunk_decay(sh.decays[i & 1], decays.value(), (int)(left < kChunk ? left : kChunk), lane);
+    };
+    fetch_decay(0);
     fetch(0);
+    Staged<D, W, kWide>::clear(sh.a, ra);
+    Staged<D, W, kWide>::clear(sh.b, rb);
+    Staged<D, W, kWide>::clear(sh.c, rc);
+    if (wave == 0) make_decay(0);
+    if (chunks > 1) fetch_decay(1);
 
-    // S[k][u][r]: row 16 k + 4 group + r, column c0 + 16 u + col; a state that the first step drops is
+    // S[k][u][r]: row state_row(k) + r, column c0 + 16 u + col; a state that the first step drops is
     // not read, whatever it holds
     const float* const init = p.init == nullptr || (!back && decays.cut(0)) ? nullptr : p.init;
     StateTiles<D, W> S;
@@ -587,149 +721,133 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
+                const int row = state_row(k, group) + r, c = c0 + u * 16 + col;
                 S[k][u][r] = init && row < p.da && c < p.dc ? init[at + state_at(p, row, c)] : 0.0f;
             }
 
+    Result<D, W, kWide> result;
+    // what chunk i left in LDS: results, and the waves' parts of the dot products
+    const auto finish = [&](int i) {
+        const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
+        const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
+        if (sizeof(D) == 4 || !y_f32) result.store(y_base + done * y_step, y_step, count, p.dc, p.y.vec);
+        if (kPrecise && wave == 0 && lane < count) {
+            float sum = 0.0f;
+            for (int w = 0; w * 16 * U < p.dc; ++w) sum += sh.dot[w][lane];
+            p.dot[head * x.T + first + done + lane] = sum;
+        }
+    };
+    const auto take = [&](int i) {
+        if (sizeof(D) == 4 || !y_f32) {
+            result.take(low, high);
+        } else {
+            const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
+            Result<D, W, kWide>::move(low, high, y_base + done * y_step, y_step,
+                                      (int)(steps - done < kChunk ? steps - done : kChunk), p.dc, p.y.vec);
+            Staged<D, W, kWide>::clear(sh.a, ra);
+        }
+    };
     for (int i = 0; i < chunks; ++i) {
         const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
         const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
-        char* const y_chunk = y_base + done * y_step;
+        if (i > 0) take(i - 1);
         ga.put(sh.a, ra);
         gb.put(sh.b, rb);
         gc.put(sh.c, rc);
-        if (wave == 0) chunk_decay(sh.decay, decays.value(), count, lane);
         __syncthreads();
-        if (i + 1 < chunks) fetch(i + 1);
-
-        // the wave's tiles of a b^T, weighted: tile j has rows (steps of b) 16 s + 4 group + r and
-        // columns (steps of a) 16 q + col; only one side of the diagonal is not zero
-        constexpr int kParts = kWaves / 4;
-        const int q0 = wave % 4;
-        f32x4 ab[4 / kParts];
-        {
-            const int step = q0 * 16 + col;
+        if (i > 0) finish(i - 1);
+        const ChunkDecay& decay = sh.decays[i & 1];
+        Raw4<D> d[2][U];
+        if constexpr (kPrecise)
 #pragma unroll
-            for (int j = 0; j < 4 / kParts; ++j) ab[j] = f32x4{};
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (k * 32 >= p.da) break;
-                const Frag<L> fa = sh.a.rows(q0 * 16, k * 32, lane);
-#pragma unroll
-                for (int j = 0; j < 4 / kParts; ++j) {
-                    const int s = j * kParts + wave / 4;
-                    if (back ? s >= q0 : s <= q0) ab[j] = mma(sh.b.rows(s * 16, k * 32, lane), fa, ab[j]);
-                }
-            }
-            const float mine = (back ? sh.decay.tail : sh.decay.head)[step] * p.p_scale;
-            const double pi = sh.decay.p[step];
-            const int mi = sh.decay.m[step];
-            const float* const theirs = back ? sh.decay.head : sh.decay.tail;
-#pragma unroll
-            for (int j = 0; j < 4 / kParts; ++j) {
-                const int s = j * kParts + wave / 4;
-                if (s == q0) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int o = s * 16 + group * 4 + r;
-                        const float d = (float)(back ? sh.decay.p[o] - pi : pi - sh.decay.p[o]);
-                        const bool in = (back ? o >= step : o <= step) && sh.decay.m[o] == mi;
-                        // (the exponential of -infinity is 0; no branch)
-                        const float w = __builtin_amdgcn_exp2f(in ? d : -INFINITY) * p.p_scale;
-                        ab[j][r] = in ? ab[j][r] * w : 0.0f;
-                    }
-                } else if (back ? s > q0 : s < q0) {
-                    ab[j] *= *reinterpret_cast<const f32x4*>(&theirs[s * 16 + group * 4]) *
-                             (mine * sh.decay.between[q0][s]);
-                }
-            }
-        }
-
-        // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col
-        f32x4 y[4][U] = {};
-        if (c0 < p.dc) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (k * 32 >= p.da) break;
-                Frag<LS> s[U];
+            for (int q = 0; q < 2; ++q) {
+                const int step = min(q * 16 + col, count - 1);
+                const D* const row = kWide ? rd.p + done * rd.step + (uint32_t)step * (uint32_t)rd.step
+                                           : rd.p + (done + step) * rd.step;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    s[u] = split<LS>(__builtin_shufflevector(S[2 * k][u], S[2 * k + 1][u], 0, 1, 2, 3, 4, 5, 6, 7));
+                    d[q][u] = load4<D>(row, c0 + u * 16 + group * 4, p.dc, kWide || rd.vec != 0);
+            }
+        if (i + 1 < chunks) {
+            fetch(i + 1);
+            // by the wave whose tile below is zero
+            if (wave == (back ? 1 : 2)) make_decay(i + 1);
+            if (i + 2 < chunks) fetch_decay(i + 2);
+        }
+
+        // a tile of a b^T for each of four waves: rows (steps of b) 16 s0 + 4 group + r, columns
+        // (steps of a) 16 q0 + col.  One of them lies on the side of the diagonal that is zero; it
+        // is computed too, since branches around products make a wave wait for each read of LDS.
+        const int q0 = wave & 1, s0 = (wave >> 1) & 1;
+        f32x4 ab = {};
+        // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col
+        f32x4 y[2][U];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const Frag<L> fa = sh.a.rows(q * 16, k * 32, lane);
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int u = 0; u < U; ++u) y[q][u] = mma(s[u], fa, y[q][u]);
-                }
+            for (int u = 0; u < U; ++u) y[q][u] = f32x4{};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (!kWide && k * 32 >= p.da) break;
+            if (kWaves == 4 || wave < 4)
+                ab = mma(sh.b.rows(s0 * 16, k * 32, lane), sh.a.rows(q0 * 16, k * 32, lane), ab);
+            Frag<LS> s[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                s[u] = split<LS>(__builtin_shufflevector(S[2 * k][u], S[2 * k + 1][u], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const Frag<L> f = sh.a.rows(q * 16, k * 32, lane);
+#pragma unroll
+                for (int u = 0; u < U; ++u) y[q][u] = mma(s[u], f, y[q][u]);
             }
         }
-        if constexpr (PassShared<D, W, LS>::kOverlay) __syncthreads();
-        {
-            StepTile<64, LS>& to = sh.ab();
+        if (kWaves == 4 || wave < 4) {
+            const int step = q0 * 16 + col, o = s0 * 16 + group * 4;
+            if (s0 == q0) {
+                const double pi = decay.p[step];
+                const int mi = decay.m[step];
 #pragma unroll
-            for (int j = 0; j < 4 / kParts; ++j) {
-                const int here = to.at(col, group * 4) + q0 * 16 * to.kRow + (j * kParts + wave / 4) * 16;
-                f32x4 v = ab[j];
-#pragma unroll
-                for (int l = 0; l < LS; ++l) {
-                    const bf16x4 e = __builtin_convertvector(v, bf16x4);
-                    *reinterpret_cast<bf16x4*>(&to.e[l][here]) = e;
-                    if (l + 1 < LS) v -= __builtin_convertvector(e, f32x4);
+                for (int r = 0; r < 4; ++r) {
+                    const float d = (float)(back ? decay.p[o + r] - pi : pi - decay.p[o + r]);
+                    const bool in = (back ? o + r >= step : o + r <= step) && decay.m[o + r] == mi;
+                    // (plus 0 or minus infinity: a choice of values would become a branch)
+                    ab[r] *= __builtin_amdgcn_exp2f(d + (in ? 0.0f : -INFINITY)) * p.p_scale;
                 }
+            } else {
+                const bool in_order = back ? s0 > q0 : s0 < q0;
+                const float mine = in_order ? (back ? decay.tail : decay.head)[step] * p.p_scale : 0.0f;
+                ab *= *reinterpret_cast<const f32x4*>(&(back ? decay.head : decay.tail)[o]) * mine;
             }
+            const int here = sh.ab.at(col, group * 4) + q0 * 16 * sh.ab.kRow + s0 * 16;
+            uint32_t lo[LS], hi[LS];
+            split2<LS>(ab[0], ab[1], lo);
+            split2<LS>(ab[2], ab[3], hi);
+#pragma unroll
+            for (int l = 0; l < LS; ++l) *reinterpret_cast<u32x2*>(&sh.ab.e[l][here]) = u32x2{lo[l], hi[l]};
         }
         __syncthreads();
 
-        if (c0 < p.dc) {
-            Raw4<D> d[4][U];
-            if constexpr (kPrecise)
+        if (kWide || c0 < p.dc) {
+            ColumnFrags<D, W> fc;  // columns c0 + 16 u + l % 16
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int step = min(q * 16 + col, count - 1);
-                    const D* const row = kWide ? rd.p + done * rd.step + (uint32_t)step * (uint32_t)rd.step
-                                               : rd.p + (done + step) * rd.step;
+            for (int u = 0; u < U; ++u) fc[u] = sh.c.columns(0, c0 + u * 16, lane);
+            const float* const from = back ? decay.exit : decay.entry;
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        d[q][u] = load4<D>(row, c0 + u * 16 + group * 4, p.dc, kWide || rd.vec != 0);
-                }
-            ColumnFrags<D, W> fc;  // columns c0 + 16 u + l % 16 of 32 steps each
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int u = 0; u < U; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
-            const float* const from = back ? sh.decay.exit : sh.decay.entry;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float in = from[q * 16 + col];
-#pragma unroll
-                for (int u = 0; u < U; ++u) y[q][u] *= in;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (back ? 2 * b + 1 < q : 2 * b > q) continue;
-                    const Frag<LS> f = sh.ab().rows(q * 16, b * 32, lane);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) y[q][u] = mma(fc[b][u], f, y[q][u]);
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 const int step = q * 16 + col;
+                const float in = from[step] * p.y_scale;
+                const Frag<LS> f = sh.ab.rows(q * 16, 0, lane);
                 float dot = 0.0f;
-                char* const to = kWide ? y_chunk + (uint32_t)step * (uint32_t)y_step : y_chunk + step * y_step;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int c = c0 + u * 16 + group * 4;
-                    const f32x4 v = y[q][u] * p.y_scale;
+                    const f32x4 v = mma(fc[u], f, y[q][u] * in);
                     if constexpr (kPrecise) {
                         const f32x4 e = unpack4<D>(d[q][u]) * v;
                         dot += (e[0] + e[1]) + (e[2] + e[3]);
                     }
-                    if (step < count) {
-                        if (y_f32)
-                            store4<float>(reinterpret_cast<float*>(to), c, p.dc, kWide || p.y.vec != 0, v);
-                        else
-                            store4<D>(reinterpret_cast<D*>(to), c, p.dc, kWide || p.y.vec != 0, v);
-                    }
+                    Result<D, W, kWide>::put(low, high,
+                                             sh.c.at(col, c0 + u * 16 + group * 4) + q * 16 * sh.c.kRow, v, f32);
                 }
                 if constexpr (kPrecise) {
                     dot += __shfl_xor(dot, 16);
@@ -738,16 +856,13 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 }
             }
             // the state after the chunk
-            add_chunk<LW, D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit, sh.decay.total, p.u_scale,
-                                p.da, lane);
+            add_chunk<LW, D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, decay.total, p.u_scale,
+                                kWide ? W : p.da, lane);
         }
         __syncthreads();
-        if (kPrecise && wave == 0 && lane < count) {
-            float sum = 0.0f;
-            for (int w = 0; w * 16 * U < p.dc; ++w) sum += sh.dot[w][lane];
-            p.dot[head * x.T + first + done + lane] = sum;
-        }
     }
+    take(chunks - 1);
+    finish(chunks - 1);
 
     if (p.last == nullptr && p.cross == nullptr) return;
     float v = 0.0f;
@@ -757,7 +872,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
+                const int row = state_row(k, group) + r, c = c0 + u * 16 + col;
                 if (row >= p.da || c >= p.dc) continue;
                 if (p.last && seg == (back ? 0 : x.segments - 1))
                     p.last[head * p.da * p.dc + state_at(p, row, c)] = S[k][u][r];
@@ -775,9 +890,10 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     }
 }
 
-// Waves per SIMD: as many blocks as LDS holds the steps' tiles of.
+// Waves per SIMD that leave enough registers for nothing to spill: a reload in
+// the loop waits for every load before it, the next chunk's among them.
 template <class D, int W>
-constexpr int kPassWaves = W == 128 ? 2 : 4 - kLimbs<D>;
+constexpr int kPassWaves = W == 128 || kLimbs<D> == 3 ? 2 : 4;
 
 template <class D, int W, bool kWide, bool kExact>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_forward(const RecurrenceArgs x)
@@ -810,7 +926,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
 {
     __shared__ struct {
         StepTile<W, kLimbs<D>> b, c;
-        ChunkDecay decay;
+        ChunkDecay decays[2];
     } sh;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -836,29 +952,41 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
     const auto fetch = [&](int i) {
         const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
         const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
-        decays.fetch(done, count, lane);
         gb.fetch(rb, done, count);
         gc.fetch(rc, done, count);
     };
-    fetch(0);
-    for (int i = 0; i < chunks; ++i) {
+    const auto fetch_decay = [&](int i) {
+        const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
+        decays.fetch(done, (int)(steps - done < kChunk ? steps - done : kChunk), lane);
+    };
+    const auto make_decay = [&](int i) {
         const int64_t left = steps - (int64_t)(back ? chunks - 1 - i : i) * kChunk;
-        const int count = (int)(left < kChunk ? left : kChunk);
+        chunk_decay(sh.decays[i & 1], decays.value(), (int)(left < kChunk ? left : kChunk), lane);
+    };
+    fetch_decay(0);
+    fetch(0);
+    Staged<D, W, kWide>::clear(sh.b, rb);
+    Staged<D, W, kWide>::clear(sh.c, rc);
+    if (wave == 0) make_decay(0);
+    if (chunks > 1) fetch_decay(1);
+    for (int i = 0; i < chunks; ++i) {
         if (i > 0) __syncthreads();
         gb.put(sh.b, rb);
         gc.put(sh.c, rc);
-        if (wave == 0) chunk_decay(sh.decay, decays.value(), count, lane);
         __syncthreads();
-        if (i + 1 < chunks) fetch(i + 1);
-        if (c0 >= p.dc) continue;
+        const ChunkDecay& decay = sh.decays[i & 1];
+        if (i + 1 < chunks) {
+            fetch(i + 1);
+            if (wave == i % (kThreads<D, W> / kWave)) make_decay(i + 1);
+            if (i + 2 < chunks) fetch_decay(i + 2);
+        }
+        total *= decay.total;
+        if (!kWide && c0 >= p.dc) continue;
         ColumnFrags<D, W> fc;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int u = 0; u < U; ++u) fc[b][u] = sh.c.columns(b * 32, c0 + u * 16, lane);
-        add_chunk<kStateLimbs<D>(kExact), D, W>(S, sh.b, fc, back ? sh.decay.entry : sh.decay.exit,
-                                                sh.decay.total, p.u_scale, p.da, lane);
-        total *= sh.decay.total;
+        for (int u = 0; u < U; ++u) fc[u] = sh.c.columns(0, c0 + u * 16, lane);
+        add_chunk<kStateLimbs<D>(kExact), D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, decay.total,
+                                                p.u_scale, kWide ? W : p.da, lane);
     }
     float* const to = p.states + (head * x.segments + next) * (int64_t)p.da * p.dc;
 #pragma unroll
@@ -867,10 +995,9 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = k * 16 + group * 4 + r, c = c0 + u * 16 + col;
+                const int row = state_row(k, group) + r, c = c0 + u * 16 + col;
                 if (row < p.da && c < p.dc) to[(int64_t)row * p.dc + c] = S[k][u][r];
             }
-    // (wave 0 always has columns, and with them the whole decay)
     if (threadIdx.x == 0) p.totals[head * x.segments + seg] = total;
 }
 
@@ -1069,6 +1196,7 @@ inline size_t round_up(size_t b) { return (b + 255) & ~size_t(255); }
 // direction; backward also q.dq and k.dk [N, H, T], <S, dS> [N, H, segments]
 // and, for shared query and key heads, each value head's dq and dk.
 constexpr int64_t kFillBlocks = 512;
+constexpr int64_t kFillBlocksBackward = 1024;
 constexpr int64_t kMinSegment = 256;
 
 struct RecurrencePlan {
@@ -1081,8 +1209,9 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
 {
     RecurrencePlan p{};
     const int64_t heads = N * H * (backward ? 3 : 1);
-    int64_t parts = std::min((kFillBlocks + heads - 1) / heads, (T + kMinSegment - 1) / kMinSegment);
-    if (heads >= kFillBlocks) parts = 1;
+    const int64_t fill = backward ? kFillBlocksBackward : kFillBlocks;
+    int64_t parts = std::min((fill + heads - 1) / heads, (T + kMinSegment - 1) / kMinSegment);
+    if (heads >= fill) parts = 1;
     p.seg_len = ((T + parts - 1) / parts + kChunk - 1) / kChunk * kChunk;
     p.segments = (T + p.seg_len - 1) / p.seg_len;
     size_t at = 0;
@@ -1117,7 +1246,7 @@ void set_vec(SeqView& v, int dim)
     v.vec = rows_on(v, 16 / s, s) && dim % 8 == 0 ? 16 : rows_on(v, 4 / s, s) && dim % (4 / s) == 0 ? 4 : s;
 }
 
-// Whether one 32-bit offset reaches 64 steps of the array.
+// Whether one 32-bit offset reaches a chunk of the array.
 inline bool steps_near(const SeqView& v)
 {
     return v.step <= (int64_t(1) << 31) / (kChunk * 4) - kMaxDim;
@@ -1133,8 +1262,9 @@ bool set_vec(PassArgs& p)
         wide = wide && v->vec == 16 && steps_near(*v);
     }
     p.d.vec = p.dc % 4 == 0 && rows_on(p.d, 4, sizeof(D));
-    p.y.vec = p.dc % 4 == 0 && rows_on(p.y, 4, p.y_f32 ? 4 : sizeof(D));
-    return wide && p.y.vec && steps_near(p.y) && (p.d.p == nullptr || (p.d.vec && steps_near(p.d)));
+    if (p.y_f32) set_vec<float>(p.y, p.dc);
+    else set_vec<D>(p.y, p.dc);
+    return wide && p.y.vec == 16 && steps_near(p.y) && (p.d.p == nullptr || (p.d.vec && steps_near(p.d)));
 }
 
 // The kernel for a call's width and accesses, and whether a state is a result of
@@ -1207,7 +1337,7 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     p.init = initial;
     p.last = final_state;
     p.y_scale = scale;
-    p.p_scale = 1.0f;
+    p.p_scale = scale;
     p.u_scale = 1.0f;
     p.da = (int32_t)dk;
     p.dc = (int32_t)dv;
@@ -1286,7 +1416,7 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     pq.dot = qdq;
     pq.cross = cross;
     pq.y_scale = scale;
-    pq.p_scale = 1.0f;
+    pq.p_scale = scale;
     pq.u_scale = 1.0f;
     pq.da = (int32_t)dv;
     pq.dc = (int32_t)dk;
