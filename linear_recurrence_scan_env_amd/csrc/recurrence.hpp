@@ -287,6 +287,11 @@ __device__ __forceinline__ void put8(StepTile<W, kLimbs<D>>& tile, int at, const
     }
 }
 
+// Waits for this wave's loads.  put() needs them anyway, but by lanes, and where
+// a branch may skip it the compiler counts them as still under way: it would wait
+// before the registers' next loads, and by then for the stores in between too.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
 // One head's steps of an array, from the first of a segment on.
 template <class D>
 struct Rows {
@@ -751,6 +756,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
         const int64_t done = (int64_t)(back ? chunks - 1 - i : i) * kChunk;
         const int count = (int)(steps - done < kChunk ? steps - done : kChunk);
         if (i > 0) take(i - 1);
+        wait_loads();
         ga.put(sh.a, ra);
         gb.put(sh.b, rb);
         gc.put(sh.c, rc);
@@ -971,6 +977,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
     if (chunks > 1) fetch_decay(1);
     for (int i = 0; i < chunks; ++i) {
         if (i > 0) __syncthreads();
+        wait_loads();
         gb.put(sh.b, rb);
         gc.put(sh.c, rc);
         __syncthreads();
