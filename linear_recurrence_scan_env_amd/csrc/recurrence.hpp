@@ -1204,7 +1204,7 @@ inline size_t round_up(size_t b) { return (b + 255) & ~size_t(255); }
 // and, for shared query and key heads, each value head's dq and dk.
 constexpr int64_t kFillBlocks = 512;
 constexpr int64_t kFillBlocksBackward = 1024;
-constexpr int64_t kMinSegment = 256;
+constexpr int64_t kMinSegment = 128;
 
 struct RecurrencePlan {
     int64_t seg_len, segments;

@@ -25,7 +25,8 @@ _F32 = torch.float32
 
 
 class _Seq:
-    """A tensor as passed to a call, with its (environment, step, head) strides."""
+    """A tensor as passed to a call, with its (environment, step, head) strides;
+    None where it is contiguous in that order."""
     __slots__ = ("t", "strides")
 
     def __init__(self, t, strides):
@@ -39,28 +40,32 @@ def _need_tensor(x, name, dims):
         raise ValueError(f"{name} must have {dims} dimensions, got {x.dim()}")
 
 
-def _in_place(x):
+def _inner(shape, axes):
+    """Whether the tensor has an axis within a row, besides environment, step and head."""
+    return len(shape) + axes.count(None) > len(axes)
+
+
+def _in_place(x, axes):
     """Whether the kernels can address x: consecutive inner elements, no axis expanded."""
     sizes, strides = x.shape, x.stride()
-    if sizes[-1] > 1 and strides[-1] != 1:
+    if _inner(sizes, axes) and sizes[-1] > 1 and strides[-1] != 1:
         return False
     return all(st > 0 or n <= 1 for n, st in zip(sizes, strides))
 
 
-def _with_strides(x, axes, per_row):
-    """axes: the positions of (environment, step, head) in x, None where it has
-    none; per_row: x has one element per row (no inner axis)."""
+def _described(x, axes):
+    """axes: the positions of (environment, step, head) in x, None where it has none."""
+    if x.is_contiguous() and axes[0] == 0:
+        return _Seq(x, None)
     st, n = x.stride(), x.shape
     return _Seq(x, tuple(0 if a is None or n[a] <= 1 else st[a] for a in axes))
 
 
 def _seq_in(x, name, dtype, shape, device, axes):
     x = _api._checked(x, name, dtype, shape, device)
-    ok = _in_place(x) if len(shape) == len([a for a in axes if a is not None]) + 1 else \
-        all(st > 0 or n <= 1 for n, st in zip(x.shape, x.stride()))
-    if not ok:
+    if not x.is_contiguous() and not _in_place(x, axes):
         x = x.contiguous()
-    return _with_strides(x, axes, False)
+    return _described(x, axes)
 
 
 def _seq_mask(x, name, shape, device, axes):
@@ -77,12 +82,11 @@ def _seq_mask(x, name, shape, device, axes):
 
 def _seq_out(out, name, dtype, shape, device, axes):
     if out is None:
-        return _with_strides(torch.empty(shape, dtype=dtype, device=device), axes, False)
+        return _described(torch.empty(shape, dtype=dtype, device=device), axes)
     o = _api._checked(out, name, dtype, shape, device)
-    inner = len(shape) > len([a for a in axes if a is not None])
-    if not (_in_place(o) if inner else all(st > 0 or n <= 1 for n, st in zip(o.shape, o.stride()))):
+    if not _in_place(o, axes):
         raise ValueError(f"{name} must have consecutive rows and no expanded axis")
-    return _with_strides(o, axes, False)
+    return _described(o, axes)
 
 
 def _state(x, name, shape, device):
@@ -98,7 +102,10 @@ def _state_out(x, name, shape, device):
 
 
 def _strides(*arrays):
-    vals = [s for a in arrays for s in ((0, 0, 0) if a is None else a.strides)]
+    """The strides argument of a call: None where every array is contiguous."""
+    if all(a is None or a.strides is None for a in arrays):
+        return None
+    vals = [s for a in arrays for s in ((0, 0, 0) if a is None or a.strides is None else a.strides)]
     return (ctypes.c_int64 * len(vals))(*vals)
 
 
@@ -108,19 +115,22 @@ def _ptr(x):
     return x.t.data_ptr() if isinstance(x, _Seq) else x.data_ptr()
 
 
-class _on:
-    """Launches on a tensor's device, whichever is current."""
+_entries = {}
 
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(stem, sfx, device, what, *args):
+    """Calls an entry point on a tensor's device, whichever is current, and its current stream."""
+    fn = _entries.get((stem, sfx))
+    if fn is None:
+        fn = _entries[stem, sfx] = getattr(_api.load(), f"lrs_{stem}_{sfx}")
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        _api._check(status, what)
 
 
 def _workspace(bytes_, device):
@@ -180,14 +190,11 @@ def compute_gated_recurrence(q, k, v, log_decay, *, reset=None, initial_state=No
     last = None
     if want_final_state:
         last = _state_out(final_state, "final_state", r.state_shape, r.dev)
-    lib = _api.load()
-    with _on(r.dev):
-        ws = _workspace(lib.lrs_gated_recurrence_workspace_bytes(*r.sizes, 0), r.dev)
-        _api._check(getattr(lib, f"lrs_gated_recurrence_{r.sfx}")(
-            *r.sizes, _ptr(r.q), _ptr(r.k), _ptr(r.v), _ptr(r.g), _ptr(r.reset), _ptr(init),
-            r.scale(scale), _ptr(y), _ptr(last), _strides(r.q, r.k, r.v, r.g, r.reset, y), _ptr(ws),
-            0 if ws is None else ws.numel(), torch.cuda.current_stream(r.dev).cuda_stream),
-            "compute_gated_recurrence")
+    ws = _workspace(_api.load().lrs_gated_recurrence_workspace_bytes(*r.sizes, 0), r.dev)
+    _call("gated_recurrence", r.sfx, r.dev, "compute_gated_recurrence",
+          *r.sizes, _ptr(r.q), _ptr(r.k), _ptr(r.v), _ptr(r.g), _ptr(r.reset), _ptr(init),
+          r.scale(scale), _ptr(y), _ptr(last), _strides(r.q, r.k, r.v, r.g, r.reset, y), _ptr(ws),
+          0 if ws is None else ws.numel())
     return y.t, last
 
 
@@ -204,15 +211,12 @@ def compute_gated_recurrence_backward(grad_out, q, k, v, log_decay, *, reset=Non
     dq, dk = r.out(None, "grad_q", r.qk_shape), r.out(None, "grad_k", r.qk_shape)
     dv, dg = r.out(None, "grad_v", r.v_shape), r.out(None, "grad_log_decay", r.g_shape)
     dinit = _state_out(None, "", r.state_shape, r.dev) if want_initial_state else None
-    lib = _api.load()
-    with _on(r.dev):
-        ws = _workspace(lib.lrs_gated_recurrence_workspace_bytes(*r.sizes, 1), r.dev)
-        _api._check(getattr(lib, f"lrs_gated_recurrence_backward_{r.sfx}")(
-            *r.sizes, _ptr(do), _ptr(r.q), _ptr(r.k), _ptr(r.v), _ptr(r.g), _ptr(r.reset), _ptr(init),
-            _ptr(dlast), r.scale(scale), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dinit),
-            _strides(do, r.q, r.k, r.v, r.g, r.reset, dq, dk, dv, dg), _ptr(ws),
-            0 if ws is None else ws.numel(), torch.cuda.current_stream(r.dev).cuda_stream),
-            "compute_gated_recurrence_backward")
+    ws = _workspace(_api.load().lrs_gated_recurrence_workspace_bytes(*r.sizes, 1), r.dev)
+    _call("gated_recurrence_backward", r.sfx, r.dev, "compute_gated_recurrence_backward",
+          *r.sizes, _ptr(do), _ptr(r.q), _ptr(r.k), _ptr(r.v), _ptr(r.g), _ptr(r.reset), _ptr(init),
+          _ptr(dlast), r.scale(scale), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dinit),
+          _strides(do, r.q, r.k, r.v, r.g, r.reset, dq, dk, dv, dg), _ptr(ws),
+          0 if ws is None else ws.numel())
     return dq.t, dk.t, dv.t, dg.t, dinit
 
 
@@ -239,13 +243,10 @@ def compute_gated_recurrence_step(q, k, v, log_decay, state, *, reset=None, scal
     old = _state(state, "state", (n, h, dk, dv), dev)
     y = _seq_out(out, "out", dt, (n, h, dv), dev, axes)
     new = _state_out(out_state, "out_state", (n, h, dk, dv), dev)
-    lib = _api.load()
-    with _on(dev):
-        _api._check(getattr(lib, f"lrs_gated_recurrence_step_{sfx}")(
-            n, h, kv, dk, dv, _ptr(qs), _ptr(ks), _ptr(vs), _ptr(gs), _ptr(rs), _ptr(old),
-            float(dk) ** -0.5 if scale is None else float(scale), _ptr(y), _ptr(new),
-            _strides(qs, ks, vs, gs, rs, y), torch.cuda.current_stream(dev).cuda_stream),
-            "compute_gated_recurrence_step")
+    _call("gated_recurrence_step", sfx, dev, "compute_gated_recurrence_step",
+          n, h, kv, dk, dv, _ptr(qs), _ptr(ks), _ptr(vs), _ptr(gs), _ptr(rs), _ptr(old),
+          float(dk) ** -0.5 if scale is None else float(scale), _ptr(y), _ptr(new),
+          _strides(qs, ks, vs, gs, rs, y))
     return y.t, new
 
 
@@ -308,13 +309,10 @@ def compute_qk_norm_rotation(q, k, q_weight, k_weight, table=None, positions=Non
     r = _Rot(q, k, q_weight, k_weight, table, positions)
     yq = r.out(None if out is None else out[0], "out[0]", r.q_shape)
     yk = r.out(None if out is None else out[1], "out[1]", r.k_shape)
-    lib = _api.load()
-    with _on(r.dev):
-        _api._check(getattr(lib, f"lrs_qk_norm_rotation_{r.sfx}")(
-            *r.sizes, _ptr(r.q), _ptr(r.k), _ptr(r.qw), _ptr(r.kw), _ptr(r.table), r.max,
-            _ptr(r.positions), float(eps), int(bool(interleaved)), _ptr(yq), _ptr(yk),
-            _strides(r.q, r.k, r.positions, yq, yk), torch.cuda.current_stream(r.dev).cuda_stream),
-            "compute_qk_norm_rotation")
+    _call("qk_norm_rotation", r.sfx, r.dev, "compute_qk_norm_rotation",
+          *r.sizes, _ptr(r.q), _ptr(r.k), _ptr(r.qw), _ptr(r.kw), _ptr(r.table), r.max,
+          _ptr(r.positions), float(eps), int(bool(interleaved)), _ptr(yq), _ptr(yk),
+          _strides(r.q, r.k, r.positions, yq, yk))
     return yq.t, yk.t
 
 
@@ -327,15 +325,12 @@ def compute_qk_norm_rotation_backward(grad_q_out, grad_k_out, q, k, q_weight, k_
     gk = _seq_in(grad_k_out, "grad_k_out", r.dt, r.k_shape, r.dev, r.axes)
     dq, dk = r.out(None, "grad_q", r.q_shape), r.out(None, "grad_k", r.k_shape)
     dqw, dkw = torch.empty_like(r.qw), torch.empty_like(r.kw)
-    lib = _api.load()
-    with _on(r.dev):
-        ws = _workspace(lib.lrs_qk_norm_rotation_workspace_bytes(*r.sizes[:5]), r.dev)
-        _api._check(getattr(lib, f"lrs_qk_norm_rotation_backward_{r.sfx}")(
-            *r.sizes, _ptr(gq), _ptr(gk), _ptr(r.q), _ptr(r.k), _ptr(r.qw), _ptr(r.kw), _ptr(r.table),
-            r.max, _ptr(r.positions), float(eps), int(bool(interleaved)), _ptr(dq), _ptr(dk),
-            _ptr(dqw), _ptr(dkw), _strides(gq, gk, r.q, r.k, r.positions, dq, dk), _ptr(ws),
-            0 if ws is None else ws.numel(), torch.cuda.current_stream(r.dev).cuda_stream),
-            "compute_qk_norm_rotation_backward")
+    ws = _workspace(_api.load().lrs_qk_norm_rotation_workspace_bytes(*r.sizes[:5]), r.dev)
+    _call("qk_norm_rotation_backward", r.sfx, r.dev, "compute_qk_norm_rotation_backward",
+          *r.sizes, _ptr(gq), _ptr(gk), _ptr(r.q), _ptr(r.k), _ptr(r.qw), _ptr(r.kw), _ptr(r.table),
+          r.max, _ptr(r.positions), float(eps), int(bool(interleaved)), _ptr(dq), _ptr(dk),
+          _ptr(dqw), _ptr(dkw), _strides(gq, gk, r.q, r.k, r.positions, dq, dk), _ptr(ws),
+          0 if ws is None else ws.numel())
     return dq.t, dk.t, dqw, dkw
 
 
