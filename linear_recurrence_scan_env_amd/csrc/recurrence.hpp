@@ -1196,14 +1196,18 @@ inline lrs_status check_state(const char* nm, const void* p, const char* what)
 inline size_t round_up(size_t b) { return (b + 255) & ~size_t(255); }
 
 // How a call is cut up, and its workspace.  A pass has a block per head and
-// segment: one segment where the heads alone fill the chip, else as many as
-// give kFillBlocks blocks, of at least kMinSegment steps (a segment costs one
-// more reading of two of its arrays and a state written and read twice).
+// segment: as many segments as fill the chip's kFillBlocks places (two blocks on
+// each of 256 CUs) once, and no more, of at least kMinSegment steps.  Segments
+// cost one more reading of two of the arrays and states written and read twice,
+// and a second round of blocks is as long as the first (training, forward and
+// backward: 8 x 2048 steps of 16 heads with 1 segment in the backward pass 446
+// us, 2 521, 3 493, 4 501, 8 567; 16384 steps of 8 heads 16: 316, 21: 294, 32:
+// 318, 43: 305; 32768 steps of 16 heads forward 16: 260, 32: 204, 64: 240; 3 x
+// 1001 steps of 6 heads with segments of 256: 139, 128: 119, 64: 131).
 // Workspace: the states before each segment and the segments' decays, per
 // direction; backward also q.dq and k.dk [N, H, T], <S, dS> [N, H, segments]
 // and, for shared query and key heads, each value head's dq and dk.
 constexpr int64_t kFillBlocks = 512;
-constexpr int64_t kFillBlocksBackward = 1024;
 constexpr int64_t kMinSegment = 128;
 
 struct RecurrencePlan {
@@ -1216,9 +1220,8 @@ inline RecurrencePlan plan_recurrence(int64_t N, int64_t T, int64_t H, int64_t K
 {
     RecurrencePlan p{};
     const int64_t heads = N * H * (backward ? 3 : 1);
-    const int64_t fill = backward ? kFillBlocksBackward : kFillBlocks;
-    int64_t parts = std::min((fill + heads - 1) / heads, (T + kMinSegment - 1) / kMinSegment);
-    if (heads >= fill) parts = 1;
+    const int64_t parts =
+        std::max<int64_t>(1, std::min(kFillBlocks / heads, (T + kMinSegment - 1) / kMinSegment));
     p.seg_len = ((T + parts - 1) / parts + kChunk - 1) / kChunk * kChunk;
     p.segments = (T + p.seg_len - 1) / p.seg_len;
     size_t at = 0;
