@@ -38,8 +38,9 @@ constexpr int kMaxDim = 128;  // largest key and value dimension
 // [N, H, segments, key_dim, value_dim] (nullable for one segment); last: where
 // the state after the last segment goes, [N, H, key_dim, value_dim], nullable.
 // y_scale multiplies what y has of the state, p_scale what it has of the products
-// a . b, u_scale what enters the state.  dot (nullable): receives y_i . d_i per [N, H, T]; cross (nullable):
-// <state after the segment, meet> per [N, H, segments], meet like init.
+// a . b, u_scale what enters the state.  dot: receives y_i . d_i per [N, H, T]
+// (dq and dk); cross (nullable): <state after the segment, meet> per
+// [N, H, segments], meet like init.
 struct PassArgs {
     SeqView a, b, c, d, y;
     const float* init;
@@ -86,7 +87,6 @@ __device__ __forceinline__ int64_t state_at(const PassArgs& p, int r, int c)
 // is split as far as its result needs.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 template <class D>
@@ -182,10 +182,9 @@ using ColumnFrags = Frag<kLimbs<D>>[kCols<D, W>];
 // group of 16 lanes, by both operands.  Rows are an odd number of 16-byte units
 // long, and the rows of each 16 are laid out 0, 4, 1, 5, ... and 8 below, so
 // that a fragment by rows (16 rows at one unit) and one by columns (rows 0..3
-// and 8..11 at two neighbouring units, transposed) touch every bank once; and
-// every fragment lies at a constant distance from one address per lane, which
-// is worth registers: pairs of 8-byte reads, whose distances are limited, took
-// 40 registers of addresses.
+// and 8..11 at two neighbouring units, transposed) touch every bank once, and
+// every fragment lies at a constant distance from one address per lane.  (The
+// fragments in eights read half of each unit, at half the rate.)
 constexpr int kChunk = 32;
 constexpr int kTile = 16;
 
@@ -306,8 +305,9 @@ struct Rows {
 };
 
 // A block moves a chunk of one head's array into a tile in two halves: fetch()
-// starts the loads (of a thread's 16-byte units), put() writes what arrived to LDS, zero beyond dim.  Steps beyond
-// `count` read the last one again: their weights are zero.  kWide: every row is
+// starts the loads (of a thread's 16-byte units), put() writes what arrived to
+// LDS, zero beyond dim.  Steps beyond `count` read the last one again: their
+// weights are zero.  kWide: every row is
 // on 16 bytes and dim a multiple of 8, and a chunk lies within 2 GiB, so that
 // one 32-bit offset per lane and access is all the addressing there is; nothing
 // then branches around the loads, which would make the wave wait for them where
@@ -464,6 +464,12 @@ struct ChunkDecay {
     float entry[kChunk];  // from the start of the chunk, inclusive
     float exit[kChunk];   // to the end of the chunk
     float total;          // of the chunk
+
+    // total, known to be the same in all lanes
+    __device__ __forceinline__ float whole() const
+    {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, total)));
+    }
 };
 
 // The log decay and the reset mask of a lane's step, as they are stored, loaded
@@ -488,10 +494,6 @@ struct DecayRows {
         t += min(lane, count - 1);
         next_g = g[t * g_step];
         next_reset = reset[t * reset_step];
-    }
-    __device__ __forceinline__ bool cut(int64_t t) const
-    {
-        return (resets && reset[t * reset_step] != 0) || to_f32(g[t * g_step]) == -INFINITY;
     }
     // -infinity where the step is cut
     __device__ __forceinline__ float value() const
@@ -578,13 +580,17 @@ __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W,
     const f32x8 w8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) fw[u] = split<LW>(joined<L>(fc[u]) * w8);
-    const float f = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, total)));
+    if (total == 0.0f)  // a cut drops the state, whatever it holds
+#pragma unroll
+        for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u) S[k][u] = f32x4{};
 #pragma unroll
     for (int k = 0; k < W / 16; ++k) {
         if (state_row(k, 0) >= da) break;  // (da: W where the whole width is to be unrolled)
         const Frag<L> fb = tb.template columns<true>(0, state_row(k, 0), lane);
 #pragma unroll
-        for (int u = 0; u < U; ++u) S[k][u] = mma(fb, fw[u], S[k][u] * f);
+        for (int u = 0; u < U; ++u) S[k][u] = mma(fb, fw[u], S[k][u] * total);
     }
 }
 
@@ -716,9 +722,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
     if (wave == 0) make_decay(0);
     if (chunks > 1) fetch_decay(1);
 
-    // S[k][u][r]: row state_row(k) + r, column c0 + 16 u + col; a state that the first step drops is
-    // not read, whatever it holds
-    const float* const init = p.init == nullptr || (!back && decays.cut(0)) ? nullptr : p.init;
+    // S[k][u][r]: row state_row(k) + r, column c0 + 16 u + col;
     StateTiles<D, W> S;
 #pragma unroll
     for (int k = 0; k < 2 * K; ++k)
@@ -727,7 +731,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = state_row(k, group) + r, c = c0 + u * 16 + col;
-                S[k][u][r] = init && row < p.da && c < p.dc ? init[at + state_at(p, row, c)] : 0.0f;
+                S[k][u][r] = p.init && row < p.da && c < p.dc ? p.init[at + state_at(p, row, c)] : 0.0f;
             }
 
     Result<D, W, kWide> result;
@@ -839,6 +843,13 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
             for (int u = 0; u < U; ++u) fc[u] = sh.c.columns(0, c0 + u * 16, lane);
             const float* const from = back ? decay.exit : decay.entry;
+            const float total = decay.whole();
+            if (total == 0.0f)  // nothing of the state passes a cut, whatever it holds
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (from[q * 16 + col] == 0.0f) y[q][u] = f32x4{};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int step = q * 16 + col;
@@ -862,7 +873,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 }
             }
             // the state after the chunk
-            add_chunk<LW, D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, decay.total, p.u_scale,
+            add_chunk<LW, D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, total, p.u_scale,
                                 kWide ? W : p.da, lane);
         }
         __syncthreads();
@@ -987,12 +998,13 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
             if (wave == i % (kThreads<D, W> / kWave)) make_decay(i + 1);
             if (i + 2 < chunks) fetch_decay(i + 2);
         }
-        total *= decay.total;
+        const float chunk_total = decay.whole();
+        total *= chunk_total;
         if (!kWide && c0 >= p.dc) continue;
         ColumnFrags<D, W> fc;
 #pragma unroll
         for (int u = 0; u < U; ++u) fc[u] = sh.c.columns(0, c0 + u * 16, lane);
-        add_chunk<kStateLimbs<D>(kExact), D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, decay.total,
+        add_chunk<kStateLimbs<D>(kExact), D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, chunk_total,
                                                 p.u_scale, kWide ? W : p.da, lane);
     }
     float* const to = p.states + (head * x.segments + next) * (int64_t)p.da * p.dc;

@@ -263,6 +263,25 @@ def test_step_drops_what_a_reset_state_holds():
     assert torch.isfinite(o).all() and torch.isfinite(S).all()
 
 
+@pytest.mark.parametrize("t", [100, 700])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_a_cut_drops_a_state_that_is_not_finite(dtype, bad, t):
+    """Everything from the cut on, and what goes back to it, is as from any other state."""
+    c = Case(2, t, 2, 1, 64, 48, dtype)
+    cut = t // 2 - 3
+    c.reset = torch.zeros(2, t, dtype=torch.bool)
+    c.reset[1, cut] = True
+    want = (*c.forward(), *c.backward())
+    c.h0[1, 0, 5, 7] = bad
+    got = (*c.forward(), *c.backward())
+    for x, y in zip(got[:1] + got[2:6], want[:1] + want[2:6]):  # out and the steps' gradients
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1, cut:], y[1, cut:])
+    for x, y in ((got[1], want[1]), (got[6], want[6])):  # the states at the ends
+        assert torch.equal(x, y)
+    assert not torch.isfinite(got[0][1, :cut, 0]).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_windows_chain(dtype):
     """The final state of one window is the initial state of the next."""
