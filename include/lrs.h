@@ -664,10 +664,13 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
  *     read and written in place; outputs must address every element once.
  *     Strides, bases and dims that keep every row on 16 bytes are fastest.
  *   - key_dim and value_dim 1 to 128; heads a multiple of kv_heads, at most
- *     65536; N * heads at most 2^22; N and T as above.
+ *     65536; N * heads at most 2^21; N and T as above.
  *   - Inputs must be finite, log_decay finite or -infinity (and is meant to be
- *     <= 0: growth is computed as given and may overflow); exact zeros where
- *     a cut separates two steps, for finite inputs.
+ *     <= 0: growth is computed as given and may overflow).  Nothing passes a
+ *     cut: a step that is not finite all the same makes NaN of what it has a
+ *     part in -- out from this step on, the gradients of q, k and v up to it
+ *     or from it on, that of log_decay in the whole episode -- and of nothing
+ *     beyond its episode.
  *   - Sums and states are fp32 (or more); outputs are rounded once.  A call
  *     gives the same bits every time.
  *   - workspace: lrs_gated_recurrence_workspace_bytes(...) bytes, 16-byte

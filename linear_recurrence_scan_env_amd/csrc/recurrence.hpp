@@ -156,6 +156,11 @@ __device__ __forceinline__ f32x8 joined(const Frag<L>& f)
     return v;
 }
 
+__device__ __forceinline__ bf16x8 masked(const bf16x8& x, const u32x4& m)
+{
+    return __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, x) & m);
+}
+
 // acc += A^T B over 32 products per lane group, all limb products down to the
 // smaller operand's last limb.
 template <int LA, int LB>
@@ -567,6 +572,9 @@ constexpr int kStateLimbs(bool exact)
     return kLimbs<D> > 1 || exact ? 3 : 2;
 }
 
+// total = 0: something in the chunk is cut, which drops the state and the steps
+// before the cut, whatever they hold.  Where that leaves something that is not
+// finite (0 times infinity or NaN is NaN) they are taken out of the products.
 template <int LW, class D, int W>
 __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W, kLimbs<D>>& tb,
                                           const ColumnFrags<D, W>& fc, const float* w, float total,
@@ -580,7 +588,7 @@ __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W,
     const f32x8 w8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) * scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) fw[u] = split<LW>(joined<L>(fc[u]) * w8);
-    if (total == 0.0f)  // a cut drops the state, whatever it holds
+    if (total == 0.0f)
 #pragma unroll
         for (int k = 0; k < W / 16; ++k)
 #pragma unroll
@@ -591,6 +599,93 @@ __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W,
         const Frag<L> fb = tb.template columns<true>(0, state_row(k, 0), lane);
 #pragma unroll
         for (int u = 0; u < U; ++u) S[k][u] = mma(fb, fw[u], S[k][u] * total);
+    }
+    if (total != 0.0f) return;
+    f32x4 sum = {};
+#pragma unroll
+    for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+        for (int u = 0; u < U; ++u) sum += S[k][u] * 0.0f;
+    if (!__any((sum[0] + sum[1]) + (sum[2] + sum[3]) != 0.0f)) return;
+    u32x4 kept;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        kept[k] = (w[group * 8 + 2 * k] != 0.0f ? 0xffffu : 0u) |
+                  (w[group * 8 + 2 * k + 1] != 0.0f ? 0xffff0000u : 0u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int l = 0; l < LW; ++l) fw[u].x[l] = masked(fw[u].x[l], kept);
+#pragma unroll
+    for (int k = 0; k < W / 16; ++k) {
+        Frag<L> fb = tb.template columns<true>(0, state_row(k, 0), lane);
+#pragma unroll
+        for (int l = 0; l < L; ++l) fb.x[l] = masked(fb.x[l], kept);
+#pragma unroll
+        for (int u = 0; u < U; ++u) S[k][u] = mma(fb, fw[u], f32x4{});
+    }
+}
+
+// A step whose c is not finite reaches the results of the steps that it has a
+// weight in, as NaN, and no others: a product with a weight of 0 would be NaN
+// too.  Which tells whether a wave's columns hold one: their product with zeros.
+// Of a chunk of finite steps this is all that is done, early enough for the
+// branch on it not to wait (256 x 128 f32, both directions: 195 us with the
+// branch right behind the product, 172 so, 170 without).
+template <class D, int W>
+__device__ __forceinline__ f32x4 times_zero(const StepTile<W, kLimbs<D>>& tc, int c0, int lane)
+{
+    f32x4 sum = {};
+#pragma unroll
+    for (int u = 0; u < kCols<D, W>; ++u)
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tc.columns(0, c0 + u * 16, lane).x[0], bf16x8{}, sum, 0, 0, 0);
+    return sum;
+}
+
+// The halves of a fragment that hold something from `least` on, all bits set.
+__device__ __forceinline__ u32x4 halves_from(const bf16x8& x, uint32_t least)
+{
+    const u32x4 w = __builtin_bit_cast(u32x4, x) & 0x7fff7fffu;
+    u32x4 m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        m[k] = ((w[k] & 0xffffu) >= least ? 0xffffu : 0u) | ((w[k] >> 16) >= least ? 0xffff0000u : 0u);
+    return m;
+}
+
+// Takes what is not finite out of c, and puts NaN in the results (and into
+// `lost`, of the wave's columns of the state) that it has a part in: those where
+// the product of the one place and the other's weight, both as 0 or 1, sums to
+// more than 0.
+template <class D, int W, int LS>
+__device__ __forceinline__ void part_nonfinite(ColumnFrags<D, W>& fc, const StepTile<kChunk, LS>& ab,
+                                               const float* w, f32x4 (&y)[2][kCols<D, W>],
+                                               bool (&lost)[kCols<D, W>], int lane)
+{
+    constexpr int L = kLimbs<D>, U = kCols<D, W>;
+    const int group = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const u32x4 bad = halves_from(fc[u].x[0], 0x7f80u);
+#pragma unroll
+        for (int l = 0; l < L; ++l) fc[u].x[l] = masked(fc[u].x[l], ~bad);
+        const Frag<1> place = {{__builtin_bit_cast(bf16x8, bad & 0x3f803f80u)}};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const u32x4 some = halves_from(ab.rows(q * 16, 0, lane).x[0], 1u);
+            const Frag<1> weight = {{__builtin_bit_cast(bf16x8, some & 0x3f803f80u)}};
+            const f32x4 hits = mma(place, weight, f32x4{});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (hits[r] != 0.0f) y[q][u][r] = __builtin_nanf("");
+        }
+        int hit = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            hit |= (bad[k / 2] >> (16 * (k & 1)) & 1) != 0 && w[group * 8 + k] != 0.0f;
+        hit |= __shfl_xor(hit, 16);
+        hit |= __shfl_xor(hit, 32);
+        lost[u] = hit != 0;
     }
 }
 
@@ -789,6 +884,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
         // (steps of a) 16 q0 + col.  One of them lies on the side of the diagonal that is zero; it
         // is computed too, since branches around products make a wave wait for each read of LDS.
         const int q0 = wave & 1, s0 = (wave >> 1) & 1;
+        const f32x4 zeros = times_zero<D, W>(sh.c, c0, lane);
         f32x4 ab = {};
         // y^T of tile q: rows c0 + 16 u + 4 group + r, column (step) 16 q + col
         f32x4 y[2][U];
@@ -821,13 +917,15 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 for (int r = 0; r < 4; ++r) {
                     const float d = (float)(back ? decay.p[o + r] - pi : pi - decay.p[o + r]);
                     const bool in = (back ? o + r >= step : o + r <= step) && decay.m[o + r] == mi;
-                    // (plus 0 or minus infinity: a choice of values would become a branch)
-                    ab[r] *= __builtin_amdgcn_exp2f(d + (in ? 0.0f : -INFINITY)) * p.p_scale;
+                    // (both factors chosen: ab may be NaN)
+                    ab[r] = (in ? ab[r] : 0.0f) * (__builtin_amdgcn_exp2f(in ? d : 0.0f) * p.p_scale);
                 }
             } else {
                 const bool in_order = back ? s0 > q0 : s0 < q0;
                 const float mine = in_order ? (back ? decay.tail : decay.head)[step] * p.p_scale : 0.0f;
-                ab *= *reinterpret_cast<const f32x4*>(&(back ? decay.head : decay.tail)[o]) * mine;
+                const f32x4 w = *reinterpret_cast<const f32x4*>(&(back ? decay.head : decay.tail)[o]) * mine;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ab[r] = w[r] == 0.0f ? 0.0f : ab[r] * w[r];
             }
             const int here = sh.ab.at(col, group * 4) + q0 * 16 * sh.ab.kRow + s0 * 16;
             uint32_t lo[LS], hi[LS];
@@ -836,6 +934,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
             for (int l = 0; l < LS; ++l) *reinterpret_cast<u32x2*>(&sh.ab.e[l][here]) = u32x2{lo[l], hi[l]};
         }
+        const bool nonfinite = __any((zeros[0] + zeros[1]) + (zeros[2] + zeros[3]) != 0.0f);
         __syncthreads();
 
         if (kWide || c0 < p.dc) {
@@ -850,6 +949,9 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
                     for (int u = 0; u < U; ++u)
                         if (from[q * 16 + col] == 0.0f) y[q][u] = f32x4{};
+            bool lost[U];
+            if (__builtin_expect(nonfinite, 0))
+                part_nonfinite<D, W, LS>(fc, sh.ab, back ? decay.entry : decay.exit, y, lost, lane);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int step = q * 16 + col;
@@ -875,6 +977,12 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
             // the state after the chunk
             add_chunk<LW, D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, total, p.u_scale,
                                 kWide ? W : p.da, lane);
+            if (__builtin_expect(nonfinite, 0))
+#pragma unroll
+                for (int k = 0; k < 2 * K; ++k)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (lost[u]) S[k][u] = f32x4{} + __builtin_nanf("");
         }
         __syncthreads();
     }
@@ -1181,7 +1289,9 @@ __global__ __launch_bounds__(256) void recurrence_one_step(const StepArgs x)
 
 // ------------------------------------------------------------------ entries
 
-constexpr int64_t kMaxHeads = int64_t(1) << 22;  // num_envs * heads of a call
+// num_envs * heads of a call: three blocks of 512 threads to each, in a grid of
+// less than 2^32 threads
+constexpr int64_t kMaxHeads = int64_t(1) << 21;
 
 inline lrs_status check_recurrence(const char* nm, int64_t N, int64_t T, int64_t H, int64_t KV,
                                    int64_t dk, int64_t dv, float scale)

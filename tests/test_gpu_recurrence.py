@@ -282,6 +282,34 @@ def test_a_cut_drops_a_state_that_is_not_finite(dtype, bad, t):
     assert not torch.isfinite(got[0][1, :cut, 0]).all()
 
 
+@pytest.mark.parametrize("where", ["q", "k", "v", "do"])
+@pytest.mark.parametrize("n, t, dk, dv", [(2, 100, 64, 48), (1, 700, 128, 128), (2, 45, 33, 20)])
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_a_step_that_is_not_finite_stays_in_its_episode(dtype, bad, n, t, dk, dv, where):
+    """Nothing of it before its time, and the same bits in all other episodes."""
+    c = Case(n, t, 2, 1, dk, dv, dtype)
+    s = t // 2 + 1
+    start, end = s - 4, s + 3  # one chunk holds all of the episode, or a part of it
+    c.reset = torch.zeros(n, t, dtype=torch.bool)
+    c.reset[:, [start, end]] = True
+    want = (*c.forward(), *c.backward())
+    getattr(c, where)[n - 1, s, 0, 5] = bad
+    got = (*c.forward(), *c.backward())
+    assert torch.equal(got[1], want[1]) and torch.equal(got[6], want[6])  # the states at the ends
+    for x, y in zip(got[:1] + got[2:6], want[:1] + want[2:6]):
+        assert torch.equal(x[:-1], y[:-1])
+        assert torch.equal(x[-1, :start], y[-1, :start]) and torch.equal(x[-1, end:], y[-1, end:])
+    for k in (0, 2):  # out and grad_q
+        assert torch.equal(got[k][-1, :s], want[k][-1, :s])
+    for k in (3, 4):  # grad_k and grad_v
+        assert torch.equal(got[k][-1, s + 1:], want[k][-1, s + 1:])
+    if where in "kv":
+        assert not torch.isfinite(got[0][-1, s:end, 0]).all(-1).any()
+    if where == "do":
+        assert not torch.isfinite(got[3][-1, start:s + 1, 0]).all(-1).any()
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_windows_chain(dtype):
     """The final state of one window is the initial state of the next."""
