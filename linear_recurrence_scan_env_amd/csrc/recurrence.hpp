@@ -1164,10 +1164,13 @@ __global__ __launch_bounds__(256) void join_segments(const RecurrenceArgs x)
     }
 }
 
-// dg of one segment of a head by one wave, 64 steps at a time from its end: a
-// suffix sum of q.dq - k.dk in 64 bits (its terms cancel), from <state after
-// the segment, its gradient>, started again at each cut, where nothing is
-// carried over and dg is 0.
+// dg of one segment of a head, 64 steps at a time from its end: a suffix sum of
+// q.dq - k.dk in 64 bits (its terms cancel), from <state after the segment, its
+// gradient>, started again at each cut, where nothing is carried over and dg is
+// 0.  The windows of 64 depend on each other through one value, and each waits
+// for its loads: a long segment is split over up to kDecayWaves waves, each of
+// which first sums what its steps hand on (those before their first cut).
+// 128 segments of 2048 steps, bf16: 33.6 us by one wave each, 13.6 by eight.
 struct DecayGradArgs {
     SeqView g, reset, dg;
     const float *qdq, *kdk, *cross;
@@ -1175,23 +1178,57 @@ struct DecayGradArgs {
     int32_t H, segments;
 };
 
-template <class D>
-__global__ __launch_bounds__(64) void decay_grad(const DecayGradArgs x)
+constexpr int kDecayWaves = 8;
+
+// Waves to a segment: at least four windows each.
+inline int decay_waves(int64_t seg_len)
 {
+    const int64_t w = seg_len / (4 * kWave);
+    return (int)(w < 1 ? 1 : w < kDecayWaves ? w : kDecayWaves);
+}
+
+template <class D>
+__global__ __launch_bounds__(kDecayWaves * kWave) void decay_grad(const DecayGradArgs x)
+{
+    __shared__ double handed[kDecayWaves];
+    __shared__ bool ended[kDecayWaves];
     const int64_t head = blockIdx.x / x.segments, n = head / x.H;
-    const int h = (int)(head % x.H), lane = threadIdx.x;
+    const int h = (int)(head % x.H), lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int waves = blockDim.x / kWave;
     const int64_t first = (int64_t)(blockIdx.x % x.segments) * x.seg_len;
     const int64_t past = x.T - first < x.seg_len ? x.T : first + x.seg_len;
+    const int64_t windows = (past - first + kWave - 1) / kWave;
+    const int64_t begin = min(past, first + wave * ((windows + waves - 1) / waves) * kWave);
+    const int64_t stop_at = min(past, first + (wave + 1) * ((windows + waves - 1) / waves) * kWave);
+    const auto load = [&](int64_t t, bool& cut) {
+        const float g = to_f32(*seq_row<D>(x.g, n, t, h));
+        cut = __expf(g) == 0.0f || (x.reset.p && *seq_row<uint8_t>(x.reset, n, t, 0) != 0);
+        return (double)x.qdq[head * x.T + t] - (double)x.kdk[head * x.T + t];
+    };
     double carry = x.cross[blockIdx.x];
-    for (int64_t end = past; end > first; end -= kWave) {
+    if (waves > 1) {
+        double sum = 0.0;
+        bool over = false;
+        for (int64_t t0 = begin; t0 < stop_at && !over; t0 += kWave) {
+            bool cut = false;
+            const double v = t0 + lane < stop_at ? load(t0 + lane, cut) : 0.0;
+            const uint64_t cuts = __ballot(cut);
+            if (cuts == 0 || lane < __ffsll((unsigned long long)cuts) - 1) sum += v;
+            over = cuts != 0;
+        }
+        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+        if (lane == 0) {
+            handed[wave] = sum;
+            ended[wave] = over;
+        }
+        __syncthreads();
+        for (int w = waves - 1; w > wave; --w) carry = ended[w] ? handed[w] : handed[w] + carry;
+    }
+    for (int64_t end = stop_at; end > begin; end -= kWave) {
         const int64_t t = end - 1 - lane;
         double v = 0.0;
         bool cut = false;
-        if (t >= first) {
-            v = (double)x.qdq[head * x.T + t] - (double)x.kdk[head * x.T + t];
-            const float g = to_f32(*seq_row<D>(x.g, n, t, h));
-            cut = __expf(g) == 0.0f || (x.reset.p && *seq_row<uint8_t>(x.reset, n, t, 0) != 0);
-        }
+        if (t >= begin) v = load(t, cut);
         // sums over the lanes up to this one, from the last cut below it on
         bool stop = __shfl_up((int)cut, 1) != 0 && lane > 0;
         for (int o = 1; o < kWave; o <<= 1) {
@@ -1203,7 +1240,7 @@ __global__ __launch_bounds__(64) void decay_grad(const DecayGradArgs x)
             }
         }
         if (!stop) v += carry;
-        if (t >= first) *seq_row_out<D>(x.dg, n, t, h) = from_f32<D>(cut ? 0.0f : (float)v);
+        if (t >= begin) *seq_row_out<D>(x.dg, n, t, h) = from_f32<D>(cut ? 0.0f : (float)v);
         carry = __shfl(v, kWave - 1);
         if (__shfl((int)cut, kWave - 1)) carry = 0.0;
     }
@@ -1590,7 +1627,7 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
                        (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x));
     DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, plan.seg_len, (int32_t)H,
                      (int32_t)plan.segments};
-    LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H * plan.segments), 64, stream, dg));
+    LRS_TRY(launch_seq(nm, decay_grad<D>, (uint64_t)(N * H * plan.segments), kWave * decay_waves(plan.seg_len), stream, dg));
     if (group > 1) {
         const int64_t blocks = (N * T * KV * dk + 255) / 256;
         for (int i = 0; i < 2; ++i) {

@@ -310,6 +310,13 @@ def test_a_step_that_is_not_finite_stays_in_its_episode(dtype, bad, n, t, dk, dv
         assert not torch.isfinite(got[3][-1, start:s + 1, 0]).all(-1).any()
 
 
+@pytest.mark.parametrize("reset", [0.0, 0.004])
+@pytest.mark.parametrize("t", [700, 2100])
+def test_decay_gradient_of_long_segments(t, reset):
+    """Many heads: one segment each, its gradient made by several waves."""
+    check_backward(Case(100, t, 2, 1, 8, 8, torch.float32, reset=reset))
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_windows_chain(dtype):
     """The final state of one window is the initial state of the next."""
