@@ -2,8 +2,6 @@
 // status strings, the last-error buffer, workspace sizing, the debug
 // schedule override and the schedule diagnostics.
 #include "entries.hpp"
-#include "recurrence.hpp"
-#include "rotation.hpp"
 
 namespace lrs {
 
@@ -40,24 +38,6 @@ size_t lrs_workspace_bytes(lrs_estimator est, int64_t num_envs, int64_t seq_len)
     const size_t row_major = workspace_bytes_for((uint64_t)num_envs * (uint64_t)seq_len);
     const size_t time_major = workspace_bytes_tm((uint64_t)num_envs, (uint64_t)seq_len);
     return row_major > time_major ? row_major : time_major;
-}
-
-size_t lrs_gated_recurrence_workspace_bytes(int64_t num_envs, int64_t seq_len, int64_t heads,
-                                            int64_t kv_heads, int64_t key_dim, int64_t value_dim,
-                                            int backward)
-{
-    if (check_recurrence("", num_envs, seq_len, heads, kv_heads, key_dim, value_dim, 1.0f) != LRS_OK)
-        return 0;
-    return plan_recurrence(num_envs, seq_len, heads, kv_heads, key_dim, value_dim, backward != 0).bytes;
-}
-
-size_t lrs_qk_norm_rotation_workspace_bytes(int64_t num_envs, int64_t seq_len, int64_t q_heads,
-                                            int64_t k_heads, int64_t dim)
-{
-    if (!valid_sizes(num_envs, seq_len) || q_heads < 1 || k_heads < 1 || q_heads > 65536 ||
-        k_heads > 65536 || dim < 1 || dim > kMaxHeadDim)
-        return 0;
-    return norm_workspace(num_envs, seq_len, q_heads, k_heads, dim);
 }
 
 lrs_status lrs_debug_set_schedule(int force_lookback, int elems_per_lane, int waves_per_block)

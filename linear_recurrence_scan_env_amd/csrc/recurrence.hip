@@ -1,9 +1,18 @@
-// recurrence.hip -- fp32 entry points of the gated recurrence.
+// recurrence.hip -- workspace size and fp32 entry points of the gated recurrence.
 #include "recurrence.hpp"
 
 using namespace lrs;
 
 extern "C" {
+
+size_t lrs_gated_recurrence_workspace_bytes(int64_t num_envs, int64_t seq_len, int64_t heads,
+                                            int64_t kv_heads, int64_t key_dim, int64_t value_dim,
+                                            int backward)
+{
+    if (check_recurrence("", num_envs, seq_len, heads, kv_heads, key_dim, value_dim, 1.0f) != LRS_OK)
+        return 0;
+    return plan_recurrence(num_envs, seq_len, heads, kv_heads, key_dim, value_dim, backward != 0).bytes;
+}
 
 lrs_status lrs_gated_recurrence_f32(int64_t N, int64_t T, int64_t H, int64_t KV, int64_t dk, int64_t dv,
     const float* q, const float* k, const float* v, const float* log_decay, const uint8_t* reset,

@@ -700,6 +700,17 @@ __device__ __forceinline__ void part_nonfinite(ColumnFrags<D, W>& fc, const Step
 // 16 columns per lane; a wave's tiles of S take their rows in fours of every 8,
 // so that two of them are an operand and S feeds the next product from the
 // registers that it is kept in.
+//
+// What bounds it: a step of the chain.  The state's registers leave two waves
+// per SIMD at W = 128, and a chunk is a chain of LDS reads, products, weights,
+// a barrier, products again: of 32768 steps of 16 heads of 128 x 128 in bf16
+// (about 120 us; 34 GFLOP with the segments' states) the vector
+// unit is busy for 36% of the cycles, LDS for 40%, the matrix unit for 27%, and
+// no two of them much at once.  Chunks of 32 steps rather than 64: the longer
+// ones do half the barriers, but their operands spill.  A second set of LDS
+// tiles, which saves one of the three barriers, measured slower (32768 steps
+// 204 -> 225 us, 8 x 2048 both directions 488 -> 541), as did three waves per
+// SIMD by smaller register budgets (206 -> 241).
 template <class D, int W, int LS>
 struct PassShared {
     StepTile<W, kLimbs<D>> a, b, c;
@@ -1029,7 +1040,10 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurren
 }
 
 // The three passes of the backward call: dq and dk with q.dq and k.dk to a
-// precision that their differences keep, and dv.
+// precision that their differences keep, and dv.  Blocks of the three passes of
+// a segment are neighbours: they read the same steps, mostly from L2.  8 x 2048
+// steps of 16 heads of 128 x 128 in bf16: 347 us, bound like the forward pass
+// with two limbs per operand; 256 x 128 of 4 heads of 64 x 64 in f32: 130 us.
 template <class D, int W, bool kWide, bool kExact>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_backward(const RecurrenceArgs x)
 {
@@ -1046,6 +1060,9 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurren
 
 // The state that one segment alone leaves (from zero), and its decay, by the
 // same products; the last segment in scan order leaves none that is used.
+// 32768 steps of 16 heads of 128 x 128 in bf16, 32 segments: 77 us, that is 2.2
+// us per chunk of each block: the loads' way to LDS and two barriers.  Two
+// chunks between barriers measured the same (207.9 and 207.4 us for the call).
 template <class D, int W, bool kWide, bool kExact>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_states(const RecurrenceArgs x)
 {
@@ -1130,7 +1147,9 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
 
 // Turns the segments' own states into the states before each of them, in scan
 // order: in[s] = own[s - 1] + total[s - 1] in[s - 1].  A thread per element;
-// the loads of kAhead segments are in flight together.
+// the loads of kAhead segments are in flight together.  Bound by the states'
+// bytes, read and written once: 16 heads of 128 x 128, 32 segments, 67 MB in
+// 14.6 us (4.6 TB/s).
 constexpr int kAhead = 8;
 
 template <class D>
@@ -1247,7 +1266,7 @@ __global__ __launch_bounds__(kDecayWaves * kWave) void decay_grad(const DecayGra
 }
 
 // Sums the value heads' gradients of a shared query or key head, in a fixed
-// order: part [N, T, H, dim] in fp32 to y [N, T, H / group, dim].
+// order (3 x 1001 steps, 6 heads: 4.6 us): part [N, T, H, dim] in fp32 to y [N, T, H / group, dim].
 struct SharedSumArgs {
     const float* part;
     SeqView y;
@@ -1270,7 +1289,13 @@ __global__ __launch_bounds__(256) void shared_sum(const SharedSumArgs x)
 }
 
 // One step of every head: the state is read, updated and written, and read by
-// the query, in one pass.  V: state elements per access.
+// the query, in one pass.  V: state elements per access (4 where value_dim is a
+// multiple of 4 and the states lie on 16 bytes).  A block per head: rows of the
+// state side by side, whose parts of out are added up in LDS in a fixed order.
+// Bound by the state's bytes, which leave nothing for a matrix instruction to
+// do: 4096 environments of 4 heads of 64 x 64, 545 MB in 99 us (5.5 TB/s, the
+// rate of a large copy).  For one environment the call is host and launch time
+// (14 us, binding included).
 struct StepArgs {
     SeqView q, k, v, g, reset, o;
     const float* state;

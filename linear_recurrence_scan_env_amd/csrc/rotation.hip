@@ -1,10 +1,19 @@
-// rotation.hip -- fp32 entry points of the norm of queries and keys with
-// the position rotation.
+// rotation.hip -- workspace size and fp32 entry points of the norm of queries
+// and keys with the position rotation.
 #include "rotation.hpp"
 
 using namespace lrs;
 
 extern "C" {
+
+size_t lrs_qk_norm_rotation_workspace_bytes(int64_t num_envs, int64_t seq_len, int64_t q_heads,
+                                            int64_t k_heads, int64_t dim)
+{
+    if (!valid_sizes(num_envs, seq_len) || q_heads < 1 || k_heads < 1 || q_heads > 65536 ||
+        k_heads > 65536 || dim < 1 || dim > kMaxHeadDim)
+        return 0;
+    return norm_workspace(num_envs, seq_len, q_heads, k_heads, dim);
+}
 
 lrs_status lrs_qk_norm_rotation_f32(int64_t N, int64_t T, int64_t HQ, int64_t HK, int64_t dim,
     int64_t rotary_dim, const float* q, const float* k, const float* q_weight, const float* k_weight,

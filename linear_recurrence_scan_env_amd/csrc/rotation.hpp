@@ -42,7 +42,8 @@ struct NormArgs {
 
 constexpr int kNormWaves = 4;
 
-// One wave per row.
+// For rows that are not on 16 bytes, or pairs that do not lie in whole 16-byte
+// units: one wave per row, an element per lane and access; the pairs meet in LDS.
 template <class D, bool kBackward>
 __global__ __launch_bounds__(kNormWaves * kWave) void norm_rotation(const NormArgs x)
 {
@@ -140,7 +141,11 @@ __global__ __launch_bounds__(kNormWaves * kWave) void norm_rotation(const NormAr
 // consecutive tokens; a lane keeps its columns' weights, and its token's angles
 // for all the heads that it walks over, in registers.  Each wave walks over
 // consecutive tokens of its own.  With kNormAhead rows in flight per lane the
-// loads are what bounds it.
+// loads are what bounds it: 32768 tokens of 32 + 8 heads of 128 in bf16, 688 MB
+// in 163 us (4.2 TB/s, 80% of a large copy's rate; by one wave per row 699 us);
+// the gradients of 8 x 2048 tokens of 16 + 16 heads, 403 MB, in 95 us.  Rows
+// that leave lanes without a unit lose by that: 72 floats take 18 of 32 lanes,
+// 37 x 513 tokens of 7 + 3 heads 39 us and their gradients 50 (2.8 and 3.2 TB/s).
 template <class D>
 constexpr int kUnit = 16 / sizeof(D);
 constexpr int kNormAhead = 4;
@@ -312,7 +317,8 @@ __global__ __launch_bounds__(kNormWaves * kWave) void norm_rotation_wide(const N
     }
 }
 
-// dw from the blocks' sums, in a fixed order: one block per element of dim.
+// dw from the blocks' sums, in a fixed order: one block per element of dim, 4.9
+// us for 1024 sums of 128 (a launch and one chain of loads).
 struct WeightSumArgs {
     const float* part[2];
     void* dw[2];
