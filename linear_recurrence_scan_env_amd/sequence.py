@@ -363,7 +363,10 @@ class _GatedRecurrence(torch.autograd.Function):
 def gated_recurrence(q, k, v, log_decay, *, reset=None, initial_state=None, scale=None,
                      time_major=False):
     """compute_gated_recurrence for autograd: differentiable in q, k, v,
-    log_decay and initial_state; returns (out, final_state)."""
+    log_decay and initial_state; returns (out, final_state).  To capture both
+    directions into a graph, call the compute_ functions, or first drop every
+    eager result of the same leaves: torch does not capture a backward pass
+    beside those."""
     return _GatedRecurrence.apply(q, k, v, log_decay, initial_state, reset, scale, time_major)
 
 
