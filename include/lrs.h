@@ -647,8 +647,9 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
  *   out_t = scale * S_t^T q_t
  *
  * cut_t where reset_t is nonzero (the step starts an episode) or log_decay_t
- * is -infinity.  S before the first step is initial_state (0 if NULL); it is
- * dropped where step 0 is cut.
+ * is below -87.33654: a decay under 2^-126, the smallest normal float32, is 0
+ * (-infinity, -1e30 and the types' lowest values alike).  S before the first
+ * step is initial_state (0 if NULL); it is dropped where step 0 is cut.
  *   - Arrays: q, k [N, T, kv_heads, key_dim]; v, out [N, T, heads,
  *     value_dim]; log_decay [N, T, heads]; reset [N, T] u8 (nullable); all
  *     of one storage type.  States are float32 in every variant,

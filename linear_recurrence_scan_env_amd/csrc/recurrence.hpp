@@ -3,7 +3,7 @@
 //
 //     S_t = (cut_t ? 0 : e^{g_t} S_{t-1}) + k_t v_t^T,    o_t = scale S_t^T q_t
 //
-// cut_t where the reset mask is set or g_t is -infinity.  With
+// cut_t where the reset mask is set or g_t is below kLeastLogDecay.  With
 // D(i, j) = e^{g_{j+1} + ... + g_i} (0 where a step in j+1..i is cut), every
 // direction is one pass of the same form,
 //
@@ -32,6 +32,13 @@
 namespace lrs {
 
 constexpr int kMaxDim = 128;  // largest key and value dimension
+
+// ln 2^-126: a decay below the smallest normal float32 is 0 in every kernel, so
+// such a step is a cut, -infinity, -1e30 and the types' lowest values alike.  (In
+// a running sum of log decays a value of that size would leave nothing of those
+// after it.)
+constexpr float kLeastLogDecay = -87.33654f;
+__device__ __forceinline__ bool cuts(float log_decay) { return log_decay < kLeastLogDecay; }
 
 // One pass over the sequence, in segments of seg_len steps that blocks work on
 // side by side.  init: each segment's state before its first step in scan order,
@@ -456,7 +463,7 @@ struct Result {
 };
 
 // The decays of a chunk of 32 steps, in two tiles of 16.  With p the running
-// sum of log2 decays within a tile (in 64 bits: a strong decay before a weak
+// sum of log2 decays within a tile (in 64 bits: a decay of 2^-126 before a weak
 // one would cost an fp32 sum the weak one's digits) and m the running count of
 // its cuts, for steps j < i of one tile D(i, j) = 2^(p_i - p_j) where m_i =
 // m_j, and for steps of the second and the first tile D(i, j) = head_i tail_j,
@@ -527,7 +534,7 @@ __device__ __forceinline__ void row_scan(double& p, int& m)
 __device__ __forceinline__ void chunk_decay(ChunkDecay& s, float g, int count, int lane)
 {
     const bool in = lane < count;
-    int m = in && g == -INFINITY;
+    int m = in && cuts(g);
     double p = m || !in ? 0.0 : (double)g * 1.4426950408889634;
     static_assert(kTile == 16, "rows of 16 lanes");
     row_scan<1>(p, m);
@@ -1221,7 +1228,7 @@ __global__ __launch_bounds__(kDecayWaves * kWave) void decay_grad(const DecayGra
     const int64_t stop_at = min(past, first + (wave + 1) * ((windows + waves - 1) / waves) * kWave);
     const auto load = [&](int64_t t, bool& cut) {
         const float g = to_f32(*seq_row<D>(x.g, n, t, h));
-        cut = __expf(g) == 0.0f || (x.reset.p && *seq_row<uint8_t>(x.reset, n, t, 0) != 0);
+        cut = cuts(g) || (x.reset.p && *seq_row<uint8_t>(x.reset, n, t, 0) != 0);
         return (double)x.qdq[head * x.T + t] - (double)x.kdk[head * x.T + t];
     };
     double carry = x.cross[blockIdx.x];
@@ -1315,7 +1322,7 @@ __global__ __launch_bounds__(256) void recurrence_one_step(const StepArgs x)
     const D* k = seq_row<D>(x.k, n, 0, h);
     const float g = to_f32(*seq_row<D>(x.g, n, 0, h));
     const bool reset = x.reset.p != nullptr && *seq_row<uint8_t>(x.reset, n, 0, 0) != 0;
-    const float f = reset ? 0.0f : __expf(g);
+    const float f = reset || cuts(g) ? 0.0f : __expf(g);
     const int64_t at = head * x.dk * x.dv;
     float v[V], y[V];
 #pragma unroll

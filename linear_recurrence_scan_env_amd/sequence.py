@@ -178,7 +178,8 @@ def compute_gated_recurrence(q, k, v, log_decay, *, reset=None, initial_state=No
 
     Per environment and head, S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T and
     out_t = scale * S_t^T q_t, the old state dropped where reset_t is set (the
-    first step of an episode) or log_decay_t is -inf.  q, k
+    first step of an episode) or log_decay_t is below -87.33654 (a decay under the
+    smallest normal float32 is 0; -inf and torch.finfo's lowest values alike).  q, k
     [num_envs, seq_len, kv_heads, key_dim]; v, out [..., heads, value_dim]
     (value head h reads key head h // (heads // kv_heads)); log_decay
     [num_envs, seq_len, heads]; reset [num_envs, seq_len]; states float32
