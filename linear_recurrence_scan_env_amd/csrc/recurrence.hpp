@@ -979,12 +979,16 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const f32x4 v = mma(fc[u], f, y[q][u] * in);
+                    // Columns beyond dim are 0, unless a holds something that is not finite: 0 times that.
+                    // Where kWide they are written by no one else, so such a result would stay in the tile,
+                    // as c of later chunks.
+                    const int c = c0 + u * 16 + group * 4;
+                    if (kWide && c >= p.dc) continue;
                     if constexpr (kPrecise) {
                         const f32x4 e = unpack4<D>(d[q][u]) * v;
                         dot += (e[0] + e[1]) + (e[2] + e[3]);
                     }
-                    Result<D, W, kWide>::put(low, high,
-                                             sh.c.at(col, c0 + u * 16 + group * 4) + q * 16 * sh.c.kRow, v, f32);
+                    Result<D, W, kWide>::put(low, high, sh.c.at(col, c) + q * 16 * sh.c.kRow, v, f32);
                 }
                 if constexpr (kPrecise) {
                     dot += __shfl_xor(dot, 16);

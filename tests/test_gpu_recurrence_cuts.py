@@ -61,3 +61,35 @@ def test_a_strong_finite_decay_drops_the_state(dtype, strong):
     grads = c.backward()
     assert all(torch.isfinite(x).all() for x in grads)
     assert (grads[3][:, 0, 0] == 0).all() and (grads[4][:, 0] == 0).all()
+
+
+def outside_is_the_same(c, change, start, end):
+    """Runs the case before and after change(c), which touches only the episode [start, end) of the
+    last environment: everything else has the same bits."""
+    want = (*c.forward(), *c.backward())
+    change(c)
+    got = (*c.forward(), *c.backward())
+    assert torch.equal(got[1], want[1]) and torch.equal(got[6], want[6])  # the states at the ends
+    for k in (0, 2, 3, 4, 5):  # out and the steps' gradients
+        x, y = got[k], want[k]
+        assert torch.equal(x[:-1], y[:-1]), k
+        assert torch.equal(x[-1, :start], y[-1, :start]), (k, "before")
+        assert torch.equal(x[-1, end:], y[-1, end:]), (k, "after")
+    return got
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "do"])
+@pytest.mark.parametrize("kv", [1, 2])
+@pytest.mark.parametrize("dk, dv", [(40, 64), (72, 40), (80, 128), (24, 24), (104, 16)])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_a_step_that_is_not_finite_leaves_no_padding_behind(dtype, dk, dv, kv, where):
+    """Dims that rows of whole 16-byte units do not fill, and episodes in later and earlier chunks."""
+    for bad in (float("nan"), -float("inf")):
+        c = Case(2, 170, 2, kv, dk, dv, dtype)
+        start, at, end = 68, 75, 79
+        c.reset = torch.zeros(2, 170, dtype=torch.bool)
+        c.reset[:, [20, start, end, 101, 120]] = True
+
+        def change(c):
+            getattr(c, where)[-1, at, 0, 5] = bad
+        outside_is_the_same(c, change, start, end)
