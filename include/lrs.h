@@ -668,10 +668,10 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
  *     65536; N * heads at most 2^21; N and T as above.
  *   - Inputs must be finite, log_decay finite or -infinity (and is meant to be
  *     <= 0: growth is computed as given and may overflow).  Nothing passes a
- *     cut: a step that is not finite all the same makes NaN of what it has a
- *     part in -- out from this step on, the gradients of q, k and v up to it
- *     or from it on, that of log_decay in the whole episode -- and of nothing
- *     beyond its episode.
+ *     cut: a step or log_decay that is not finite all the same, or growth that
+ *     overflows, makes NaN or infinities of what it has a part in -- out from
+ *     this step on, the gradients of q, k and v up to it or from it on, that
+ *     of log_decay in the whole episode -- and of nothing beyond its episode.
  *   - Sums and states are fp32 (or more); outputs are rounded once.  A call
  *     gives the same bits every time.
  *   - workspace: lrs_gated_recurrence_workspace_bytes(...) bytes, 16-byte

@@ -464,10 +464,12 @@ struct Result {
 
 // The decays of a chunk of 32 steps, in two tiles of 16.  With p the running
 // sum of log2 decays within a tile (in 64 bits: a decay of 2^-126 before a weak
-// one would cost an fp32 sum the weak one's digits) and m the running count of
-// its cuts, for steps j < i of one tile D(i, j) = 2^(p_i - p_j) where m_i =
-// m_j, and for steps of the second and the first tile D(i, j) = head_i tail_j,
-// where each factor is at most 1 for log decays up to 0.
+// one would cost an fp32 sum the weak one's digits), started again at each cut,
+// and m the running count of its cuts, for steps j < i of one tile D(i, j) =
+// 2^(p_i - p_j) where m_i = m_j, and for steps of the second and the first tile
+// D(i, j) = head_i tail_j, where each factor is at most 1 for log decays up to 0.
+// A decay that is not finite, or growth that overflows, thus stays between the
+// cuts around it; what crosses a cut is 0 by choice, not as a factor of 0.
 struct ChunkDecay {
     double p[kChunk];
     int m[kChunk];
@@ -522,12 +524,15 @@ __device__ __forceinline__ int row_below(int v, int none)
 {
     return __builtin_amdgcn_update_dpp(none, v, 0x110 + kShift, 0xf, 0xf, false);
 }
+// One step of the scan: p over the steps up to this one from the last cut on (m
+// counts those of the steps taken in so far), m over all of them.
 template <int kShift>
 __device__ __forceinline__ void row_scan(double& p, int& m)
 {
     const uint64_t bits = __builtin_bit_cast(uint64_t, p);
     const uint32_t lo = row_below<kShift>((int)(uint32_t)bits, 0), hi = row_below<kShift>((int)(bits >> 32), 0);
-    p += __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    const double below = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    p += m ? 0.0 : below;
     m += row_below<kShift>(m, 0);
 }
 
@@ -545,7 +550,6 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& s, float g, int count, i
     const uint64_t bits = __builtin_bit_cast(uint64_t, p);
     double ptot[2];
     int mtot[2];
-    float w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int end = k * kTile + kTile - 1;
@@ -553,20 +557,20 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& s, float g, int count, i
         const uint32_t hi = __builtin_amdgcn_readlane((int)(bits >> 32), end);
         ptot[k] = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
         mtot[k] = __builtin_amdgcn_readlane(m, end);
-        w[k] = mtot[k] ? 0.0f : __builtin_amdgcn_exp2f((float)ptot[k]);
     }
-    const float head = m ? 0.0f : __builtin_amdgcn_exp2f((float)p);
-    const float tail =
-        m != (second ? mtot[1] : mtot[0]) ? 0.0f : __builtin_amdgcn_exp2f((float)((second ? ptot[1] : ptot[0]) - p));
+    // 2^e, 0 across a cut and of steps beyond the end
+    const auto decay = [](bool whole, double e) { return whole ? __builtin_amdgcn_exp2f((float)e) : 0.0f; };
+    const double left = (second ? ptot[1] : ptot[0]) - p;
+    const bool headed = in && m == 0, tailed = in && m == (second ? mtot[1] : mtot[0]);
     if (lane < kChunk) {
         s.p[lane] = p;
         s.m[lane] = in ? m : -1;  // steps beyond the end have no part in anything
-        s.head[lane] = in ? head : 0.0f;
-        s.tail[lane] = in ? tail : 0.0f;
-        s.entry[lane] = in ? (second ? w[0] * head : head) : 0.0f;
-        s.exit[lane] = in ? (second ? tail : w[1] * tail) : 0.0f;
+        s.head[lane] = decay(headed, p);
+        s.tail[lane] = decay(tailed, left);
+        s.entry[lane] = decay(headed && !(second && mtot[0]), second ? ptot[0] + p : p);
+        s.exit[lane] = decay(tailed && !(!second && mtot[1]), second ? left : left + ptot[1]);
     }
-    if (lane == 0) s.total = w[0] * w[1];
+    if (lane == 0) s.total = decay(!mtot[0] && !mtot[1], ptot[0] + ptot[1]);
 }
 
 // S = total S + b^T (w c) over a chunk; w: the weight of each step,
@@ -940,10 +944,13 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 }
             } else {
                 const bool in_order = back ? s0 > q0 : s0 < q0;
-                const float mine = in_order ? (back ? decay.tail : decay.head)[step] * p.p_scale : 0.0f;
-                const f32x4 w = *reinterpret_cast<const f32x4*>(&(back ? decay.head : decay.tail)[o]) * mine;
+                const float mine = in_order ? (back ? decay.tail : decay.head)[step] : 0.0f;
+                const f32x4 w = *reinterpret_cast<const f32x4*>(&(back ? decay.head : decay.tail)[o]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) ab[r] = w[r] == 0.0f ? 0.0f : ab[r] * w[r];
+                for (int r = 0; r < 4; ++r) {
+                    const float f = w[r] * (mine * p.p_scale);
+                    ab[r] = mine == 0.0f || w[r] == 0.0f || f == 0.0f ? 0.0f : ab[r] * f;
+                }
             }
             const int here = sh.ab.at(col, group * 4) + q0 * 16 * sh.ab.kRow + s0 * 16;
             uint32_t lo[LS], hi[LS];
@@ -1135,7 +1142,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
             if (i + 2 < chunks) fetch_decay(i + 2);
         }
         const float chunk_total = decay.whole();
-        total *= chunk_total;
+        total = total == 0.0f || chunk_total == 0.0f ? 0.0f : total * chunk_total;
         if (!kWide && c0 >= p.dc) continue;
         ColumnFrags<D, W> fc;
 #pragma unroll

@@ -93,3 +93,28 @@ def test_a_step_that_is_not_finite_leaves_no_padding_behind(dtype, dk, dv, kv, w
         def change(c):
             getattr(c, where)[-1, at, 0, 5] = bad
         outside_is_the_same(c, change, start, end)
+
+
+# start, bad step and end of an episode from the start of a chunk of 32 steps on
+EPISODES = [(3, 7, 10), (10, 20, 25), (14, 15, 17), (10, 20, 40), (2, 40, 60), (17, 18, 31)]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 300.0])
+@pytest.mark.parametrize("cut", ["reset", "decay"])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_a_log_decay_that_is_not_finite_stays_in_its_episode(dtype, cut, bad):
+    """NaN, infinite growth, and growth that overflows."""
+    for t, dk, dv in ((150, 40, 24), (700, 64, 64)):
+        for start, at, end in EPISODES:
+            c = Case(2, t, 2, 1, dk, dv, dtype)
+            start, at, end = (x + t // 64 * 32 for x in (start, at, end))
+            if cut == "reset":
+                c.reset = torch.zeros(2, t, dtype=torch.bool)
+                c.reset[:, [start, end]] = True
+            else:
+                c.g[:, [start, end]] = -float("inf")
+
+            def change(c):
+                c.g[-1, at, 0] = bad
+            got = outside_is_the_same(c, change, start, end)
+            assert not torch.isfinite(got[0][-1, at, 0]).any()
