@@ -672,8 +672,11 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
  *     overflows, makes NaN or infinities of what it has a part in -- out from
  *     this step on, the gradients of q, k and v up to it or from it on, that
  *     of log_decay in the whole episode -- and of nothing beyond its episode.
- *   - Sums and states are fp32 (or more); outputs are rounded once.  A call
- *     gives the same bits every time.
+ *   - Sums and states are fp32 (or more); outputs are rounded once.  What is
+ *     made on the way and multiplied again (weighted products, a state that a
+ *     query reads) keeps at least 16 bits in the 16-bit variants and 24 in
+ *     f32.  A call gives the same bits every time, whichever of the nullable
+ *     outputs are asked for.
  *   - workspace: lrs_gated_recurrence_workspace_bytes(...) bytes, 16-byte
  *     aligned, any contents; NULL with 0 bytes where that is 0.  Nothing in
  *     it outlives the call's kernels.  Do not pass the estimators' workspace:

@@ -109,6 +109,13 @@ constexpr int kCols = W == 128 && kLimbs<D> == 1 ? 2 : 1;
 template <class D, int W>
 constexpr int kThreads = 4 * W / kCols<D, W>;
 
+// Limbs of a b^T and of the state as operands: as many as the inputs have, and
+// two at least, which keep 16 bits, so that the rounding of a 16-bit result is
+// the only one to be seen in it (with one limb bf16 results were off by 0.0023
+// of their size, with two by the 0.0017 of the type).
+template <class D>
+constexpr int kOperandLimbs = kLimbs<D> > 2 ? kLimbs<D> : 2;
+
 template <int L>
 struct Frag {
     bf16x8 x[L];
@@ -574,24 +581,20 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& s, float g, int count, i
 }
 
 // S = total S + b^T (w c) over a chunk; w: the weight of each step,
-// fc: the wave's columns of c.  The weighted c is fp32: two limbs keep 16 of its
-// bits, enough for what is made of S in 16-bit results and their differences; a
-// state that is itself a result takes a third (LW = 3, all 24).
-template <class D>
-constexpr int kStateLimbs(bool exact)
-{
-    return kLimbs<D> > 1 || exact ? 3 : 2;
-}
+// fc: the wave's columns of c.  The weighted c is fp32 and keeps its 24 bits in
+// three limbs, so that S is what fp32 sums make it (in bf16 two would save 3% of
+// 8 x 2048 training, 481 us and 468).
+constexpr int kStateLimbs = 3;
 
 // total = 0: something in the chunk is cut, which drops the state and the steps
 // before the cut, whatever they hold.  Where that leaves something that is not
 // finite (0 times infinity or NaN is NaN) they are taken out of the products.
-template <int LW, class D, int W>
+template <class D, int W>
 __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W, kLimbs<D>>& tb,
                                           const ColumnFrags<D, W>& fc, const float* w, float total,
                                           float scale, int da, int lane)
 {
-    constexpr int L = kLimbs<D>, U = kCols<D, W>;
+    constexpr int L = kLimbs<D>, U = kCols<D, W>, LW = kStateLimbs;
     const int group = lane >> 4;
     Frag<LW> fw[U];
     const f32x4 lo = *reinterpret_cast<const f32x4*>(&w[group * 8]);
@@ -722,10 +725,10 @@ __device__ __forceinline__ void part_nonfinite(ColumnFrags<D, W>& fc, const Step
 // tiles, which saves one of the three barriers, measured slower (32768 steps
 // 204 -> 225 us, 8 x 2048 both directions 488 -> 541), as did three waves per
 // SIMD by smaller register budgets (206 -> 241).
-template <class D, int W, int LS>
+template <class D, int W>
 struct PassShared {
     StepTile<W, kLimbs<D>> a, b, c;
-    StepTile<kChunk, LS> ab;
+    StepTile<kChunk, kOperandLimbs<D>> ab;
     ChunkDecay decays[2];  // this chunk's, and the next one's as it is made
     float dot[W / 16][kChunk];
     float cross[W / 16];
@@ -773,19 +776,11 @@ __device__ __forceinline__ f32x4 unpack4(const Raw4<D>& v)
     return f;
 }
 
-// Limbs of a b^T and of the state as operands: as many as the inputs have, and
-// at least two where q.dq and k.dk are wanted.
-template <class D>
-constexpr int kOperandLimbs(bool precise)
-{
-    return kLimbs<D> > 1 ? kLimbs<D> : (precise ? 2 : 1);
-}
-
-template <class D, int W, bool kWide, bool back, bool kPrecise, int LW, int LS>
+template <class D, int W, bool kWide, bool back, bool kPrecise>
 __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs& p, uint32_t block,
-                                         PassShared<D, W, LS>& sh)
+                                         PassShared<D, W>& sh)
 {
-    constexpr int L = kLimbs<D>;
+    constexpr int L = kLimbs<D>, LS = kOperandLimbs<D>;
     constexpr int K = W / 32, U = kCols<D, W>, kWaves = W / 16 / U;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -1004,7 +999,7 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 }
             }
             // the state after the chunk
-            add_chunk<LW, D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, total, p.u_scale,
+            add_chunk<D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, total, p.u_scale,
                                 kWide ? W : p.da, lane);
             if (__builtin_expect(nonfinite, 0))
 #pragma unroll
@@ -1049,12 +1044,11 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 template <class D, int W>
 constexpr int kPassWaves = W == 128 || kLimbs<D> == 3 ? 2 : 4;
 
-template <class D, int W, bool kWide, bool kExact>
+template <class D, int W, bool kWide>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_forward(const RecurrenceArgs x)
 {
-    constexpr int LS = kOperandLimbs<D>(false);
-    __shared__ PassShared<D, W, LS> sh;
-    run_pass<D, W, kWide, false, false, kStateLimbs<D>(kExact), LS>(x, x.pass[0], blockIdx.x, sh);
+    __shared__ PassShared<D, W> sh;
+    run_pass<D, W, kWide, false, false>(x, x.pass[0], blockIdx.x, sh);
 }
 
 // The three passes of the backward call: dq and dk with q.dq and k.dk to a
@@ -1062,18 +1056,14 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurren
 // a segment are neighbours: they read the same steps, mostly from L2.  8 x 2048
 // steps of 16 heads of 128 x 128 in bf16: 347 us, bound like the forward pass
 // with two limbs per operand; 256 x 128 of 4 heads of 64 x 64 in f32: 130 us.
-template <class D, int W, bool kWide, bool kExact>
+template <class D, int W, bool kWide>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_backward(const RecurrenceArgs x)
 {
-    constexpr int LS = kOperandLimbs<D>(true), LV = kOperandLimbs<D>(false);
-    __shared__ union {
-        PassShared<D, W, LS> precise;
-        PassShared<D, W, LV> plain;
-    } sh;
+    __shared__ PassShared<D, W> sh;
     const uint32_t block = blockIdx.x / 3, pass = blockIdx.x % 3;
-    if (pass == 0) run_pass<D, W, kWide, false, true, kStateLimbs<D>(false), LS>(x, x.pass[0], block, sh.precise);
-    else if (pass == 1) run_pass<D, W, kWide, true, true, kStateLimbs<D>(false), LS>(x, x.pass[1], block, sh.precise);
-    else run_pass<D, W, kWide, true, false, kStateLimbs<D>(kExact), LV>(x, x.pass[2], block, sh.plain);
+    if (pass == 0) run_pass<D, W, kWide, false, true>(x, x.pass[0], block, sh);
+    else if (pass == 1) run_pass<D, W, kWide, true, true>(x, x.pass[1], block, sh);
+    else run_pass<D, W, kWide, true, false>(x, x.pass[2], block, sh);
 }
 
 // The state that one segment alone leaves (from zero), and its decay, by the
@@ -1081,7 +1071,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurren
 // 32768 steps of 16 heads of 128 x 128 in bf16, 32 segments: 77 us, that is 2.2
 // us per chunk of each block: the loads' way to LDS and two barriers.  Two
 // chunks between barriers measured the same (207.9 and 207.4 us for the call).
-template <class D, int W, bool kWide, bool kExact>
+template <class D, int W, bool kWide>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_states(const RecurrenceArgs x)
 {
     __shared__ struct {
@@ -1147,7 +1137,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_
         ColumnFrags<D, W> fc;
 #pragma unroll
         for (int u = 0; u < U; ++u) fc[u] = sh.c.columns(0, c0 + u * 16, lane);
-        add_chunk<kStateLimbs<D>(kExact), D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, chunk_total,
+        add_chunk<D, W>(S, sh.b, fc, back ? decay.entry : decay.exit, chunk_total,
                                                 p.u_scale, kWide ? W : p.da, lane);
     }
     float* const to = p.states + (head * x.segments + next) * (int64_t)p.da * p.dc;
@@ -1479,19 +1469,14 @@ bool set_vec(PassArgs& p)
     return wide && p.y.vec == 16 && steps_near(p.y) && (p.d.p == nullptr || (p.d.vec && steps_near(p.d)));
 }
 
-// The kernel for a call's width and accesses, and whether a state is a result of
-// the call (kExact differs from not only where inputs are one limb).
-#define LRS_PICK_EXACT(kernel, D, W, wide, exact)                                             \
-    ((exact) || kLimbs<D> > 1 ? ((wide) ? kernel<D, W, true, true> : kernel<D, W, false, true>) \
-                              : ((wide) ? kernel<D, W, true, kLimbs<D> != 1>                    \
-                                        : kernel<D, W, false, kLimbs<D> != 1>))
-#define LRS_PICK(kernel, D, widest, wide, exact)                   \
-    ((widest) <= 64 ? LRS_PICK_EXACT(kernel, D, 64, wide, exact)   \
-                    : LRS_PICK_EXACT(kernel, D, 128, wide, exact))
+// The kernel for a call's width and accesses.
+#define LRS_PICK(kernel, D, widest, wide)                                       \
+    ((widest) <= 64 ? ((wide) ? kernel<D, 64, true> : kernel<D, 64, false>)     \
+                    : ((wide) ? kernel<D, 128, true> : kernel<D, 128, false>))
 
 // The states before every segment, in x.carry's directions.
 template <class D>
-lrs_status launch_carries(const char* nm, RecurrenceArgs& x, bool wide, bool exact, hipStream_t stream)
+lrs_status launch_carries(const char* nm, RecurrenceArgs& x, bool wide, hipStream_t stream)
 {
     if (x.segments == 1) return LRS_OK;
     for (int i = 0; i < x.carries; ++i) {
@@ -1500,7 +1485,7 @@ lrs_status launch_carries(const char* nm, RecurrenceArgs& x, bool wide, bool exa
     }
     const int da = x.carry[0].da, dc = x.carry[0].dc, widest = std::max(da, dc);
     const uint64_t heads = (uint64_t)x.N * x.H, blocks = heads * (x.segments - 1) * x.carries;
-    LRS_TRY(launch_seq(nm, LRS_PICK(segment_states, D, widest, wide, exact), blocks, (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x));
+    LRS_TRY(launch_seq(nm, LRS_PICK(segment_states, D, widest, wide), blocks, (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x));
     return launch_seq(nm, join_segments<D>, (heads * da * dc + 255) / 256 * x.carries, 256, stream, x);
 }
 
@@ -1555,9 +1540,8 @@ lrs_status recurrence_entry(const char* nm, int64_t N, int64_t T, int64_t H, int
     p.dc = (int32_t)dv;
     const int widest = (int)std::max(dk, dv);
     const bool wide = set_vec<D>(p);
-    const bool exact = final_state != nullptr;
-    LRS_TRY(launch_carries<D>(nm, x, wide, exact, stream));
-    return launch_seq(nm, LRS_PICK(recurrence_forward, D, widest, wide, exact), (uint64_t)(N * H * plan.segments),
+    LRS_TRY(launch_carries<D>(nm, x, wide, stream));
+    return launch_seq(nm, LRS_PICK(recurrence_forward, D, widest, wide), (uint64_t)(N * H * plan.segments),
                       (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x);
 }
 
@@ -1664,9 +1648,8 @@ lrs_status recurrence_backward_entry(const char* nm, int64_t N, int64_t T, int64
     const int widest = (int)std::max(dk, dv);
     bool wide = true;
     for (PassArgs& p : x.pass) wide = set_vec<D>(p) && wide;
-    const bool exact = grad_initial != nullptr;
-    LRS_TRY(launch_carries<D>(nm, x, wide, exact, stream));
-    LRS_TRY(launch_seq(nm, LRS_PICK(recurrence_backward, D, widest, wide, exact), (uint64_t)(N * H * plan.segments) * 3,
+    LRS_TRY(launch_carries<D>(nm, x, wide, stream));
+    LRS_TRY(launch_seq(nm, LRS_PICK(recurrence_backward, D, widest, wide), (uint64_t)(N * H * plan.segments) * 3,
                        (widest <= 64 ? kThreads<D, 64> : kThreads<D, 128>), stream, x));
     DecayGradArgs dg{w[4], w[5], w[9], qdq, kdk, cross, N, T, plan.seg_len, (int32_t)H,
                      (int32_t)plan.segments};
