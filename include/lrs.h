@@ -686,9 +686,12 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
  * Backward: the gradients of q, k, v and log_decay (of the same storage
  * type; those of q and k summed over the heads that share them) and of
  * initial_state (nullable: not written), from grad_out and grad_final_state
- * (nullable = 0).  grad_log_decay is 0 at cut steps.  The states of the
- * forward call are computed again; nothing of it has to be kept but its
- * inputs.
+ * (nullable = 0).  grad_log_decay is 0 at cut steps.  Elsewhere it is a sum,
+ * in 64 bits, of q.dq - k.dk over the later steps of its episode, each term
+ * exact to 16 bits or more (24 in f32): where one step decays far more than the
+ * steps after it, its small gradient carries the error of their larger terms.
+ * The states of the forward call are computed again; nothing of it has to be
+ * kept but its inputs.
  *
  * Step: one step of every environment: q, k [N, kv_heads, key_dim], v, out
  * [N, heads, value_dim], log_decay [N, heads], reset [N]; strides as above

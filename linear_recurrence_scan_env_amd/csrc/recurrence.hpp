@@ -22,7 +22,9 @@
 //     dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_T>,
 //
 // since q_s . dq_s sums the products of s with all steps up to it and
-// k_s . dk_s with all steps from it on; what lies wholly behind t cancels.
+// k_s . dk_s with all steps from it on; what lies wholly behind t cancels.  The
+// product of s with itself is in both: it is left out of both sums, or strong
+// decays would leave dg the difference of numbers far larger than itself.
 #pragma once
 
 #include <algorithm>
@@ -45,8 +47,8 @@ __device__ __forceinline__ bool cuts(float log_decay) { return log_decay < kLeas
 // [N, H, segments, key_dim, value_dim] (nullable for one segment); last: where
 // the state after the last segment goes, [N, H, key_dim, value_dim], nullable.
 // y_scale multiplies what y has of the state, p_scale what it has of the products
-// a . b, u_scale what enters the state.  dot: receives y_i . d_i per [N, H, T]
-// (dq and dk); cross (nullable): <state after the segment, meet> per
+// a . b, u_scale what enters the state.  dot: receives y_i . d_i per [N, H, T],
+// without step i's own part of y_i (dq and dk); cross (nullable): <state after the segment, meet> per
 // [N, H, segments], meet like init.
 struct PassArgs {
     SeqView a, b, c, d, y;
@@ -225,6 +227,22 @@ struct StepTile {
 #pragma unroll
         for (int l = 0; l < L; ++l) f.x[l] = *reinterpret_cast<const bf16x8*>(&e[l][mine + to]);
         return f;
+    }
+    // The four values of a row from `at` on.
+    __device__ __forceinline__ f32x4 four(int at) const
+    {
+        f32x4 v;
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(&e[l][at]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+                v[2 * k] = l == 0 ? lo : v[2 * k] + lo;
+                v[2 * k + 1] = l == 0 ? hi : v[2 * k + 1] + hi;
+            }
+        }
+        return v;
     }
     // The transposed fragment over the 32 rows from `row`: lane l holds rows
     // 8 (l / 16) + 0..7 of column col + l % 16, or, kEights, of column
@@ -730,6 +748,7 @@ struct PassShared {
     StepTile<W, kLimbs<D>> a, b, c;
     StepTile<kChunk, kOperandLimbs<D>> ab;
     ChunkDecay decays[2];  // this chunk's, and the next one's as it is made
+    float own[kChunk];  // where dots are wanted: a_i . b_i, which ab then lacks
     float dot[W / 16][kChunk];
     float cross[W / 16];
 };
@@ -936,6 +955,10 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                     const bool in = (back ? o + r >= step : o + r <= step) && decay.m[o + r] == mi;
                     // (both factors chosen: ab may be NaN)
                     ab[r] = (in ? ab[r] : 0.0f) * (__builtin_amdgcn_exp2f(in ? d : 0.0f) * p.p_scale);
+                    if (kPrecise && o + r == step) {
+                        sh.own[step] = ab[r];
+                        ab[r] = 0.0f;
+                    }
                 }
             } else {
                 const bool in_order = back ? s0 > q0 : s0 < q0;
@@ -977,20 +1000,23 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
                 const int step = q * 16 + col;
                 const float in = from[step] * p.y_scale;
                 const Frag<LS> f = sh.ab.rows(q * 16, 0, lane);
+                const float own = kPrecise ? sh.own[step] : 0.0f;
                 float dot = 0.0f;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const f32x4 v = mma(fc[u], f, y[q][u] * in);
+                    f32x4 v = mma(fc[u], f, y[q][u] * in);
                     // Columns beyond dim are 0, unless a holds something that is not finite: 0 times that.
                     // Where kWide they are written by no one else, so such a result would stay in the tile,
                     // as c of later chunks.
                     const int c = c0 + u * 16 + group * 4;
                     if (kWide && c >= p.dc) continue;
+                    const int here = sh.c.at(col, c) + q * 16 * sh.c.kRow;
                     if constexpr (kPrecise) {
                         const f32x4 e = unpack4<D>(d[q][u]) * v;
                         dot += (e[0] + e[1]) + (e[2] + e[3]);
+                        v += sh.c.four(here) * own;
                     }
-                    Result<D, W, kWide>::put(low, high, sh.c.at(col, c) + q * 16 * sh.c.kRow, v, f32);
+                    Result<D, W, kWide>::put(low, high, here, v, f32);
                 }
                 if constexpr (kPrecise) {
                     dot += __shfl_xor(dot, 16);
@@ -1040,12 +1066,15 @@ __device__ __forceinline__ void run_pass(const RecurrenceArgs& x, const PassArgs
 }
 
 // Waves per SIMD that leave enough registers for nothing to spill: a reload in
-// the loop waits for every load before it, the next chunk's among them.
-template <class D, int W>
-constexpr int kPassWaves = W == 128 || kLimbs<D> == 3 ? 2 : 4;
+// the loop waits for every load before it, the next chunk's among them.  (The
+// backward kernels of 16-bit types at W = 64 spill some all the same, as did those
+// of f32 at three waves where not kWide; 256 x 128 f32 training 203 us at two
+// waves, 178 at three.)
+template <class D, int W, bool kWide>
+constexpr int kPassWaves = W == 128 || (kLimbs<D> == 3 && !kWide) ? 2 : kLimbs<D> == 3 ? 3 : 4;
 
 template <class D, int W, bool kWide>
-__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_forward(const RecurrenceArgs x)
+__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void recurrence_forward(const RecurrenceArgs x)
 {
     __shared__ PassShared<D, W> sh;
     run_pass<D, W, kWide, false, false>(x, x.pass[0], blockIdx.x, sh);
@@ -1057,7 +1086,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurren
 // steps of 16 heads of 128 x 128 in bf16: 347 us, bound like the forward pass
 // with two limbs per operand; 256 x 128 of 4 heads of 64 x 64 in f32: 130 us.
 template <class D, int W, bool kWide>
-__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurrence_backward(const RecurrenceArgs x)
+__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void recurrence_backward(const RecurrenceArgs x)
 {
     __shared__ PassShared<D, W> sh;
     const uint32_t block = blockIdx.x / 3, pass = blockIdx.x % 3;
@@ -1072,7 +1101,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void recurren
 // us per chunk of each block: the loads' way to LDS and two barriers.  Two
 // chunks between barriers measured the same (207.9 and 207.4 us for the call).
 template <class D, int W, bool kWide>
-__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W>)) void segment_states(const RecurrenceArgs x)
+__global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void segment_states(const RecurrenceArgs x)
 {
     __shared__ struct {
         StepTile<W, kLimbs<D>> b, c;

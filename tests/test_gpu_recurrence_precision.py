@@ -7,6 +7,13 @@ product passes through at most one such operand; M is the same sum over absolute
 values and n the number of fp32 roundings that one sum can collect:
 
     |x - ref| <= u |ref| + (2^-16 + n 2^-24) M + s
+
+The gradient of log_decay is a suffix sum over steps s of q_s.dq_s - k_s.dk_s
+without what a step has of itself, which cancels.  Each of these terms is off by
+at most 2^-16 of its sum A_s over absolute values, by roundings of its own; the
+sum of independent errors is taken as four times the root of the sum of their
+squares, and the fp32 roundings, which carried states share, as 2^-24 of the sum
+of A_s itself.
 """
 import pytest
 
@@ -74,3 +81,69 @@ def test_what_else_is_asked_for_changes_no_bits(dtype, t):
     g = lrs.compute_gated_recurrence_backward(c.do.cuda(), *args, **kw)
     g2 = lrs.compute_gated_recurrence_backward(c.do.cuda(), *args, **kw, want_initial_state=False)
     assert g2[4] is None and all(torch.equal(x, y) for x, y in zip(g[:4], g2[:4]))
+
+
+def decay_gradient_and_bound(c):
+    """The gradient of log_decay (one value head to a key head) and its bound without u |ref|."""
+    a, h0, dhT = absolute(c)
+    dg = ref.gated_recurrence_backward(c.do, *c.inputs(), c.reset, c.h0, c.dhT)[3]
+    M = ref.gated_recurrence_backward(c.do.abs(), *a, c.reset, h0, dhT)
+    q, k, v, do = (x.double().abs() for x in (c.q, c.k, c.v, c.do))
+    own = c.q.shape[3] ** -0.5 * (q * k).sum(-1) * (do * v).sum(-1)
+    A = (q * M[0]).sum(-1) + (k * M[1]).sum(-1) - 2 * own
+    cut = torch.isneginf(c.g)
+    if c.reset is not None:
+        cut = cut | c.reset[..., None]
+    _, MS, _, _ = ref.gated_recurrence(*a, c.reset, h0)
+    end = 0 * A[:, 0] if dhT is None else (MS * dhT).sum((-1, -2))
+    square, linear, bound = 0 * end, end.clone(), torch.empty_like(A)
+    for i in range(A.shape[1] - 1, -1, -1):
+        square, linear = square + A[:, i] ** 2, linear + A[:, i]
+        bound[:, i] = torch.where(cut[:, i], 0.0, 4 * 2.0 ** -16 * square.sqrt() + 2.0 ** -24 * linear)
+        square, linear = torch.where(cut[:, i], 0.0, square), torch.where(cut[:, i], 0.0, linear)
+    return dg, bound
+
+
+def typical(x):
+    return x.square().mean().sqrt().item()
+
+
+@pytest.mark.parametrize("decay", [0.1, 1.0, 4.0, 12.0])
+@pytest.mark.parametrize("t", [300, 2100])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_decay_gradient_by_its_own_size(dtype, t, decay):
+    """Rows of one segment (many heads) whose steps all decay alike, weakly to strongly."""
+    c = Case(45, t, 2, 2, 8, 8, dtype, decay=(decay, decay * 1.01), state=False)
+    dg, bound = decay_gradient_and_bound(c)
+    assert typical(bound) < 0.25 * typical(dg)
+    near(c.backward()[3], dg, HALF_STEP[dtype] * dg.abs() + bound, "grad_log_decay")
+
+
+@pytest.mark.parametrize("shape", [(1, 3000, 2, 2, 64, 64), (1, 2111, 1, 1, 128, 128), (2, 200, 2, 2, 40, 72)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_decay_gradient_over_segments(dtype, shape):
+    c = Case(*shape, dtype, reset=0.005, decay=(0.02, 0.5))
+    dg, bound = decay_gradient_and_bound(c)
+    assert typical(bound) < 0.25 * typical(dg)
+    near(c.backward()[3], dg, HALF_STEP[dtype] * dg.abs() + bound, "grad_log_decay")
+
+
+@pytest.mark.parametrize("n", [1, 90])
+@pytest.mark.parametrize("at", [31, 32, 64, 65, 127, 128, 511, 512, 1023, 1024, 1089])
+def test_decay_gradient_up_to_a_reset_and_after_it(at, n):
+    """Rows that start again at a step are two rows: at the ends of chunks, windows, waves, segments."""
+    t = 1500
+    c = Case(n, t, 1, 1, 16, 8, torch.float32, decay=(0.05, 0.3))
+    c.reset = torch.zeros(n, t, dtype=torch.bool)
+    c.reset[:, at] = True
+    dg, bound = decay_gradient_and_bound(c)
+    assert typical(bound) < 0.25 * typical(dg)
+    args, do = [x.cuda() for x in c.inputs()], c.do.cuda()
+    one = lrs.compute_gated_recurrence_backward(do[:, :at], *(x[:, :at] for x in args), initial_state=c.h0.cuda())
+    two = lrs.compute_gated_recurrence_backward(do[:, at:], *(x[:, at:] for x in args),
+                                                reset=c.reset[:, at:].cuda(), grad_final_state=c.dhT.cuda())
+    got = c.backward()[3]
+    parts = torch.cat([one[3], two[3]], 1).double().cpu()
+    near(got, parts, 2 * (HALF_STEP[c.dtype] * parts.abs() + bound), "grad_log_decay")
+    assert (got[:, at] == 0).all()
