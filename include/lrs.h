@@ -661,8 +661,10 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
  *     inputs and outputs alike (forward: q, k, v, log_decay, reset, out;
  *     backward: grad_out, q, k, v, log_decay, reset, grad_q, grad_k, grad_v,
  *     grad_log_decay; reset's head stride is ignored).  Elements of a row are
- *     consecutive.  Views of one projection buffer and time-major arrays are
- *     read and written in place; outputs must address every element once.
+ *     consecutive.  Inputs may be views of one projection buffer, and any array
+ *     may be time-major.  An output must address every element once, and from
+ *     its first to its last element share no memory with another array: two
+ *     outputs interleaved in one buffer are refused.
  *     Strides, bases and dims that keep every row on 16 bytes are fastest.
  *   - key_dim and value_dim 1 to 128; heads a multiple of kv_heads, at most
  *     65536; N * heads at most 2^21; N and T as above.
@@ -672,6 +674,7 @@ lrs_status lrs_affine_scan_tm_f16(int64_t num_envs, int64_t seq_len,
  *     overflows, makes NaN or infinities of what it has a part in -- out from
  *     this step on, the gradients of q, k and v up to it or from it on, that
  *     of log_decay in the whole episode -- and of nothing beyond its episode.
+ *     In f32 magnitudes from 3.3962e38 on (2^128 in 8 bits) count as infinite.
  *   - Sums and states are fp32 (or more); outputs are rounded once.  What is
  *     made on the way and multiplied again (weighted products, a state that a
  *     query reads) keeps at least 16 bits in the 16-bit variants and 24 in
@@ -767,6 +770,8 @@ lrs_status lrs_gated_recurrence_step_f16(int64_t num_envs, int64_t heads, int64_
  *     grad_k).
  *   - dim 1 to 256; rotary_dim even, 0 (no rotation: table and positions may
  *     be NULL) to dim; heads 1 to 65536 each; eps >= 0.
+ *   - mean(x^2) is taken in fp32: a head with elements beyond 2^59, or with eps 0
+ *     one whose elements are all below 2^-63, is out of its range.
  * Backward: the gradients of q and k, and those of the weights summed over
  * every token and head in a fixed order (all outputs required); workspace
  * lrs_qk_norm_rotation_workspace_bytes(...) bytes, any contents.          */

@@ -103,9 +103,12 @@ constexpr int kLimbs = std::is_same<D, bf16_t>::value ? 1 : std::is_same<D, f16_
 
 // Tiles of 16 columns that a wave holds of the state (W: its padded dimension,
 // 64 or 128), and the threads of a block.  Two tiles halve the reads of the
-// shared fragments per product; one tile leaves room for twice the waves, which
-// is worth more where several limbs fill LDS and registers: 4096 x 128, f16,
-// 439 us with two and 338 with one; 32768 steps of bf16, W = 128, 204 and 239.
+// shared fragments per product; one tile leaves room for twice the waves.  bf16
+// at W = 128: 32768 steps forward 239 us with two and 282 with one, 8 x 2048
+// backward 344 and 489.  f16 at W = 128, which takes one: 16384 steps of 8 heads
+// 349 us backward with one and 284 with two, 3 x 1001 forward 41 and 48.  f32's
+// three limbs leave no registers for two; W = 64 needs the four waves that one
+// tile each gives it, for the four tiles of a b^T.
 template <class D, int W>
 constexpr int kCols = W == 128 && kLimbs<D> == 1 ? 2 : 1;
 template <class D, int W>
@@ -202,10 +205,11 @@ using ColumnFrags = Frag<kLimbs<D>>[kCols<D, W>];
 // values that a matrix instruction sums over are taken in order, eight to a
 // group of 16 lanes, by both operands.  Rows are an odd number of 16-byte units
 // long, and the rows of each 16 are laid out 0, 4, 1, 5, ... and 8 below, so
-// that a fragment by rows (16 rows at one unit) and one by columns (rows 0..3
-// and 8..11 at two neighbouring units, transposed) touch every bank once, and
-// every fragment lies at a constant distance from one address per lane.  (The
-// fragments in eights read half of each unit, at half the rate.)
+// that every fragment lies at a constant distance from one address per lane, and
+// a fragment by rows (16 rows at one unit) and one by columns (rows 0..3 and
+// 8..11 at two neighbouring units, transposed) spread over all banks.  The
+// fragments in eights read half of each unit: with them 32% of the cycles that
+// LDS is busy in recurrence_forward (bf16, W = 128) are conflicts.
 constexpr int kChunk = 32;
 constexpr int kTile = 16;
 
@@ -397,7 +401,9 @@ struct Staged {
 // its next Staged::put(), and store() writes it out.  Stores go out before the
 // next loads start: the wait for the loads would otherwise be one for the
 // stores as well, which are slower to be acknowledged (a pass of 32768 steps of
-// 16 heads took 150 us where they came between).
+// 16 heads took a quarter longer where they came between).  move(), for the
+// partial gradients of shared heads in 16-bit types, stores right before that
+// wait all the same: its fp32 rows are twice what the registers would hold.
 template <class D, int W, bool kWide>
 struct Result {
     static constexpr int kUnits = Staged<D, W, kWide>::kUnits, kApart = Staged<D, W, kWide>::kApart;
@@ -662,8 +668,8 @@ __device__ __forceinline__ void add_chunk(StateTiles<D, W>& S, const StepTile<W,
 // weight in, as NaN, and no others: a product with a weight of 0 would be NaN
 // too.  Which tells whether a wave's columns hold one: their product with zeros.
 // Of a chunk of finite steps this is all that is done, early enough for the
-// branch on it not to wait (256 x 128 f32, both directions: 195 us with the
-// branch right behind the product, 172 so, 170 without).
+// branch on it not to wait (256 x 128 f32, both directions: 1% longer than without,
+// 15% with the branch right behind the product).
 template <class D, int W>
 __device__ __forceinline__ f32x4 times_zero(const StepTile<W, kLimbs<D>>& tc, int c0, int lane)
 {
@@ -736,13 +742,12 @@ __device__ __forceinline__ void part_nonfinite(ColumnFrags<D, W>& fc, const Step
 // What bounds it: a step of the chain.  The state's registers leave two waves
 // per SIMD at W = 128, and a chunk is a chain of LDS reads, products, weights,
 // a barrier, products again: of 32768 steps of 16 heads of 128 x 128 in bf16
-// (about 120 us; 34 GFLOP with the segments' states) the vector
-// unit is busy for 36% of the cycles, LDS for 40%, the matrix unit for 27%, and
-// no two of them much at once.  Chunks of 32 steps rather than 64: the longer
+// (172 us traced; 34 GFLOP with the segments' states) the vector unit is issued to
+// in 42% of the cycles, LDS is busy for 33%, the matrix unit for 28%, and no two
+// of them much at once.  Chunks of 32 steps rather than 64: the longer
 // ones do half the barriers, but their operands spill.  A second set of LDS
-// tiles, which saves one of the three barriers, measured slower (32768 steps
-// 204 -> 225 us, 8 x 2048 both directions 488 -> 541), as did three waves per
-// SIMD by smaller register budgets (206 -> 241).
+// tiles, which saves one of the three barriers, measured 10% slower, three waves
+// per SIMD by smaller register budgets 17%.
 template <class D, int W>
 struct PassShared {
     StepTile<W, kLimbs<D>> a, b, c;
@@ -1083,8 +1088,8 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void r
 // The three passes of the backward call: dq and dk with q.dq and k.dk to a
 // precision that their differences keep, and dv.  Blocks of the three passes of
 // a segment are neighbours: they read the same steps, mostly from L2.  8 x 2048
-// steps of 16 heads of 128 x 128 in bf16: 347 us, bound like the forward pass
-// with two limbs per operand; 256 x 128 of 4 heads of 64 x 64 in f32: 130 us.
+// steps of 16 heads of 128 x 128 in bf16: 343 us, bound like the forward pass;
+// 256 x 128 of 4 heads of 64 x 64 in f32: 137 us.
 template <class D, int W, bool kWide>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void recurrence_backward(const RecurrenceArgs x)
 {
@@ -1097,9 +1102,9 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void r
 
 // The state that one segment alone leaves (from zero), and its decay, by the
 // same products; the last segment in scan order leaves none that is used.
-// 32768 steps of 16 heads of 128 x 128 in bf16, 32 segments: 77 us, that is 2.2
+// 32768 steps of 16 heads of 128 x 128 in bf16, 32 segments: 80 us, that is 2.5
 // us per chunk of each block: the loads' way to LDS and two barriers.  Two
-// chunks between barriers measured the same (207.9 and 207.4 us for the call).
+// chunks between barriers measured the same.
 template <class D, int W, bool kWide>
 __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void segment_states(const RecurrenceArgs x)
 {
@@ -1186,7 +1191,7 @@ __global__ __launch_bounds__((kThreads<D, W>), (kPassWaves<D, W, kWide>)) void s
 // order: in[s] = own[s - 1] + total[s - 1] in[s - 1].  A thread per element;
 // the loads of kAhead segments are in flight together.  Bound by the states'
 // bytes, read and written once: 16 heads of 128 x 128, 32 segments, 67 MB in
-// 14.6 us (4.6 TB/s).
+// 14.7 us (4.6 TB/s).
 constexpr int kAhead = 8;
 
 template <class D>
@@ -1226,7 +1231,7 @@ __global__ __launch_bounds__(256) void join_segments(const RecurrenceArgs x)
 // 0.  The windows of 64 depend on each other through one value, and each waits
 // for its loads: a long segment is split over up to kDecayWaves waves, each of
 // which first sums what its steps hand on (those before their first cut).
-// 128 segments of 2048 steps, bf16: 33.6 us by one wave each, 13.6 by eight.
+// 128 segments of 2048 steps, bf16: 33.6 us by one wave each, 12.8 by eight.
 struct DecayGradArgs {
     SeqView g, reset, dg;
     const float *qdq, *kdk, *cross;
@@ -1303,7 +1308,9 @@ __global__ __launch_bounds__(kDecayWaves * kWave) void decay_grad(const DecayGra
 }
 
 // Sums the value heads' gradients of a shared query or key head, in a fixed
-// order (3 x 1001 steps, 6 heads: 4.6 us): part [N, T, H, dim] in fp32 to y [N, T, H / group, dim].
+// order: part [N, T, H, dim] in fp32 to y [N, T, H / group, dim].  3 x 1001 steps
+// of 6 heads: 4.6 us; 8 x 2048 of 16 heads of 128 over 4: 50 us (3 TB/s) for each
+// of dq and dk, beside 360 for the passes, whose fp32 results it reads back.
 struct SharedSumArgs {
     const float* part;
     SeqView y;
@@ -1417,14 +1424,22 @@ inline lrs_status check_state(const char* nm, const void* p, const char* what)
 inline size_t round_up(size_t b) { return (b + 255) & ~size_t(255); }
 
 // How a call is cut up, and its workspace.  A pass has a block per head and
-// segment: as many segments as fill the chip's kFillBlocks places (two blocks on
-// each of 256 CUs) once, and no more, of at least kMinSegment steps.  Segments
-// cost one more reading of two of the arrays and states written and read twice,
-// and a second round of blocks is as long as the first (training, forward and
-// backward: 8 x 2048 steps of 16 heads with 1 segment in the backward pass 446
-// us, 2 521, 3 493, 4 501, 8 567; 16384 steps of 8 heads 16: 316, 21: 294, 32:
-// 318, 43: 305; 32768 steps of 16 heads forward 16: 260, 32: 204, 64: 240; 3 x
-// 1001 steps of 6 heads with segments of 256: 139, 128: 119, 64: 131).
+// segment: as many segments as make kFillBlocks blocks, and no more, of at least
+// kMinSegment steps.  Segments cost one more reading of two of the arrays and
+// states written and read twice.  512 blocks are two on each of 256 CUs, all that
+// bf16 at W = 128 has room for, and a second round is as long as the first; f16
+// and f32 at W = 128 have room for one on each, f32 at W = 64 for three, 16-bit
+// types there for four, and take the same number:
+//   backward, bf16, 8 x 2048 of 16 heads of 128 x 128: 1 segment 345 us, 2 427, 3
+//   408, 4 404, 8 476; 16384 of 8 heads 16: 253, 21: 227, 32: 256, 64: 259;
+//   forward 32768 of 16 heads 16: 316, 32: 238, 64: 265;
+//   16384 steps of 8 heads of 128 x 128, forward and backward, f32 10: 400 and
+//   487, 21: 209 and 458, 32: 151 and 446, 64: 160 and 490; f16 21: 156 and 349,
+//   32: 116 and 335, 64: 123 and 381;
+//   of 64 x 64 in bf16 21: 87 and 136, 32: 64 and 111, 64: 53 and 116 (the rule
+//   takes 64 and 21: a fifth is left there in the backward call);
+//   3 x 1001 steps of 6 heads of 72 x 40 in f16 4: 62 and 90, 8: 40 and 87, 16: 46
+//   and 100.
 // Workspace: the states before each segment and the segments' decays, per
 // direction; backward also q.dq and k.dk [N, H, T], <S, dS> [N, H, segments]
 // and, for shared query and key heads, each value head's dq and dk.

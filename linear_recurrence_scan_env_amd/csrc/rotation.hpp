@@ -43,7 +43,10 @@ struct NormArgs {
 constexpr int kNormWaves = 4;
 
 // For rows that are not on 16 bytes, or pairs that do not lie in whole 16-byte
-// units: one wave per row, an element per lane and access; the pairs meet in LDS.
+// units (halves of rotary_dim that are not a multiple of a unit: 24 of 96 in 16-bit
+// types): one wave per row, an element per lane and access; the pairs meet in LDS.
+// 32768 tokens of 32 + 8 heads of 96 in bf16, 24 of them rotated: 503 MB in 596 us
+// (0.8 TB/s), bound by the loads' width.
 template <class D, bool kBackward>
 __global__ __launch_bounds__(kNormWaves * kWave) void norm_rotation(const NormArgs x)
 {

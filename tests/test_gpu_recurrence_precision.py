@@ -3,8 +3,10 @@ operands made on the way of at least 16 bits, results rounded once.
 
 Tolerances.  u is half a rounding step of the storage type.  An fp32 value kept
 as two bf16 parts (8 bits each) is off by at most 2^-16 of itself, and each
-product passes through at most one such operand; M is the same sum over absolute
-values and n the number of fp32 roundings that one sum can collect:
+product passes through at most one such operand (f16 inputs are two parts
+themselves; what the product of two second parts adds, 2^-16 at most and of
+either sign, is left to the same term); M is the same sum over absolute values
+and n the number of fp32 roundings that one sum can collect:
 
     |x - ref| <= u |ref| + (2^-16 + n 2^-24) M + s
 
