@@ -273,36 +273,6 @@ struct StepTile {
 // The rows of the state that a wave holds in tile k: four from here on.
 __device__ __forceinline__ int state_row(int k, int group) { return (k >> 1) * 32 + group * 8 + (k & 1) * 4; }
 
-// Eight elements of a row from column c on as they are stored, zero beyond
-// `dim`; `vec`: the bytes that an access may take (16, 4 or one element).
-template <class D>
-struct Raw8 {
-    u32x4 w[sizeof(D) / 2];
-};
-
-template <class D>
-__device__ __forceinline__ Raw8<D> load8(const D* row, int c, int dim, int vec)
-{
-    Raw8<D> v = {};
-    if (vec == 16 && c + 8 <= dim) {
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(D) / 2; ++k)
-            v.w[k] = *reinterpret_cast<const u32x4*>(row + c + k * (16 / sizeof(D)));
-    } else if (sizeof(D) == 4 || vec >= 4) {
-        const uint32_t* const words = reinterpret_cast<const uint32_t*>(row + c);
-        constexpr int per = 4 / sizeof(D);
-#pragma unroll
-        for (int k = 0; k < 8 / per; ++k)
-            if (c + k * per < dim) v.w[k / 4][k % 4] = words[k];
-    } else {
-        const uint16_t* const halves = reinterpret_cast<const uint16_t*>(row + c);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (c + k < dim) v.w[0][k / 2] |= (uint32_t)halves[k] << (16 * (k & 1));
-    }
-    return v;
-}
-
 template <class D, int W>
 __device__ __forceinline__ void put8(StepTile<W, kLimbs<D>>& tile, int at, const Raw8<D>& v)
 {

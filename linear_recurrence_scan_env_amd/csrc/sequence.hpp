@@ -29,6 +29,36 @@ __device__ __forceinline__ D* seq_row_out(const SeqView& v, int64_t n, int64_t t
     return const_cast<D*>(seq_row<D>(v, n, t, h));
 }
 
+// Eight elements of a row from column c on as they are stored, zero beyond
+// `dim`; `vec`: the bytes that an access may take (16, 4 or one element).
+template <class D>
+struct Raw8 {
+    u32x4 w[sizeof(D) / 2];
+};
+
+template <class D>
+__device__ __forceinline__ Raw8<D> load8(const D* row, int c, int dim, int vec)
+{
+    Raw8<D> v = {};
+    if (vec == 16 && c + 8 <= dim) {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(D) / 2; ++k)
+            v.w[k] = *reinterpret_cast<const u32x4*>(row + c + k * (16 / sizeof(D)));
+    } else if (sizeof(D) == 4 || vec >= 4) {
+        const uint32_t* const words = reinterpret_cast<const uint32_t*>(row + c);
+        constexpr int per = 4 / sizeof(D);
+#pragma unroll
+        for (int k = 0; k < 8 / per; ++k)
+            if (c + k * per < dim) v.w[k / 4][k % 4] = words[k];
+    } else {
+        const uint16_t* const halves = reinterpret_cast<const uint16_t*>(row + c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k < dim) v.w[0][k / 2] |= (uint32_t)halves[k] << (16 * (k & 1));
+    }
+    return v;
+}
+
 // One array argument of a sequence call, as checked on the host.
 struct SeqArg {
     const void* p;
@@ -37,6 +67,7 @@ struct SeqArg {
     bool out;
     bool required;
     const char* what;
+    int64_t steps = 0;  // where its steps are not the call's T
 };
 
 constexpr int64_t kMaxSeqExtent = int64_t(1) << 60;
@@ -80,8 +111,9 @@ lrs_status check_seq_arrays(const char* nm, int64_t N, int64_t T, const SeqArg (
         }
         if ((uintptr_t)a.p % a.elem_bytes != 0)
             return fail(LRS_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", nm, a.what);
-        const int64_t size[3] = {N, T, a.heads};
-        int64_t st[3] = {T * a.heads * a.dim, a.heads * a.dim, a.dim};
+        const int64_t steps = a.steps != 0 ? a.steps : T;
+        const int64_t size[3] = {N, steps, a.heads};
+        int64_t st[3] = {steps * a.heads * a.dim, a.heads * a.dim, a.dim};
         int64_t extent = a.dim;
         for (int k = 0; k < 3; ++k) {
             if (strides != nullptr && strides[3 * i + k] != 0) st[k] = strides[3 * i + k];
