@@ -816,6 +816,215 @@ lrs_status lrs_qk_norm_rotation_backward_f16(int64_t num_envs, int64_t seq_len, 
     lrs_f16* grad_k_weight, const int64_t* strides, void* workspace, size_t workspace_bytes,
     hipStream_t stream);
 
+/* Attention over a window of steps and the first steps of each episode.  Per
+ * environment and head (key head h / (heads / kv_heads)), with e(i) the first
+ * step of i's episode, query step i sees key step j where
+ *
+ *   e(i) <= j <= i  and  (j > i - window or j < e(i) + sinks)
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij)   over the j seen
+ *   out_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ * Steps are counted along the keys; the queries are the keys' last query_steps.
+ *   - Arrays: q [N, T, heads, key_dim], k [N, TK, kv_heads, key_dim], v [N, TK,
+ *     kv_heads, value_dim], out [N, T, heads, value_dim] of one storage type;
+ *     reset [N, TK] u8 (nullable), nonzero at the first step of an episode (the
+ *     first step of a row counts as one); lse [N, T, heads] float32 (nullable
+ *     in the forward call: not written).
+ *   - strides: as for the gated recurrence, in signature order (reset's head
+ *     stride is ignored; lse's elements are rows of one).  Strides, bases and
+ *     dims that keep every row on 16 bytes are fastest.
+ *   - key_dim and value_dim 1 to 128; heads a multiple of kv_heads, at most
+ *     65536; window at least 1, sinks 0 or more, any size; scale finite, not 0.
+ *   - What a query does not see has no part in its result, NaN and infinities
+ *     included; what it sees is computed as written.
+ *   - Softmax sums are fp32.  In the 16-bit variants weights and their
+ *     gradients are rounded to the type before they multiply rows.  A call gives
+ *     the same bits every time.
+ *   - workspace: lrs_windowed_attention_workspace_bytes(...) bytes, 16-byte
+ *     aligned, any contents; NULL with 0 bytes where that is 0.  Nothing in it
+ *     outlives the call's kernels.
+ *
+ * Backward: the gradients of q, k and v (those of k and v summed over the heads
+ * that share them; 0 for key steps that no query sees) from grad_out and the
+ * forward call's out and lse.
+ *
+ * Step: one step of every environment over caches [N, slots, kv_heads, ...] with
+ * slots = sinks + window, updated in place.  positions [N] i32, consecutive: the
+ * step's place p in its episode.  k and v go into slot p (p < sinks) or sinks +
+ * (p - sinks) % window, and the query sees the first min(p + 1, slots) slots.
+ * p < 0: the caches are left alone and out is 0.  q [N, heads, key_dim], k, v
+ * [N, kv_heads, ...], out [N, heads, value_dim]; strides with the step stride
+ * ignored but for the caches, whose steps are the slots, and positions, which
+ * have none.
+ *
+ * Fill: the slots of the caches that the steps of k and v [N, T, kv_heads, ...]
+ * would have left there step by step: positions [N, T] i32, of which the last of
+ * each row counts; the steps before it are taken to be its episode's.  Slots
+ * whose steps lie before the row are left alone; so is everything of a row whose
+ * last position is negative.                                              */
+size_t lrs_windowed_attention_workspace_bytes(int64_t num_envs, int64_t query_steps, int64_t key_steps,
+    int64_t heads, int64_t kv_heads, int64_t key_dim, int64_t value_dim, int64_t window, int64_t sinks,
+    int has_reset, int backward);
+size_t lrs_windowed_attention_step_workspace_bytes(int64_t num_envs, int64_t heads, int64_t kv_heads,
+    int64_t slots, int64_t sinks, int64_t key_dim, int64_t value_dim);
+lrs_status lrs_windowed_attention_f32(int64_t num_envs, int64_t query_steps, int64_t key_steps,
+    int64_t heads, int64_t kv_heads, int64_t key_dim, int64_t value_dim, int64_t window, int64_t sinks,
+    const float* q, const float* k, const float* v, const uint8_t* reset, float scale, float* out,
+    float* lse, const int64_t* strides, void* workspace, size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_windowed_attention_backward_f32(int64_t num_envs, int64_t query_steps, int64_t key_steps,
+    int64_t heads, int64_t kv_heads, int64_t key_dim, int64_t value_dim, int64_t window, int64_t sinks,
+    const float* grad_out, const float* q, const float* k, const float* v, const uint8_t* reset,
+    const float* out, const float* lse, float scale, float* grad_q, float* grad_k, float* grad_v,
+    const int64_t* strides, void* workspace, size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_windowed_attention_step_f32(int64_t num_envs, int64_t heads, int64_t kv_heads,
+    int64_t slots, int64_t sinks, int64_t key_dim, int64_t value_dim, const float* q, const float* k,
+    const float* v, float* key_cache, float* value_cache, const int32_t* positions, float scale,
+    float* out, const int64_t* strides, void* workspace, size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_windowed_attention_fill_f32(int64_t num_envs, int64_t seq_len, int64_t kv_heads,
+    int64_t slots, int64_t sinks, int64_t key_dim, int64_t value_dim, const float* k, const float* v,
+    const int32_t* positions, float* key_cache, float* value_cache, const int64_t* strides,
+    hipStream_t stream);
+lrs_status lrs_windowed_attention_bf16(int64_t num_envs, int64_t query_steps, int64_t key_steps,
+    int64_t heads, int64_t kv_heads, int64_t key_dim, int64_t value_dim, int64_t window, int64_t sinks,
+    const lrs_bf16* q, const lrs_bf16* k, const lrs_bf16* v, const uint8_t* reset, float scale,
+    lrs_bf16* out, float* lse, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+lrs_status lrs_windowed_attention_backward_bf16(int64_t num_envs, int64_t query_steps,
+    int64_t key_steps, int64_t heads, int64_t kv_heads, int64_t key_dim, int64_t value_dim,
+    int64_t window, int64_t sinks, const lrs_bf16* grad_out, const lrs_bf16* q, const lrs_bf16* k,
+    const lrs_bf16* v, const uint8_t* reset, const lrs_bf16* out, const float* lse, float scale,
+    lrs_bf16* grad_q, lrs_bf16* grad_k, lrs_bf16* grad_v, const int64_t* strides, void* workspace,
+    size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_windowed_attention_step_bf16(int64_t num_envs, int64_t heads, int64_t kv_heads,
+    int64_t slots, int64_t sinks, int64_t key_dim, int64_t value_dim, const lrs_bf16* q,
+    const lrs_bf16* k, const lrs_bf16* v, lrs_bf16* key_cache, lrs_bf16* value_cache,
+    const int32_t* positions, float scale, lrs_bf16* out, const int64_t* strides, void* workspace,
+    size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_windowed_attention_fill_bf16(int64_t num_envs, int64_t seq_len, int64_t kv_heads,
+    int64_t slots, int64_t sinks, int64_t key_dim, int64_t value_dim, const lrs_bf16* k,
+    const lrs_bf16* v, const int32_t* positions, lrs_bf16* key_cache, lrs_bf16* value_cache,
+    const int64_t* strides, hipStream_t stream);
+lrs_status lrs_windowed_attention_f16(int64_t num_envs, int64_t query_steps, int64_t key_steps,
+    int64_t heads, int64_t kv_heads, int64_t key_dim, int64_t value_dim, int64_t window, int64_t sinks,
+    const lrs_f16* q, const lrs_f16* k, const lrs_f16* v, const uint8_t* reset, float scale,
+    lrs_f16* out, float* lse, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+lrs_status lrs_windowed_attention_backward_f16(int64_t num_envs, int64_t query_steps, int64_t key_steps,
+    int64_t heads, int64_t kv_heads, int64_t key_dim, int64_t value_dim, int64_t window, int64_t sinks,
+    const lrs_f16* grad_out, const lrs_f16* q, const lrs_f16* k, const lrs_f16* v, const uint8_t* reset,
+    const lrs_f16* out, const float* lse, float scale, lrs_f16* grad_q, lrs_f16* grad_k,
+    lrs_f16* grad_v, const int64_t* strides, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+lrs_status lrs_windowed_attention_step_f16(int64_t num_envs, int64_t heads, int64_t kv_heads,
+    int64_t slots, int64_t sinks, int64_t key_dim, int64_t value_dim, const lrs_f16* q,
+    const lrs_f16* k, const lrs_f16* v, lrs_f16* key_cache, lrs_f16* value_cache,
+    const int32_t* positions, float scale, lrs_f16* out, const int64_t* strides, void* workspace,
+    size_t workspace_bytes, hipStream_t stream);
+lrs_status lrs_windowed_attention_fill_f16(int64_t num_envs, int64_t seq_len, int64_t kv_heads,
+    int64_t slots, int64_t sinks, int64_t key_dim, int64_t value_dim, const lrs_f16* k,
+    const lrs_f16* v, const int32_t* positions, lrs_f16* key_cache, lrs_f16* value_cache,
+    const int64_t* strides, hipStream_t stream);
+
+/* Log probabilities of actions, and the clipped policy loss with a KL term.  Per
+ * token with logits z, z' = z / temperature and p = softmax(z'):
+ *
+ *   lse = log sum_v exp(z'_v),  lp = z'_action - lse,  H = -sum_v p_v log p_v
+ *   r = exp(lp - old_log_prob),  d = ref_log_prob - lp
+ *   loss = -min(r A, clamp(r, 1 - clip, 1 + clip_high) A)
+ *          + kl_coef (exp(d) - d - 1) - entropy_coef H
+ *
+ *   - Arrays: logits, grad_logits [N, T, num_actions] of one storage type;
+ *     actions [N, T] i64; mask [N, T] u8 (nullable); everything else per token
+ *     [N, T] float32 in every variant: old_log_probs, advantages,
+ *     ref_log_probs (nullable where kl_coef is 0, and not read then), weights
+ *     (nullable = 1), and the results.
+ *   - strides: as for the gated recurrence, in signature order, the head stride
+ *     ignored; num_actions is the row of the logits.  Rows may start on any
+ *     element; a gradient whose rows lie on the same bytes modulo 16 as those
+ *     of the logits is written in 16-byte units.
+ *   - num_actions 1 to 2^24; temperature > 0; clip and clip_high >= 0; all
+ *     coefficients finite.
+ *   - Logits of -infinity have probability 0 and gradient 0.  NaN or +infinity,
+ *     a token whose logits are all -infinity, and an action outside 0 ..
+ *     num_actions - 1 make NaN of the token's results and of its row of the
+ *     gradient.  A token whose mask is 0 has zeros for everything and nothing of
+ *     it is used.
+ *   - Sums are fp32; a gradient is rounded once.  A call gives the same bits
+ *     every time.  There is no workspace.
+ *
+ * The backward calls take the entropy and lse of the forward call with the same
+ * inputs.  The gradient of the clipped term is that of r A where r has not
+ * passed the bound that A's sign makes it stop at (1 + clip_high for A >= 0,
+ * 1 - clip for A < 0), and 0 beyond it.  lrs_policy_loss_and_gradient reads the
+ * logits once for the loss and for the gradient of sum(weights * loss) (rows of
+ * more than 16384 16-byte units are read twice).                          */
+lrs_status lrs_action_log_probs_f32(int64_t num_envs, int64_t seq_len, int64_t num_actions, const float*
+    logits, const int64_t* actions, const uint8_t* mask, float temperature, float* log_probs, float*
+    entropy, float* lse, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_action_log_probs_backward_f32(int64_t num_envs, int64_t seq_len, int64_t num_actions,
+    const float* grad_log_probs, const float* grad_entropy, const float* logits, const int64_t* actions,
+    const uint8_t* mask, float temperature, const float* entropy, const float* lse, float* grad_logits,
+    const int64_t* strides, hipStream_t stream);
+lrs_status lrs_policy_loss_f32(int64_t num_envs, int64_t seq_len, int64_t num_actions, const float*
+    logits, const int64_t* actions, const float* old_log_probs, const float* advantages, const float*
+    ref_log_probs, const uint8_t* mask, float clip, float clip_high, float kl_coef, float entropy_coef,
+    float temperature, float* loss, float* log_probs, float* entropy, float* lse, const int64_t*
+    strides, hipStream_t stream);
+lrs_status lrs_policy_loss_backward_f32(int64_t num_envs, int64_t seq_len, int64_t num_actions, const
+    float* grad_loss, const float* logits, const int64_t* actions, const float* old_log_probs, const
+    float* advantages, const float* ref_log_probs, const uint8_t* mask, float clip, float clip_high,
+    float kl_coef, float entropy_coef, float temperature, const float* entropy, const float* lse, float*
+    grad_logits, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_policy_loss_and_gradient_f32(int64_t num_envs, int64_t seq_len, int64_t num_actions,
+    const float* logits, const int64_t* actions, const float* old_log_probs, const float* advantages,
+    const float* ref_log_probs, const uint8_t* mask, const float* weights, float clip, float clip_high,
+    float kl_coef, float entropy_coef, float temperature, float* loss, float* log_probs, float* entropy,
+    float* grad_logits, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_action_log_probs_bf16(int64_t num_envs, int64_t seq_len, int64_t num_actions, const
+    lrs_bf16* logits, const int64_t* actions, const uint8_t* mask, float temperature, float* log_probs,
+    float* entropy, float* lse, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_action_log_probs_backward_bf16(int64_t num_envs, int64_t seq_len, int64_t num_actions,
+    const float* grad_log_probs, const float* grad_entropy, const lrs_bf16* logits, const int64_t*
+    actions, const uint8_t* mask, float temperature, const float* entropy, const float* lse, lrs_bf16*
+    grad_logits, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_policy_loss_bf16(int64_t num_envs, int64_t seq_len, int64_t num_actions, const lrs_bf16*
+    logits, const int64_t* actions, const float* old_log_probs, const float* advantages, const float*
+    ref_log_probs, const uint8_t* mask, float clip, float clip_high, float kl_coef, float entropy_coef,
+    float temperature, float* loss, float* log_probs, float* entropy, float* lse, const int64_t*
+    strides, hipStream_t stream);
+lrs_status lrs_policy_loss_backward_bf16(int64_t num_envs, int64_t seq_len, int64_t num_actions, const
+    float* grad_loss, const lrs_bf16* logits, const int64_t* actions, const float* old_log_probs, const
+    float* advantages, const float* ref_log_probs, const uint8_t* mask, float clip, float clip_high,
+    float kl_coef, float entropy_coef, float temperature, const float* entropy, const float* lse,
+    lrs_bf16* grad_logits, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_policy_loss_and_gradient_bf16(int64_t num_envs, int64_t seq_len, int64_t num_actions,
+    const lrs_bf16* logits, const int64_t* actions, const float* old_log_probs, const float* advantages,
+    const float* ref_log_probs, const uint8_t* mask, const float* weights, float clip, float clip_high,
+    float kl_coef, float entropy_coef, float temperature, float* loss, float* log_probs, float* entropy,
+    lrs_bf16* grad_logits, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_action_log_probs_f16(int64_t num_envs, int64_t seq_len, int64_t num_actions, const
+    lrs_f16* logits, const int64_t* actions, const uint8_t* mask, float temperature, float* log_probs,
+    float* entropy, float* lse, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_action_log_probs_backward_f16(int64_t num_envs, int64_t seq_len, int64_t num_actions,
+    const float* grad_log_probs, const float* grad_entropy, const lrs_f16* logits, const int64_t*
+    actions, const uint8_t* mask, float temperature, const float* entropy, const float* lse, lrs_f16*
+    grad_logits, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_policy_loss_f16(int64_t num_envs, int64_t seq_len, int64_t num_actions, const lrs_f16*
+    logits, const int64_t* actions, const float* old_log_probs, const float* advantages, const float*
+    ref_log_probs, const uint8_t* mask, float clip, float clip_high, float kl_coef, float entropy_coef,
+    float temperature, float* loss, float* log_probs, float* entropy, float* lse, const int64_t*
+    strides, hipStream_t stream);
+lrs_status lrs_policy_loss_backward_f16(int64_t num_envs, int64_t seq_len, int64_t num_actions, const
+    float* grad_loss, const lrs_f16* logits, const int64_t* actions, const float* old_log_probs, const
+    float* advantages, const float* ref_log_probs, const uint8_t* mask, float clip, float clip_high,
+    float kl_coef, float entropy_coef, float temperature, const float* entropy, const float* lse,
+    lrs_f16* grad_logits, const int64_t* strides, hipStream_t stream);
+lrs_status lrs_policy_loss_and_gradient_f16(int64_t num_envs, int64_t seq_len, int64_t num_actions,
+    const lrs_f16* logits, const int64_t* actions, const float* old_log_probs, const float* advantages,
+    const float* ref_log_probs, const uint8_t* mask, const float* weights, float clip, float clip_high,
+    float kl_coef, float entropy_coef, float temperature, float* loss, float* log_probs, float* entropy,
+    lrs_f16* grad_logits, const int64_t* strides, hipStream_t stream);
+
 /* Diagnostics and tuning (process-wide; not for concurrent use).
  * force_lookback != 0: every later call takes the multi-block carry-
  *   propagation path, even where whole rows fit in one tile.

@@ -69,6 +69,15 @@ _SEQ_SIGS = {
     "lrs_qk_norm_rotation": [_I64] * 6 + [_P] * 5 + [_I64, _P, _F, ctypes.c_int] + [_P] * 4,
     "lrs_qk_norm_rotation_backward": [_I64] * 6 + [_P] * 7 + [_I64, _P, _F, ctypes.c_int] +
                                      [_P] * 4 + _TAIL,
+    "lrs_windowed_attention": [_I64] * 9 + [_P] * 4 + [_F] + [_P] * 2 + _TAIL,
+    "lrs_windowed_attention_backward": [_I64] * 9 + [_P] * 7 + [_F] + [_P] * 3 + _TAIL,
+    "lrs_windowed_attention_step": [_I64] * 7 + [_P] * 6 + [_F, _P] + _TAIL,
+    "lrs_windowed_attention_fill": [_I64] * 7 + [_P] * 7,
+    "lrs_action_log_probs": [_I64] * 3 + [_P] * 3 + [_F] + [_P] * 5,
+    "lrs_action_log_probs_backward": [_I64] * 3 + [_P] * 5 + [_F] + [_P] * 5,
+    "lrs_policy_loss": [_I64] * 3 + [_P] * 6 + [_F] * 5 + [_P] * 6,
+    "lrs_policy_loss_backward": [_I64] * 3 + [_P] * 7 + [_F] * 5 + [_P] * 5,
+    "lrs_policy_loss_and_gradient": [_I64] * 3 + [_P] * 7 + [_F] * 5 + [_P] * 6,
 }
 for _name, _args in _SEQ_SIGS.items():
     for _sfx in ("f32", "bf16", "f16"):
@@ -129,6 +138,10 @@ def load():
         lib.lrs_gated_recurrence_workspace_bytes.argtypes = [_I64] * 6 + [ctypes.c_int]
         lib.lrs_qk_norm_rotation_workspace_bytes.restype = _SZ
         lib.lrs_qk_norm_rotation_workspace_bytes.argtypes = [_I64] * 5
+        lib.lrs_windowed_attention_workspace_bytes.restype = _SZ
+        lib.lrs_windowed_attention_workspace_bytes.argtypes = [_I64] * 9 + [ctypes.c_int] * 2
+        lib.lrs_windowed_attention_step_workspace_bytes.restype = _SZ
+        lib.lrs_windowed_attention_step_workspace_bytes.argtypes = [_I64] * 7
         lib.lrs_debug_set_schedule.restype = ctypes.c_int
         lib.lrs_debug_set_schedule.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int]
         lib.lrs_debug_set_time_major_waves.argtypes = [ctypes.c_int]

@@ -1,0 +1,1478 @@
+// attention.hpp -- attention over a window of steps and the first steps of each
+// episode.  Per environment and head (key head h / (heads / kv_heads)), with
+// e(i) the first step of i's episode, query step i sees key step j where
+//
+//     e(i) <= j <= i   and   (j > i - window  or  j < e(i) + sinks)
+//
+// and with s_ij = scale q_i . k_j over the steps that it sees
+//
+//     lse_i = log sum_j e^{s_ij},   p_ij = e^{s_ij - lse_i},   o_i = sum_j p_ij v_j
+//     D_i = do_i . o_i,   ds_ij = scale p_ij (do_i . v_j - D_i)
+//     dq_i = sum_j ds_ij k_j,   dk_j = sum_i ds_ij q_i,   dv_j = sum_i p_ij do_i.
+//
+// What a query sees is two ranges of keys: the near one, from
+// max(e(i), i - window + 1) to i, and the far one, the episode's first steps
+// before that.  Queries follow each other, so a block of them sees one range of
+// near keys and one of far keys, and only tiles at their ends need the mask.
+//
+// All three kernels (forward, dq, dk and dv) have one form.  A wave holds 32
+// queries (or keys) as the columns of 32x32 matrix products; the other side comes
+// through LDS in tiles.  The scores arrive with a lane's own column in its
+// registers, so softmax statistics are per lane, and the weights go back as an
+// operand as they lie: the rows that a lane holds of a product, 8 (r / 4) +
+// 4 (lane / 32) + r % 4, are taken as the order of the sum, and the other operand
+// is read by columns of LDS in the same order.
+#pragma once
+
+#include "sequence.hpp"
+
+namespace lrs {
+
+constexpr int kMaxAttDim = 128;
+constexpr float kAttLog2e = 1.44269504088896341f;
+constexpr float kAttLn2 = 0.693147180559945309f;
+
+struct AttArgs {
+    SeqView q, k, v, o, lse;    // lse float32 [N, T, H], nullable in the forward
+    SeqView dout, dq, dk, dv;
+    const int32_t* starts;      // [N, TK]: the first step of each key step's episode; null: 0
+    float* delta;               // D, [N, H, T]
+    int64_t N;
+    int32_t T, TK, H, group, window, sinks, dim_k, dim_v;
+    int32_t hpb, tiles;         // heads per block, blocks per row of steps
+    uint8_t sum_delta;          // whether dq sums D itself
+    float scale, c;             // c = |scale| log2(e)
+};
+
+// ------------------------------------------------------- matrix instructions
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 abf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 af16x8 __attribute__((ext_vector_type(8)));
+typedef short as16x4 __attribute__((ext_vector_type(4)));
+
+// Eight values of one row or column of an operand: what a lane gives to a product
+// over 16 values (lanes 0..31 the first eight, 32..63 the others).
+template <class D>
+using AFrag = Raw8<D>;
+
+// acc += A B over 16 values.  float32 takes the matrix instructions of its own
+// type, two values at a time.
+template <class D>
+__device__ __forceinline__ f32x16 mma32(const AFrag<D>& a, const AFrag<D>& b, f32x16 acc)
+{
+    if constexpr (std::is_same<D, bf16_t>::value) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(abf16x8, a.w[0]),
+                                                       __builtin_bit_cast(abf16x8, b.w[0]), acc, 0, 0, 0);
+    } else if constexpr (std::is_same<D, f16_t>::value) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(af16x8, a.w[0]),
+                                                      __builtin_bit_cast(af16x8, b.w[0]), acc, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w[e / 4][e % 4]),
+                                                       __uint_as_float(b.w[e / 4][e % 4]), acc, 0, 0, 0);
+        return acc;
+    }
+}
+
+// The row that register r of a product holds for a lane of half h.
+__device__ __forceinline__ int acc_row(int r, int h) { return 8 * (r / 4) + 4 * h + r % 4; }
+
+// Registers 8u .. 8u + 7 as an operand: 16-bit types round the weights here, once
+// (to 2^-9 or 2^-12 of each; they are summed in float32 before that).
+template <class D>
+__device__ __forceinline__ AFrag<D> operand(const f32x16& v, int u)
+{
+    AFrag<D> f;
+    if constexpr (sizeof(D) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.w[e / 4][e % 4] = __float_as_uint(v[8 * u + e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.w[0][e] = pack2<D>(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
+    }
+    return f;
+}
+
+// What operand() left of the values, as a second operand.  ds goes into its products
+// as these two parts: with one, gradients of q and k in 16-bit types were off by 1.45
+// to 1.7 times the one rounding of the result.  Both use the same fragment of LDS.
+template <class D>
+__device__ __forceinline__ AFrag<D> operand_rest(const f32x16& v, int u, const AFrag<D>& f)
+{
+    AFrag<D> g;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        unpack2<D>(f.w[0][e], lo, hi);
+        g.w[0][e] = pack2<D>(v[8 * u + 2 * e] - lo, v[8 * u + 2 * e + 1] - hi);
+    }
+    return g;
+}
+
+// ------------------------------------------------------------- tiles in LDS
+// Rows of W elements without padding; 16-byte chunk c of row r lies at c ^ turn(r)
+// so that 16 rows at one chunk, and the reads by columns, spread over all banks.
+template <class D, int W>
+struct AttTile {
+    static constexpr int kRow = W * (int)sizeof(D);
+    static __device__ __forceinline__ int turn(int r)
+    {
+        if constexpr (sizeof(D) == 4) return (((r >> 2) & 1) << 3) | (((r >> 3) & 1) << 2) | (r & 3);
+        else if constexpr (W == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+        else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    }
+    static __device__ __forceinline__ int at(int r, int chunk) { return r * kRow + ((chunk ^ turn(r)) << 4); }
+
+    // Elements 8 c8 .. of row r.
+    static __device__ __forceinline__ void put(char* tile, int r, int c8, const Raw8<D>& v)
+    {
+        constexpr int n = (int)sizeof(D) / 2;
+#pragma unroll
+        for (int k = 0; k < n; ++k) *reinterpret_cast<u32x4*>(tile + at(r, n * c8 + k)) = v.w[k];
+    }
+    // Rows row + lane % 32, elements 16 ks + 8 (lane / 32) + 0..7.
+    static __device__ __forceinline__ AFrag<D> rows(const char* tile, int row, int ks, int lane)
+    {
+        constexpr int n = (int)sizeof(D) / 2;
+        AFrag<D> f;
+#pragma unroll
+        for (int k = 0; k < n; ++k)
+            f.w[k] = *reinterpret_cast<const u32x4*>(
+                tile + at(row + (lane & 31), n * (2 * ks + (lane >> 5)) + k));
+        return f;
+    }
+    // Column col + lane % 32 of rows row + 8 (e / 4) + 4 (lane / 32) + e % 4, e = 0..7.
+    // A transposing read hands the 16 lanes of a group four rows of four groups of 4
+    // columns, 8 bytes read by each lane.
+    static __device__ __forceinline__ AFrag<D> columns(const char* tile, int row, int col, int lane)
+    {
+        AFrag<D> f;
+        const int h = lane >> 5;
+        if constexpr (sizeof(D) == 4) {
+            const int c = col + (lane & 31);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f.w[e / 4][e % 4] = *reinterpret_cast<const uint32_t*>(
+                    tile + at(row + 8 * (e / 4) + 4 * h + e % 4, c / 4) + 4 * (c % 4));
+        } else {
+            typedef __attribute__((address_space(3))) as16x4* lds_ptr;
+            const int r = row + 4 * h + ((lane & 15) >> 2);
+            const int c = col + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+            const as16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at(r, c / 8) + 2 * (c % 8)));
+            const as16x4 hi =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at(r + 8, c / 8) + 2 * (c % 8)));
+            typedef short s16x8 __attribute__((ext_vector_type(8)));
+            f.w[0] = __builtin_bit_cast(u32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        return f;
+    }
+};
+
+// Rows of memory on their way into a tile of kRows rows, by all threads of a block
+// of 256.  Rows from `count` on and elements beyond the dimension become zeros.
+template <class D, int W, int kRows>
+struct AttStage {
+    static constexpr int kUnits = kRows * (W / 8) / 256;
+    Raw8<D> r[kUnits];
+
+    __device__ __forceinline__ void fetch(const SeqView& v, int64_t n, int h, int64_t t0, int count, int dim)
+    {
+        const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+        const D* const from = seq_row<D>(v, n, t0, h);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int at = row + u * (256 / (W / 8));
+            r[u] = Raw8<D>{};
+            if (at < count && c < dim) r[u] = load8<D>(from + (int64_t)at * v.step, c, dim, v.vec);
+        }
+    }
+    __device__ __forceinline__ void put(char* tile) const
+    {
+        const int row = threadIdx.x / (W / 8), c8 = threadIdx.x % (W / 8);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) AttTile<D, W>::put(tile, row + u * (256 / (W / 8)), c8, r[u]);
+    }
+};
+
+// -------------------------------------------------------------- what is seen
+// The two ranges of keys of one query, as first key and length.
+struct Seen {
+    int near, near_len, far, far_len;
+};
+
+__device__ __forceinline__ int episode_start(const AttArgs& x, int64_t n, int j)
+{
+    return x.starts != nullptr ? x.starts[n * x.TK + j] : 0;
+}
+
+__device__ __forceinline__ Seen seen_by(const AttArgs& x, int i, int start)
+{
+    Seen s;
+    s.near = max(start, i - x.window + 1);
+    s.near_len = i - s.near + 1;
+    s.far = start;
+    s.far_len = min(x.sinks, s.near - start);
+    return s;
+}
+
+__device__ __forceinline__ bool sees(const Seen& s, int j)
+{
+    return (unsigned)(j - s.near) < (unsigned)s.near_len || (unsigned)(j - s.far) < (unsigned)s.far_len;
+}
+
+// What a block's queries see: tiles of kTile keys, the far range's first.
+struct KeyTiles {
+    int far, far_end, near, near_end, far_tiles, tiles;
+
+    __device__ __forceinline__ KeyTiles(const AttArgs& x, int64_t n, int first, int last, int tile)
+    {
+        const Seen s = seen_by(x, first, episode_start(x, n, first));
+        far = s.far;
+        far_end = s.far + s.far_len;
+        near = s.near;
+        near_end = last + 1;
+        far_tiles = (s.far_len + tile - 1) / tile;
+        tiles = far_tiles + (near_end - near + tile - 1) / tile;
+    }
+    __device__ __forceinline__ void get(int it, int tile, int& j0, int& j1) const
+    {
+        const bool is_far = it < far_tiles;
+        j0 = is_far ? far + it * tile : near + (it - far_tiles) * tile;
+        j1 = min(j0 + tile, is_far ? far_end : near_end);
+    }
+};
+
+// The wave's 32 queries, a lane's own being lane % 32.
+struct WaveQueries {
+    int i;        // the query's step among the keys
+    bool valid;
+    Seen seen;
+    int first, last;     // of the wave's queries, first > last where it has none
+    int lo_most, lo_least;  // of their near ranges
+
+    __device__ __forceinline__ WaveQueries(const AttArgs& x, int64_t n, int step0, int block_near, int lane)
+    {
+        const int past = x.TK - x.T;
+        const int step = step0 + (lane & 31);
+        valid = step < x.T;
+        i = past + min(step, x.T - 1);
+        first = past + step0;
+        last = past + min(step0 + 31, x.T - 1);
+        seen = seen_by(x, i, episode_start(x, n, i));
+        // first steps that lie among the block's near keys come with their tiles
+        const int least = seen.far + x.sinks > block_near ? max(seen.far, block_near) : seen.near;
+        lo_least = __shfl(least, 0);
+        lo_most = __shfl(seen.near, 31);
+        // steps ascend and so do starts: lane 31 (clamped to the last step) has the most
+        if (!valid) seen.near_len = seen.far_len = 0;
+    }
+    __device__ __forceinline__ bool any() const { return first <= last; }
+    // Whether some query may see keys j0 .. j1 - 1 of a tile, and whether all see all.
+    __device__ __forceinline__ bool touches(const KeyTiles& kt, bool is_far, int j0, int j1) const
+    {
+        return any() && (is_far || (j0 <= last && j1 > lo_least));
+    }
+    __device__ __forceinline__ bool whole(bool is_far, int j0, int j1, int tile) const
+    {
+        return !is_far && j1 - j0 == tile && j0 >= lo_most && j1 - 1 <= first;
+    }
+};
+
+// Blocks by eighths: consecutive blocks go to the eight XCDs in turn, and each of
+// these then works on one stretch of neighbouring tiles, whose keys its L2 holds.
+__device__ __forceinline__ uint32_t by_xcd(uint32_t b, uint32_t blocks)
+{
+    const uint32_t per = blocks / 8, rest = blocks % 8, x = b % 8, k = b / 8;
+    return x * per + min(x, rest) + k;
+}
+
+// ---------------------------------------------------------- the careful form
+// One query (or key) at a time by one wave, from the formulas: lanes are keys
+// while scores are made and elements while rows are summed, and what is not seen
+// is neither read nor multiplied.  The fast forms multiply unseen values by 0;
+// where a result is not finite it is computed again here, so that NaN and
+// infinities reach exactly the results that have a part in them.
+template <class D>
+__device__ __forceinline__ float row_dot(const D* a, const D* b, int dim)
+{
+    float s = 0.0f;
+    for (int d = 0; d < dim; ++d) s = fmaf(to_f32(a[d]), to_f32(b[d]), s);
+    return s;
+}
+
+template <class D>
+__device__ __forceinline__ void careful_forward(const AttArgs& x, int64_t n, int head, int i, int lane)
+{
+    const int t = i - (x.TK - x.T), kvh = head / x.group;
+    const Seen s = seen_by(x, i, episode_start(x, n, i));
+    const D* const q = seq_row<D>(x.q, n, t, head);
+    const int total = s.far_len + s.near_len;
+    float m = -INFINITY;
+    bool nan = false;
+    for (int a = lane; a < total; a += kWave) {
+        const int j = a < s.far_len ? s.far + a : s.near + a - s.far_len;
+        const float v = x.scale * row_dot(q, seq_row<D>(x.k, n, j, kvh), x.dim_k);
+        nan |= v != v;
+        m = fmaxf(m, v);
+    }
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (__any(nan)) m = __builtin_nanf("");
+    float l = 0.0f, acc[2] = {0.0f, 0.0f};
+    for (int a0 = 0; a0 < total; a0 += kWave) {
+        const int a = a0 + lane, j = a < s.far_len ? s.far + a : s.near + a - s.far_len;
+        float p = 0.0f;
+        if (a < total) p = expf(x.scale * row_dot(q, seq_row<D>(x.k, n, j, kvh), x.dim_k) - m);
+        l += p;
+        for (int b = 0; b < min(kWave, total - a0); ++b) {
+            const float w = __shfl(p, b);
+            const D* const v = seq_row<D>(x.v, n, __shfl(j, b), kvh);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (lane + k * kWave < x.dim_v) acc[k] = fmaf(w, to_f32(v[lane + k * kWave]), acc[k]);
+        }
+    }
+    for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
+    D* const out = seq_row_out<D>(x.o, n, t, head);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (lane + k * kWave < x.dim_v) out[lane + k * kWave] = from_f32<D>(acc[k] / l);
+    if (lane == 0 && x.lse.p != nullptr) *seq_row_out<float>(x.lse, n, t, head) = m + logf(l);
+}
+
+template <class D>
+__device__ __forceinline__ void careful_dq(const AttArgs& x, int64_t n, int head, int i, int lane)
+{
+    const int t = i - (x.TK - x.T), kvh = head / x.group;
+    const Seen s = seen_by(x, i, episode_start(x, n, i));
+    const D *const q = seq_row<D>(x.q, n, t, head), *const d_o = seq_row<D>(x.dout, n, t, head);
+    const float lse = *seq_row<float>(x.lse, n, t, head);
+    const float delta = row_dot(d_o, seq_row<D>(x.o, n, t, head), x.dim_v);
+    const int total = s.far_len + s.near_len;
+    float acc[2] = {0.0f, 0.0f};
+    for (int a0 = 0; a0 < total; a0 += kWave) {
+        const int a = a0 + lane, j = a < s.far_len ? s.far + a : s.near + a - s.far_len;
+        float ds = 0.0f;
+        if (a < total) {
+            const float p = expf(x.scale * row_dot(q, seq_row<D>(x.k, n, j, kvh), x.dim_k) - lse);
+            ds = x.scale * (p * (row_dot(d_o, seq_row<D>(x.v, n, j, kvh), x.dim_v) - delta));
+        }
+        for (int b = 0; b < min(kWave, total - a0); ++b) {
+            const float w = __shfl(ds, b);
+            const D* const k = seq_row<D>(x.k, n, __shfl(j, b), kvh);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (lane + e * kWave < x.dim_k) acc[e] = fmaf(w, to_f32(k[lane + e * kWave]), acc[e]);
+        }
+    }
+    D* const out = seq_row_out<D>(x.dq, n, t, head);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (lane + e * kWave < x.dim_k) out[lane + e * kWave] = from_f32<D>(acc[e]);
+}
+
+template <class D>
+__device__ __forceinline__ void careful_dkv(const AttArgs& x, int64_t n, int kvh, int j, int lane)
+{
+    const int past = x.TK - x.T;
+    const D *const k = seq_row<D>(x.k, n, j, kvh), *const v = seq_row<D>(x.v, n, j, kvh);
+    float dk[2] = {0.0f, 0.0f}, dv[2] = {0.0f, 0.0f};
+    for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head)
+        for (int i0 = max(j, past); i0 < x.TK; i0 += kWave) {
+            const int i = i0 + lane, in = min(i, x.TK - 1), start = episode_start(x, n, in);
+            const bool mine = i < x.TK && sees(seen_by(x, in, start), j);
+            const uint64_t who = __ballot(mine);
+            // no later query sees j once this lane's is beyond the window, or the episode
+            if (who == 0 && (__shfl(start, 0) > j || (i0 - j >= x.window && j >= __shfl(start, 0) + x.sinks))) break;
+            float p = 0.0f, ds = 0.0f;
+            const int t = in - past;
+            if (mine) {
+                const D* const d_o = seq_row<D>(x.dout, n, t, head);
+                p = expf(x.scale * row_dot(seq_row<D>(x.q, n, t, head), k, x.dim_k) -
+                         *seq_row<float>(x.lse, n, t, head));
+                ds = x.scale * (p * (row_dot(d_o, v, x.dim_v) -
+                                     row_dot(d_o, seq_row<D>(x.o, n, t, head), x.dim_v)));
+            }
+            for (int b = 0; b < kWave; ++b) {
+                if (!((who >> b) & 1)) continue;
+                const float pb = __shfl(p, b), sb = __shfl(ds, b);
+                const D* const q = seq_row<D>(x.q, n, i0 + b - past, head);
+                const D* const d_o = seq_row<D>(x.dout, n, i0 + b - past, head);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = lane + e * kWave;
+                    if (c < x.dim_k) dk[e] = fmaf(sb, to_f32(q[c]), dk[e]);
+                    if (c < x.dim_v) dv[e] = fmaf(pb, to_f32(d_o[c]), dv[e]);
+                }
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int c = lane + e * kWave;
+        if (c < x.dim_k) seq_row_out<D>(x.dk, n, j, kvh)[c] = from_f32<D>(dk[e]);
+        if (c < x.dim_v) seq_row_out<D>(x.dv, n, j, kvh)[c] = from_f32<D>(dv[e]);
+    }
+}
+
+// -------------------------------------------------------------- fast kernels
+
+// 32 rows (queries or keys, a lane's own) as operands: element 16 ks + 8 h + e.
+template <class D, int W>
+struct OwnRows {
+    AFrag<D> f[W / 16];
+
+    __device__ __forceinline__ void load(const SeqView& v, int64_t n, int64_t t, int h, int dim, bool valid,
+                                         int lane)
+    {
+        const D* const row = seq_row<D>(v, n, t, h);
+#pragma unroll
+        for (int ks = 0; ks < W / 16; ++ks) {
+            const int c = 16 * ks + 8 * (lane >> 5);
+            f[ks] = AFrag<D>{};
+            if (valid && c < dim) f[ks] = load8<D>(row, c, dim, v.vec);
+        }
+    }
+    // Every value's sign turned over where `turn`.
+    __device__ __forceinline__ void signs(bool turn)
+    {
+        const uint32_t m = !turn ? 0u : sizeof(D) == 4 ? 0x80000000u : 0x80008000u;
+#pragma unroll
+        for (int ks = 0; ks < W / 16; ++ks)
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(D) / 2; ++k) f[ks].w[k] ^= u32x4{m, m, m, m};
+    }
+};
+
+// Writes a product whose columns are the wave's rows (a lane's own: `row`) and
+// whose rows are elements; rows of memory get four elements at a time.
+template <class D, int kTiles>
+__device__ __forceinline__ void store_own(D* row, const f32x16 (&acc)[kTiles], float by, int dim, int vec, int h)
+{
+#pragma unroll
+    for (int dt = 0; dt < kTiles; ++dt)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int c = 32 * dt + 8 * r4 + 4 * h;
+            const float v[4] = {acc[dt][4 * r4] * by, acc[dt][4 * r4 + 1] * by, acc[dt][4 * r4 + 2] * by,
+                                acc[dt][4 * r4 + 3] * by};
+            if (vec == 16 && c + 4 <= dim) {
+                if constexpr (sizeof(D) == 4)
+                    *reinterpret_cast<f32x4*>(row + c) = f32x4{v[0], v[1], v[2], v[3]};
+                else
+                    *reinterpret_cast<u32x2*>(row + c) = u32x2{pack2<D>(v[0], v[1]), pack2<D>(v[2], v[3])};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < dim) row[c + e] = from_f32<D>(v[e]);
+            }
+        }
+}
+
+// Whether all values are finite.
+template <int kTiles>
+__device__ __forceinline__ bool finite(const f32x16 (&acc)[kTiles])
+{
+    float z = 0.0f;
+#pragma unroll
+    for (int dt = 0; dt < kTiles; ++dt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) z = fmaf(acc[dt][r], 0.0f, z);
+    return z == 0.0f;
+}
+
+template <class D, int W>
+constexpr int kKeyTile = sizeof(D) == 4 ? 32 : 64;
+template <class D, int W>
+constexpr int kAttBlocks = sizeof(D) == 4 && W == 128 ? 1 : 2;  // blocks per CU
+
+// A block's place: its heads, and the steps of its four waves.
+struct AttBlock {
+    int64_t n;
+    int head, step0, first, last, kvh;
+
+    __device__ __forceinline__ AttBlock(const AttArgs& x)
+    {
+        const uint32_t id = by_xcd(blockIdx.x, gridDim.x);
+        const int hblocks = x.H / x.hpb, rows = 4 / x.hpb * 32;
+        const uint32_t tile = id % x.tiles, hb = id / x.tiles % hblocks;
+        n = id / x.tiles / hblocks;
+        const int wave = threadIdx.x / kWave;
+        head = hb * x.hpb + wave % x.hpb;
+        kvh = head / x.group;
+        step0 = tile * rows + wave / x.hpb * 32;
+        first = x.TK - x.T + tile * rows;
+        last = min(first + rows, x.TK) - 1;
+    }
+};
+
+template <class D, int W>
+__global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const AttArgs x)
+{
+    using Tile = AttTile<D, W>;
+    constexpr int BK = kKeyTile<D, W>, kBytes = BK * Tile::kRow, S = BK / 32;
+    __shared__ alignas(16) char lds[2][2][kBytes];
+    const int lane = threadIdx.x % kWave, h = lane >> 5;
+    const AttBlock b(x);
+    const KeyTiles kt(x, b.n, b.first, b.last, BK);
+    const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
+    OwnRows<D, W> q;
+    q.load(x.q, b.n, wq.i - (x.TK - x.T), b.head, x.dim_k, wq.valid, lane);
+    q.signs(x.scale < 0.0f);
+
+    AttStage<D, W, BK> sk, sv;
+    auto fetch = [&](int it) {
+        int j0, j1;
+        kt.get(it, BK, j0, j1);
+        sk.fetch(x.k, b.n, b.kvh, j0, j1 - j0, x.dim_k);
+        sv.fetch(x.v, b.n, b.kvh, j0, j1 - j0, x.dim_v);
+    };
+    fetch(0);
+    sk.put(lds[0][0]);
+    sv.put(lds[0][1]);
+    if (kt.tiles > 1) fetch(1);
+
+    f32x16 o[W / 32] = {};
+    float m = -INFINITY, l = 0.0f;  // m: the largest score; l: this half's sum
+    for (int it = 0; it < kt.tiles; ++it) {
+        __syncthreads();
+        const char *const tk = lds[it & 1][0], *const tv = lds[it & 1][1];
+        int j0, j1;
+        kt.get(it, BK, j0, j1);
+        const bool is_far = it < kt.far_tiles;
+        if (wq.touches(kt, is_far, j0, j1)) {
+            f32x16 s[S] = {};
+#pragma unroll
+            for (int ks = 0; ks < W / 16; ++ks)
+#pragma unroll
+                for (int a = 0; a < S; ++a) s[a] = mma32<D>(Tile::rows(tk, 32 * a, ks, lane), q.f[ks], s[a]);
+            if (!wq.whole(is_far, j0, j1, BK)) {
+                Seen see = wq.seen;
+                if (is_far) {
+                    see.near_len = 0;
+                    see.far_len = min(see.far_len, max(0, j1 - see.far));
+                }
+#pragma unroll
+                for (int a = 0; a < S; ++a)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (!sees(see, j0 + 32 * a + acc_row(r, h))) s[a][r] = -INFINITY;
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int a = 0; a < S; ++a)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[a][r]);
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // the sums are scaled again only when the largest score has grown by 2^8
+            if (__any((top - m) * x.c > 8.0f)) {
+                const float to = fmaxf(m, top);
+                const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - to) * x.c);
+                m = to;
+                l *= f;
+#pragma unroll
+                for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[dt][r] *= f;
+            }
+            const float base = m == -INFINITY ? 0.0f : m * x.c;
+#pragma unroll
+            for (int a = 0; a < S; ++a)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    s[a][r] = __builtin_amdgcn_exp2f(fmaf(s[a][r], x.c, -base));
+                    l += s[a][r];
+                }
+#pragma unroll
+            for (int a = 0; a < S; ++a)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const AFrag<D> p = operand<D>(s[a], u);
+#pragma unroll
+                    for (int dt = 0; dt < W / 32; ++dt)
+                        o[dt] = mma32<D>(Tile::columns(tv, 32 * a + 16 * u, 32 * dt, lane), p, o[dt]);
+                }
+        }
+        if (it + 1 < kt.tiles) {
+            sk.put(lds[(it + 1) & 1][0]);
+            sv.put(lds[(it + 1) & 1][1]);
+            if (it + 2 < kt.tiles) fetch(it + 2);
+        }
+    }
+    if (!wq.any()) return;
+    l += __shfl_xor(l, 32);
+    const float by = 1.0f / l, lse = (m * x.c + __builtin_amdgcn_logf(l)) * kAttLn2;
+    const int t = wq.i - (x.TK - x.T);
+    const bool fine = finite(o) && by < INFINITY && fabsf(lse) < INFINITY;
+    if (wq.valid) {
+        store_own<D>(seq_row_out<D>(x.o, b.n, t, b.head), o, by, x.dim_v, x.o.vec, h);
+        if (h == 0 && x.lse.p != nullptr) *seq_row_out<float>(x.lse, b.n, t, b.head) = lse;
+    }
+    uint64_t again = __ballot(wq.valid && !fine);
+    for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
+        careful_forward<D>(x, b.n, b.head, wq.first + __builtin_ctzll(again), lane);
+}
+
+template <class D, int W>
+__global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttArgs x)
+{
+    using Tile = AttTile<D, W>;
+    constexpr int BK = 32, kBytes = BK * Tile::kRow;
+    __shared__ alignas(16) char lds[2][2][kBytes];
+    const int lane = threadIdx.x % kWave, h = lane >> 5;
+    const AttBlock b(x);
+    const KeyTiles kt(x, b.n, b.first, b.last, BK);
+    const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
+    const int t = wq.i - (x.TK - x.T);
+    OwnRows<D, W> q, d_o;
+    q.load(x.q, b.n, t, b.head, x.dim_k, wq.valid, lane);
+    q.signs(x.scale < 0.0f);
+    d_o.load(x.dout, b.n, t, b.head, x.dim_v, wq.valid, lane);
+    float delta = 0.0f;
+    {
+        OwnRows<D, W> o;
+        o.load(x.o, b.n, t, b.head, x.dim_v, wq.valid, lane);
+#pragma unroll
+        for (int ks = 0; ks < W / 16; ++ks)
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(D) / 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (sizeof(D) == 4) {
+                        delta = fmaf(__uint_as_float(o.f[ks].w[k][e]), __uint_as_float(d_o.f[ks].w[k][e]), delta);
+                    } else {
+                        float a0, a1, b0, b1;
+                        unpack2<D>(o.f[ks].w[k][e], a0, a1);
+                        unpack2<D>(d_o.f[ks].w[k][e], b0, b1);
+                        delta = fmaf(a1, b1, fmaf(a0, b0, delta));
+                    }
+                }
+    }
+    delta += __shfl_xor(delta, 32);
+    const float lse2 = (wq.valid ? *seq_row<float>(x.lse, b.n, t, b.head) : 0.0f) * kAttLog2e;
+
+    AttStage<D, W, BK> sk, sv;
+    auto fetch = [&](int it) {
+        int j0, j1;
+        kt.get(it, BK, j0, j1);
+        sk.fetch(x.k, b.n, b.kvh, j0, j1 - j0, x.dim_k);
+        sv.fetch(x.v, b.n, b.kvh, j0, j1 - j0, x.dim_v);
+    };
+    f32x16 dq[W / 32] = {};
+    // the first pass, for short windows, is for D alone, as sum_j p_ij do_i . v_j
+    for (int pass = x.sum_delta ? 0 : 1; pass < 2; ++pass) {
+        float sum = 0.0f;
+        fetch(0);
+        __syncthreads();
+        sk.put(lds[0][0]);
+        sv.put(lds[0][1]);
+        if (kt.tiles > 1) fetch(1);
+        for (int it = 0; it < kt.tiles; ++it) {
+            __syncthreads();
+            const char *const tk = lds[it & 1][0], *const tv = lds[it & 1][1];
+            int j0, j1;
+            kt.get(it, BK, j0, j1);
+            const bool is_far = it < kt.far_tiles;
+            if (wq.touches(kt, is_far, j0, j1)) {
+                f32x16 s = {}, dp = {};
+#pragma unroll
+                for (int ks = 0; ks < W / 16; ++ks) {
+                    s = mma32<D>(Tile::rows(tk, 0, ks, lane), q.f[ks], s);
+                    dp = mma32<D>(Tile::rows(tv, 0, ks, lane), d_o.f[ks], dp);
+                }
+                const float less = pass == 0 ? 0.0f : delta;
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2)) * (dp[r] - less);
+                if (!wq.whole(is_far, j0, j1, BK)) {
+                    Seen see = wq.seen;
+                    if (is_far) {
+                        see.near_len = 0;
+                        see.far_len = min(see.far_len, max(0, j1 - see.far));
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (!sees(see, j0 + acc_row(r, h))) dp[r] = 0.0f;
+                }
+                if (pass == 0) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sum += dp[r];
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const AFrag<D> ds = operand<D>(dp, u);
+                        AFrag<D> rest;
+                        if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
+#pragma unroll
+                        for (int dt = 0; dt < W / 32; ++dt) {
+                            const AFrag<D> k = Tile::columns(tk, 16 * u, 32 * dt, lane);
+                            dq[dt] = mma32<D>(k, ds, dq[dt]);
+                            if constexpr (sizeof(D) == 2) dq[dt] = mma32<D>(k, rest, dq[dt]);
+                        }
+                    }
+                }
+            }
+            if (it + 1 < kt.tiles) {
+                sk.put(lds[(it + 1) & 1][0]);
+                sv.put(lds[(it + 1) & 1][1]);
+                if (it + 2 < kt.tiles) fetch(it + 2);
+            }
+        }
+        if (pass == 0) delta = sum + __shfl_xor(sum, 32);
+    }
+    if (wq.valid && h == 0) x.delta[(b.n * x.H + b.head) * x.T + t] = delta;
+    if (!wq.any()) return;
+    const bool fine = finite(dq);
+    if (wq.valid)
+        store_own<D>(seq_row_out<D>(x.dq, b.n, t, b.head), dq, x.scale, x.dim_k, x.dq.vec, h);
+    uint64_t again = __ballot(wq.valid && !fine);
+    for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
+        careful_dq<D>(x, b.n, b.head, wq.first + __builtin_ctzll(again), lane);
+}
+
+// float16 weights go into the products 2^10 times as large: a key's weights may all
+// be small (1 / window and less), and below 2^-14 float16 has ever fewer bits.
+template <class D>
+constexpr float kWeightBits = std::is_same<D, f16_t>::value ? 10.0f : 0.0f;
+
+// Keys are the columns: a wave holds 32 of them and their values, a block 128;
+// queries and their gradients come in tiles of 32, head after head of the group.
+template <class D, int W>
+__global__ __launch_bounds__(256, 1) void attend_dkv(const AttArgs x)
+{
+    using Tile = AttTile<D, W>;
+    constexpr int BQ = 32, kBytes = BQ * Tile::kRow;
+    constexpr float kLess = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
+    struct Rows {
+        alignas(16) float lse2[BQ], delta[BQ];
+        alignas(16) int32_t start[BQ];
+    };
+    __shared__ alignas(16) char lds[2][2][kBytes];
+    __shared__ Rows rows[2];
+    const int lane = threadIdx.x % kWave, h = lane >> 5, wave = threadIdx.x / kWave;
+    const int past = x.TK - x.T, kv = x.H / x.group;
+    const uint32_t id = by_xcd(blockIdx.x, gridDim.x);
+    const int kvh = id / x.tiles % kv;
+    const int64_t n = id / x.tiles / kv;
+    const int j0 = (int)(id % x.tiles) * 128, j1 = min(j0 + 128, x.TK);
+    const int mine0 = j0 + 32 * wave, j = mine0 + (lane & 31);
+    const bool valid = j < x.TK;
+    OwnRows<D, W> k, v;
+    k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
+    k.signs(x.scale < 0.0f);
+    v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
+
+    // Tiles of queries from `begin` on; more() says whether any from i on sees a key here.
+    const int begin = max(j0, past);
+    auto more = [&](int i) {
+        if (i >= x.TK) return false;
+        const int start = episode_start(x, n, i);
+        if (start >= j1) return false;
+        return i - x.window + 1 < j1 || start + x.sinks > j0;
+    };
+    AttStage<D, W, BQ> sq, so;
+    float r_lse = 0.0f, r_delta = 0.0f;
+    int r_start = 0;
+    auto fetch = [&](int head, int i) {
+        const int count = min(BQ, x.TK - i);
+        sq.fetch(x.q, n, head, i - past, count, x.dim_k);
+        so.fetch(x.dout, n, head, i - past, count, x.dim_v);
+        if ((int)threadIdx.x < BQ) {
+            const bool in = (int)threadIdx.x < count;
+            const int at = min(i + (int)threadIdx.x, x.TK - 1);
+            r_lse = in ? fmaf(*seq_row<float>(x.lse, n, at - past, head), kAttLog2e, -kWeightBits<D>) : INFINITY;
+            r_delta = in ? x.delta[(n * x.H + head) * x.T + at - past] * kLess : 0.0f;
+            r_start = episode_start(x, n, at);
+        }
+    };
+    auto put = [&](int to) {
+        sq.put(lds[to][0]);
+        so.put(lds[to][1]);
+        if ((int)threadIdx.x < BQ) {
+            rows[to].lse2[threadIdx.x] = r_lse;
+            rows[to].delta[threadIdx.x] = r_delta;
+            rows[to].start[threadIdx.x] = r_start;
+        }
+    };
+    f32x16 dk[W / 32] = {}, dv[W / 32] = {};
+    if (more(begin)) {
+        int head = kvh * x.group, i = begin;           // being computed
+        int nhead = head, ni = i;                      // fetched next
+        const int end_head = (kvh + 1) * x.group;
+        auto advance = [&](int& hd, int& at) {
+            at += BQ;
+            if (!more(at)) {
+                at = begin;
+                ++hd;
+            }
+        };
+        fetch(nhead, ni);
+        put(0);
+        advance(nhead, ni);
+        if (nhead < end_head) fetch(nhead, ni);
+        for (int it = 0; head < end_head; ++it) {
+            __syncthreads();
+            const char *const tq = lds[it & 1][0], *const to = lds[it & 1][1];
+            const Rows& row = rows[it & 1];
+            const int i_last = min(i + BQ, x.TK) - 1;
+            // the wave's keys: those up to the last query that some query still reaches
+            const int mine1 = min(mine0 + 32, x.TK);
+            const int s0 = row.start[0];
+            const bool touches = mine0 <= i_last && mine1 > s0 &&
+                                 (mine1 > i - x.window + 1 || mine0 < row.start[BQ - 1] + x.sinks);
+            if (touches) {
+                f32x16 s = {}, dp = {};
+#pragma unroll
+                for (int ks = 0; ks < W / 16; ++ks) {
+                    s = mma32<D>(Tile::rows(tq, 0, ks, lane), k.f[ks], s);
+                    dp = mma32<D>(Tile::rows(to, 0, ks, lane), v.f[ks], dp);
+                }
+                // whole: every query of the tile sees every key of the wave
+                const bool whole = i + BQ <= x.TK && mine0 + 32 <= x.TK && mine0 + 31 <= i &&
+                                   row.start[BQ - 1] <= mine0 && mine0 > i + BQ - 1 - x.window;
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&row.lse2[8 * r4 + 4 * h]);
+                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&row.delta[8 * r4 + 4 * h]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 4 * r4 + e;
+                        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2[e]));
+                        dp[r] = s[r] * (kLess == 1.0f ? dp[r] - delta[e] : fmaf(dp[r], kLess, -delta[e]));
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int r4 = 0; r4 < 4; ++r4) {
+                        const u32x4 st = *reinterpret_cast<const u32x4*>(&row.start[8 * r4 + 4 * h]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 4 * r4 + e, qi = i + 8 * r4 + 4 * h + e, start = (int)st[e];
+                            const bool see = j <= qi && j >= start && qi < x.TK && valid &&
+                                             (j > qi - x.window || j < start + x.sinks);
+                            if (!see) s[r] = dp[r] = 0.0f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const AFrag<D> p = operand<D>(s, u), ds = operand<D>(dp, u);
+                    AFrag<D> rest;
+                    if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
+#pragma unroll
+                    for (int dt = 0; dt < W / 32; ++dt) {
+                        dv[dt] = mma32<D>(Tile::columns(to, 16 * u, 32 * dt, lane), p, dv[dt]);
+                        const AFrag<D> q = Tile::columns(tq, 16 * u, 32 * dt, lane);
+                        dk[dt] = mma32<D>(q, ds, dk[dt]);
+                        if constexpr (sizeof(D) == 2) dk[dt] = mma32<D>(q, rest, dk[dt]);
+                    }
+                }
+            }
+            advance(head, i);
+            if (nhead < end_head) {
+                put((it + 1) & 1);
+                advance(nhead, ni);
+                if (nhead < end_head) fetch(nhead, ni);
+            }
+        }
+    }
+    const bool fine = finite(dk) && finite(dv);
+    if (valid) {
+        store_own<D>(seq_row_out<D>(x.dk, n, j, kvh), dk, x.scale, x.dim_k, x.dk.vec, h);
+        store_own<D>(seq_row_out<D>(x.dv, n, j, kvh), dv, kLess, x.dim_v, x.dv.vec, h);
+    }
+    uint64_t again = __ballot(valid && !fine);
+    for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
+        careful_dkv<D>(x, n, kvh, mine0 + __builtin_ctzll(again), lane);
+}
+
+// The first step of each step's episode, [N, TK]: a running maximum of the steps
+// where the reset mask is set, one block to a row.
+static __global__ __launch_bounds__(256) void episode_starts(const SeqView reset, int64_t N, int32_t TK, int32_t* out)
+{
+    __shared__ int part[4];
+    const int64_t n = blockIdx.x;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    int carry = 0;
+    for (int t0 = 0; t0 < TK; t0 += 256) {
+        const int t = t0 + threadIdx.x;
+        int v = t < TK && *seq_row<uint8_t>(reset, n, t, 0) != 0 ? t : 0;
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int u = __shfl_up(v, o);
+            if (lane >= o) v = max(v, u);
+        }
+        if (lane == kWave - 1) part[wave] = v;
+        __syncthreads();
+        v = max(v, carry);
+        for (int w = 0; w < wave; ++w) v = max(v, part[w]);
+        for (int w = 0; w < 4; ++w) carry = max(carry, part[w]);
+        if (t < TK) out[n * TK + t] = v;
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------- single steps
+// One step of an environment at position p of its episode: its key and value go
+// into slot p (p < sinks) or sinks + (p - sinks) % window of the caches, and its
+// query sees the first min(p + 1, sinks + window) slots: what the ring holds is
+// the window, and the order of a softmax's terms is free.
+
+struct AttStepArgs {
+    SeqView q, k, v, kc, vc, o;  // kc, vc: the slots are the steps
+    const int32_t* positions;
+    float* part;                 // splits > 1: [N, H, splits, dim_v + 2]
+    int32_t KV, group, chunks, splits, per_split, sinks, window, dim_k, dim_v;
+    float c;                     // scale log2(e)
+    uint8_t wide;                // rows are whole 16-byte units
+};
+
+// What lane i of 2^k neighbours has in common with the others: their sum.
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    auto dpp = [](float x, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value,
+                                                                  0xf, 0xf, true));
+    };
+    if constexpr (N >= 2) v += dpp(v, std::integral_constant<int, 0xb1>{});   // quad_perm 1,0,3,2
+    if constexpr (N >= 4) v += dpp(v, std::integral_constant<int, 0x4e>{});   // quad_perm 2,3,0,1
+    if constexpr (N >= 8) v += dpp(v, std::integral_constant<int, 0x141>{});  // row_half_mirror
+    if constexpr (N >= 16) v += dpp(v, std::integral_constant<int, 0x140>{}); // row_mirror
+    if constexpr (N >= 32) v += __shfl_xor(v, 16);
+    return v;
+}
+
+// A 16-byte unit of a row from element c on, zeros beyond dim.
+template <class D>
+__device__ __forceinline__ u32x4 load_unit(const D* row, int c, int dim, bool wide)
+{
+    constexpr int E = 16 / (int)sizeof(D);
+    u32x4 w = {};
+    if (wide) {
+        if (c < dim) w = *reinterpret_cast<const u32x4*>(row + c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (c + e < dim) {
+                if constexpr (sizeof(D) == 4) w[e] = reinterpret_cast<const uint32_t*>(row)[c + e];
+                else w[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[c + e] << (16 * (e & 1));
+            }
+    }
+    return w;
+}
+
+template <class D>
+__device__ __forceinline__ void store_row_unit(D* row, int c, int dim, bool wide, const u32x4& w)
+{
+    constexpr int E = 16 / (int)sizeof(D);
+    if (wide) {
+        if (c < dim) *reinterpret_cast<u32x4*>(row + c) = w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (c + e < dim) {
+                if constexpr (sizeof(D) == 4) reinterpret_cast<uint32_t*>(row)[c + e] = w[e];
+                else reinterpret_cast<uint16_t*>(row)[c + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+    }
+}
+
+template <class D>
+__device__ __forceinline__ void unit_f32(const u32x4& w, float (&v)[16 / sizeof(D)])
+{
+    if constexpr (sizeof(D) == 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) unpack2<D>(w[e], v[2 * e], v[2 * e + 1]);
+    }
+}
+
+// LR lanes hold a row of a cache, 16 bytes each, a wave 64 / LR rows at a time, and
+// G query heads of a key head are served at once.  Each group of LR lanes keeps a
+// running maximum and sum of its own; groups, waves and splits are joined after.
+template <class D, int LR, int G>
+__global__ __launch_bounds__(256) void attend_step(const AttStepArgs x)
+{
+    constexpr int E = 16 / (int)sizeof(D), R = kWave / LR, U = 4;
+    __shared__ float sm[4][G], sl[4][G], sa[4][G][LR * E];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    uint32_t id = blockIdx.x;
+    const int split = id % x.splits;
+    id /= x.splits;
+    const int chunk = id % x.chunks;
+    id /= x.chunks;
+    const int kvh = id % x.KV;
+    const int64_t n = id / x.KV;
+    const int head0 = kvh * x.group + chunk * G, heads = min(G, x.group - chunk * G);
+    const int slots = x.sinks + x.window;
+    const int64_t p = x.positions[n];
+    if (p < 0) {  // this environment waits
+        if (split == 0)
+            for (int a = threadIdx.x; a < heads * x.dim_v; a += 256)
+                seq_row_out<D>(x.o, n, 0, head0 + a / x.dim_v)[a % x.dim_v] = from_f32<D>(0.0f);
+        return;
+    }
+    const int count = (int)min(p + 1, (int64_t)slots);
+    const int mine = (int)(p < x.sinks ? p : x.sinks + (p - x.sinks) % x.window);
+    const int begin = split * x.per_split, end = min(begin + x.per_split, count);
+    const int c = lane % LR * E, r = lane / LR;
+    const D *const kin = seq_row<D>(x.k, n, 0, kvh), *const vin = seq_row<D>(x.v, n, 0, kvh);
+
+    // the step's own key and value go into its slot; every block takes them from k and v
+    if (chunk == 0 && mine >= begin && mine < begin + x.per_split && wave == 0 && r == 0) {
+        store_row_unit<D>(seq_row_out<D>(x.kc, n, mine, kvh), c, x.dim_k, x.wide, load_unit<D>(kin, c, x.dim_k, x.wide));
+        store_row_unit<D>(seq_row_out<D>(x.vc, n, mine, kvh), c, x.dim_v, x.wide, load_unit<D>(vin, c, x.dim_v, x.wide));
+    }
+    float q[G][E], acc[G][E] = {}, m[G], l[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        u32x4 w = {};
+        if (g < heads) w = load_unit<D>(seq_row<D>(x.q, n, 0, head0 + g), c, x.dim_k, x.wide);
+        unit_f32<D>(w, q[g]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) q[g][e] *= x.c;
+        m[g] = -INFINITY;
+        l[g] = 0.0f;
+    }
+    for (int s0 = begin + wave * R * U + r; s0 < end; s0 += 4 * R * U) {
+        u32x4 kw[U], vw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * R;
+            kw[u] = vw[u] = u32x4{};
+            if (s < end) {
+                kw[u] = load_unit<D>(s == mine ? kin : seq_row<D>(x.kc, n, s, kvh), c, x.dim_k, x.wide);
+                vw[u] = load_unit<D>(s == mine ? vin : seq_row<D>(x.vc, n, s, kvh), c, x.dim_v, x.wide);
+            }
+        }
+        float s[G][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float kf[E];
+            unit_f32<D>(kw[u], kf);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float d = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) d = fmaf(q[g][e], kf[e], d);
+                d = lanes_sum<LR>(d);
+                s[g][u] = s0 + u * R < end ? d : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float top = m[g];
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, s[g][u]);
+            const float f = m[g] == top ? 1.0f : __builtin_amdgcn_exp2f(m[g] - top);
+            m[g] = top;
+            l[g] *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[g][e] *= f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // slots behind the end have a weight of 0 even where no score is above -infinity
+                s[g][u] = s0 + u * R < end ? __builtin_amdgcn_exp2f(s[g][u] - top) : 0.0f;
+                l[g] += s[g][u];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float vf[E];
+            unit_f32<D>(vw[u], vf);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[g][e] = fmaf(s[g][u], vf[e], acc[g][e]);
+        }
+    }
+    // groups of lanes, then waves
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float top = m[g];
+#pragma unroll
+        for (int o = LR; o < kWave; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+        const float f = m[g] == top ? 1.0f : __builtin_amdgcn_exp2f(m[g] - top);
+        l[g] *= f;
+#pragma unroll
+        for (int o = LR; o < kWave; o <<= 1) l[g] += __shfl_xor(l[g], o);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float a = acc[g][e] * f;
+#pragma unroll
+            for (int o = LR; o < kWave; o <<= 1) a += __shfl_xor(a, o);
+            if (r == 0) sa[wave][g][c + e] = a;
+        }
+        if (lane == 0) {
+            sm[wave][g] = top;
+            sl[wave][g] = l[g];
+        }
+    }
+    __syncthreads();
+    for (int a = threadIdx.x; a < heads * x.dim_v; a += 256) {
+        const int g = a / x.dim_v, d = a % x.dim_v;
+        float top = sm[0][g], sum = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int w = 1; w < 4; ++w) top = fmaxf(top, sm[w][g]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = sm[w][g] == top ? 1.0f : __builtin_amdgcn_exp2f(sm[w][g] - top);
+            sum = fmaf(sl[w][g], f, sum);
+            v = fmaf(sa[w][g][d], f, v);
+        }
+        if (x.splits == 1) {
+            seq_row_out<D>(x.o, n, 0, head0 + g)[d] = from_f32<D>(v / sum);
+        } else {
+            float* const to = x.part + ((n * x.KV * x.group + head0 + g) * x.splits + split) * (x.dim_v + 2);
+            to[d] = v;
+            if (d == 0) {
+                to[x.dim_v] = top;
+                to[x.dim_v + 1] = sum;
+            }
+        }
+    }
+}
+
+// Joins the splits of a head, in their order.
+template <class D>
+__global__ __launch_bounds__(128) void join_step(const AttStepArgs x)
+{
+    const int H = x.KV * x.group, head = blockIdx.x % H, d = threadIdx.x;
+    const int64_t n = blockIdx.x / H;
+    if (d >= x.dim_v || x.positions[n] < 0) return;
+    const float* const from = x.part + (int64_t)blockIdx.x * x.splits * (x.dim_v + 2);
+    float top = -INFINITY, sum = 0.0f, v = 0.0f;
+    for (int s = 0; s < x.splits; ++s) top = fmaxf(top, from[s * (x.dim_v + 2) + x.dim_v]);
+    for (int s = 0; s < x.splits; ++s) {
+        const float* const at = from + s * (x.dim_v + 2);
+        const float f = at[x.dim_v] == top ? 1.0f : __builtin_amdgcn_exp2f(at[x.dim_v] - top);
+        sum = fmaf(at[x.dim_v + 1], f, sum);
+        v = fmaf(at[d], f, v);
+    }
+    seq_row_out<D>(x.o, n, 0, head)[d] = from_f32<D>(v / sum);
+}
+
+// The caches after the last episode of each row of k and v, slot by slot: a slot
+// takes the last step that belongs into it, if the row has one.
+struct AttFillArgs {
+    SeqView k, v, kc, vc, positions;
+    int64_t N;
+    int32_t T, KV, sinks, window, dim_k, dim_v;
+};
+
+template <class D>
+__global__ __launch_bounds__(256) void fill_slots(const AttFillArgs x, const uint32_t wide)
+{
+    const int slots = x.sinks + x.window, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int64_t at = (int64_t)blockIdx.x * 4 + wave;
+    if (at >= x.N * slots) return;
+    const int64_t n = at / slots;
+    const int slot = (int)(at % slots);
+    const int64_t last = *seq_row<int32_t>(x.positions, n, x.T - 1, 0);
+    int64_t p = slot;
+    if (slot >= x.sinks && last >= slot) p = slot + (last - slot) / x.window * x.window;
+    const int64_t t = x.T - 1 - (last - p);
+    if (p > last || t < 0) return;
+    constexpr int E = 16 / (int)sizeof(D);
+    const int uk = (x.dim_k + E - 1) / E, uv = (x.dim_v + E - 1) / E;
+    for (int a = lane; a < x.KV * (uk + uv); a += kWave) {
+        const bool key = a < x.KV * uk;
+        const int b = key ? a : a - x.KV * uk, u = key ? uk : uv, h = b / u, c = b % u * E;
+        const int dim = key ? x.dim_k : x.dim_v;
+        const SeqView &from = key ? x.k : x.v, &to = key ? x.kc : x.vc;
+        store_row_unit<D>(seq_row_out<D>(to, n, slot, h), c, dim, wide,
+                          load_unit<D>(seq_row<D>(from, n, t, h), c, dim, wide));
+    }
+}
+
+// ------------------------------------------------------------------ entries
+
+inline bool att_sizes_ok(int64_t H, int64_t KV, int64_t dk, int64_t dv)
+{
+    return KV >= 1 && H >= 1 && H <= 65536 && H % KV == 0 && dk >= 1 && dv >= 1 && dk <= kMaxAttDim &&
+           dv <= kMaxAttDim;
+}
+
+inline lrs_status check_attention(const char* nm, int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV,
+                                  int64_t dk, int64_t dv, int64_t window, int64_t sinks, float scale)
+{
+    LRS_TRY(check_common(nm, N, T));
+    LRS_REQUIRE(TK >= T && valid_sizes(N, TK), "%s: key_steps must be at least query_steps, and within their limits", nm);
+    LRS_REQUIRE(KV >= 1 && H >= 1 && H <= 65536 && H % KV == 0,
+                "%s: heads must be a multiple of kv_heads and 1 to 65536 (got %lld and %lld)", nm, (long long)H,
+                (long long)KV);
+    LRS_REQUIRE(dk >= 1 && dv >= 1 && dk <= kMaxAttDim && dv <= kMaxAttDim,
+                "%s: key_dim and value_dim must be 1 to %d (got %lld and %lld)", nm, kMaxAttDim, (long long)dk,
+                (long long)dv);
+    LRS_REQUIRE(window >= 1, "%s: window must be at least 1 (got %lld)", nm, (long long)window);
+    LRS_REQUIRE(sinks >= 0 && sinks < (int64_t(1) << 31), "%s: sinks must be 0 or more (got %lld)", nm,
+                (long long)sinks);
+    LRS_REQUIRE(scale - scale == 0.0f && scale != 0.0f && std::abs(scale) * kAttLog2e <= 1e30f,
+                "%s: scale must be finite and not 0", nm);
+    return LRS_OK;
+}
+
+// How wide the accesses to an array's rows may be, in bytes.
+inline void set_vec(SeqView& v, int64_t dim, int s)
+{
+    v.vec = rows_on(v, 16 / s, s) && dim % 8 == 0 ? 16 : rows_on(v, 4 / s, s) && dim % (4 / s) == 0 ? 4 : s;
+}
+
+inline size_t att_workspace(int64_t N, int64_t T, int64_t TK, int64_t H, bool reset, bool backward)
+{
+    size_t b = 0;
+    if (reset) b += ((size_t)(N * TK) * 4 + 255) / 256 * 256;
+    if (backward) b += ((size_t)(N * T * H) * 4 + 255) / 256 * 256;
+    return b;
+}
+
+inline void fill_attention(AttArgs& x, int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV, int64_t dk,
+                           int64_t dv, int64_t window, int64_t sinks, float scale, const void* reset, void* ws)
+{
+    x.N = N;
+    x.T = (int32_t)T;
+    x.TK = (int32_t)TK;
+    x.H = (int32_t)H;
+    x.group = (int32_t)(H / KV);
+    x.window = (int32_t)std::min(window, TK);
+    x.sinks = (int32_t)std::min(sinks, TK);
+    x.dim_k = (int32_t)dk;
+    x.dim_v = (int32_t)dv;
+    x.scale = scale;
+    x.c = std::abs(scale) * kAttLog2e;
+    // D from the rounded results is off by their rounding, which counts where few weights
+    // share a query: gradients of 16-bit types were off by twice the rounding of their own
+    // at a window of 2, 1.4 times at 4, by nothing to be seen from 30 on.
+    x.sum_delta = x.window <= 16;
+    x.hpb = x.group % 4 == 0 ? 4 : x.group % 2 == 0 ? 2 : 1;
+    char* at = static_cast<char*>(ws);
+    x.starts = reset != nullptr ? reinterpret_cast<const int32_t*>(at) : nullptr;
+    if (reset != nullptr) at += ((size_t)(N * TK) * 4 + 255) / 256 * 256;
+    x.delta = reinterpret_cast<float*>(at);
+}
+
+inline lrs_status launch_starts(const char* nm, const AttArgs& x, const SeqView& reset, hipStream_t stream)
+{
+    if (x.starts == nullptr) return LRS_OK;
+    return launch_seq(nm, episode_starts, (uint64_t)x.N, 256, stream, reset, x.N, x.TK,
+                      const_cast<int32_t*>(x.starts));
+}
+
+constexpr uint64_t kMaxGrid = 0x7fffffffull;
+
+// Blocks of the forward and of dq: 128 queries of hpb heads.
+inline uint64_t query_blocks(AttArgs& x)
+{
+    const int rows = 4 / x.hpb * 32;
+    x.tiles = (x.T + rows - 1) / rows;
+    return (uint64_t)x.N * (uint64_t)(x.H / x.hpb) * (uint64_t)x.tiles;
+}
+inline uint64_t key_blocks(AttArgs& x)
+{
+    x.tiles = (x.TK + 127) / 128;
+    return (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.tiles;
+}
+
+template <class D>
+lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV, int64_t dk,
+                           int64_t dv, int64_t window, int64_t sinks, const D* q, const D* k, const D* v,
+                           const uint8_t* reset, float scale, D* out, float* lse, const int64_t* strides,
+                           void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    LRS_TRY(check_attention(nm, N, T, TK, H, KV, dk, dv, window, sinks, scale));
+    constexpr int s = sizeof(D);
+    const SeqArg args[6] = {{q, H, dk, s, false, true, "q"},
+                            {k, KV, dk, s, false, true, "k", TK},
+                            {v, KV, dv, s, false, true, "v", TK},
+                            {reset, 1, 1, 1, false, false, "reset", TK},
+                            {out, H, dv, s, true, true, "out"},
+                            {lse, H, 1, 4, true, false, "lse"}};
+    const Span more[] = {{ws, ws_bytes}};
+    SeqView a[6];
+    LRS_TRY(check_seq_arrays(nm, N, T, args, strides, more, 1, 1, a));
+    LRS_TRY(check_workspace(nm, att_workspace(N, T, TK, H, reset != nullptr, false), ws, ws_bytes));
+    AttArgs x{};
+    fill_attention(x, N, T, TK, H, KV, dk, dv, window, sinks, scale, reset, ws);
+    x.q = a[0];
+    x.k = a[1];
+    x.v = a[2];
+    x.o = a[4];
+    x.lse = a[5];
+    set_vec(x.q, dk, s);
+    set_vec(x.k, dk, s);
+    set_vec(x.v, dv, s);
+    set_vec(x.o, dv, s);
+    const uint64_t blocks = query_blocks(x);
+    LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N <= kMaxGrid, "%s: num_envs * heads * steps is too large", nm);
+    LRS_TRY(launch_starts(nm, x, a[3], stream));
+    return launch_seq(nm, std::max(dk, dv) <= 64 ? attend_forward<D, 64> : attend_forward<D, 128>, blocks, 256,
+                      stream, x);
+}
+
+template <class D>
+lrs_status attention_backward_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV,
+                                    int64_t dk, int64_t dv, int64_t window, int64_t sinks, const D* grad_out,
+                                    const D* q, const D* k, const D* v, const uint8_t* reset, const D* out,
+                                    const float* lse, float scale, D* grad_q, D* grad_k, D* grad_v,
+                                    const int64_t* strides, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    LRS_TRY(check_attention(nm, N, T, TK, H, KV, dk, dv, window, sinks, scale));
+    constexpr int s = sizeof(D);
+    const SeqArg args[10] = {{grad_out, H, dv, s, false, true, "grad_out"},
+                             {q, H, dk, s, false, true, "q"},
+                             {k, KV, dk, s, false, true, "k", TK},
+                             {v, KV, dv, s, false, true, "v", TK},
+                             {reset, 1, 1, 1, false, false, "reset", TK},
+                             {out, H, dv, s, false, true, "out"},
+                             {lse, H, 1, 4, false, true, "lse"},
+                             {grad_q, H, dk, s, true, true, "grad_q"},
+                             {grad_k, KV, dk, s, true, true, "grad_k", TK},
+                             {grad_v, KV, dv, s, true, true, "grad_v", TK}};
+    const Span more[] = {{ws, ws_bytes}};
+    SeqView a[10];
+    LRS_TRY(check_seq_arrays(nm, N, T, args, strides, more, 1, 1, a));
+    LRS_TRY(check_workspace(nm, att_workspace(N, T, TK, H, reset != nullptr, true), ws, ws_bytes));
+    AttArgs x{};
+    fill_attention(x, N, T, TK, H, KV, dk, dv, window, sinks, scale, reset, ws);
+    x.dout = a[0];
+    x.q = a[1];
+    x.k = a[2];
+    x.v = a[3];
+    x.o = a[5];
+    x.lse = a[6];
+    x.dq = a[7];
+    x.dk = a[8];
+    x.dv = a[9];
+    for (SeqView* w : {&x.q, &x.k, &x.dq, &x.dk}) set_vec(*w, dk, s);
+    for (SeqView* w : {&x.v, &x.o, &x.dout, &x.dv}) set_vec(*w, dv, s);
+    LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && (uint64_t)N <= kMaxGrid,
+                "%s: num_envs * heads * steps is too large", nm);
+    const bool narrow = std::max(dk, dv) <= 64;
+    LRS_TRY(launch_starts(nm, x, a[4], stream));
+    uint64_t blocks = query_blocks(x);
+    LRS_TRY(launch_seq(nm, narrow ? attend_dq<D, 64> : attend_dq<D, 128>, blocks, 256, stream, x));
+    blocks = key_blocks(x);
+    return launch_seq(nm, narrow ? attend_dkv<D, 64> : attend_dkv<D, 128>, blocks, 256, stream, x);
+}
+
+// The splits of a step's slots: as many as make four blocks for each of 256 CUs, of
+// 256 slots each at least.
+inline void plan_step(AttStepArgs& x, int64_t N)
+{
+    const int64_t slots = (int64_t)x.sinks + x.window, blocks = N * x.KV * x.chunks;
+    int64_t splits = std::min<int64_t>((1024 + blocks - 1) / blocks, (slots + 255) / 256);
+    splits = std::max<int64_t>(1, std::min<int64_t>(splits, 256));
+    x.per_split = (int32_t)((slots + splits - 1) / splits);
+    x.splits = (int32_t)((slots + x.per_split - 1) / x.per_split);
+}
+
+// Heads of a group that a block serves at once.
+inline int step_heads(int64_t group) { return group >= 3 ? 4 : (int)group; }
+
+inline bool fill_step(AttStepArgs& x, int64_t N, int64_t H, int64_t KV, int64_t slots, int64_t sinks, int64_t dk,
+                      int64_t dv)
+{
+    if (N < 1 || N > (int64_t(1) << 31) || !att_sizes_ok(H, KV, dk, dv) || sinks < 0 || slots <= sinks ||
+        slots >= (int64_t(1) << 31))
+        return false;
+    x.KV = (int32_t)KV;
+    x.group = (int32_t)(H / KV);
+    x.chunks = (x.group + step_heads(x.group) - 1) / step_heads(x.group);
+    x.sinks = (int32_t)sinks;
+    x.window = (int32_t)(slots - sinks);
+    x.dim_k = (int32_t)dk;
+    x.dim_v = (int32_t)dv;
+    plan_step(x, N);
+    return true;
+}
+
+inline size_t step_workspace(const AttStepArgs& x, int64_t N)
+{
+    if (x.splits == 1) return 0;
+    return (size_t)N * x.KV * x.group * x.splits * (size_t)(x.dim_v + 2) * 4;
+}
+
+template <class D, int G>
+auto step_kernel(int units) -> void (*)(AttStepArgs)
+{
+    if (units <= 2) return attend_step<D, 2, G>;
+    if (units <= 4) return attend_step<D, 4, G>;
+    if (units <= 8) return attend_step<D, 8, G>;
+    if (units <= 16) return attend_step<D, 16, G>;
+    if constexpr (sizeof(D) == 4) return attend_step<D, 32, G>;
+    return attend_step<D, 16, G>;
+}
+
+template <class D>
+lrs_status attention_step_entry(const char* nm, int64_t N, int64_t H, int64_t KV, int64_t slots, int64_t sinks,
+                                int64_t dk, int64_t dv, const D* q, const D* k, const D* v, D* key_cache,
+                                D* value_cache, const int32_t* positions, float scale, D* out,
+                                const int64_t* strides, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    LRS_REQUIRE(slots >= 1 && slots < (int64_t(1) << 31), "%s: slots must be 1 to 2^31 - 1 (got %lld)", nm,
+                (long long)slots);
+    LRS_TRY(check_attention(nm, N, 1, 1, H, KV, dk, dv, slots - sinks, sinks, scale));
+    constexpr int s = sizeof(D);
+    const SeqArg args[7] = {{q, H, dk, s, false, true, "q"},
+                            {k, KV, dk, s, false, true, "k"},
+                            {v, KV, dv, s, false, true, "v"},
+                            {key_cache, KV, dk, s, true, true, "key_cache", slots},
+                            {value_cache, KV, dv, s, true, true, "value_cache", slots},
+                            {positions, 1, 1, 4, false, true, "positions"},
+                            {out, H, dv, s, true, true, "out"}};
+    const Span more[] = {{ws, ws_bytes}};
+    SeqView a[7];
+    LRS_TRY(check_seq_arrays(nm, N, 1, args, strides, more, 1, 1, a));
+    LRS_REQUIRE(a[5].env == 1 || N == 1, "%s: positions must be consecutive", nm);
+    AttStepArgs x{};
+    LRS_REQUIRE(fill_step(x, N, H, KV, slots, sinks, dk, dv), "%s: unsupported sizes", nm);
+    LRS_TRY(check_workspace(nm, step_workspace(x, N), ws, ws_bytes));
+    x.q = a[0];
+    x.k = a[1];
+    x.v = a[2];
+    x.kc = a[3];
+    x.vc = a[4];
+    x.positions = positions;
+    x.o = a[6];
+    x.part = static_cast<float*>(ws);
+    x.c = scale * kAttLog2e;
+    constexpr int E = 16 / s;
+    x.wide = dk % E == 0 && dv % E == 0;
+    for (int i = 0; i < 5; ++i) x.wide = x.wide && rows_on(a[i], E, s);
+    const uint64_t blocks = (uint64_t)N * KV * x.chunks * x.splits;
+    LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N * H <= kMaxGrid, "%s: num_envs * heads is too large", nm);
+    const int units = (int)((std::max(dk, dv) + E - 1) / E), g = step_heads(x.group);
+    LRS_TRY(launch_seq(nm, g == 1 ? step_kernel<D, 1>(units) : g == 2 ? step_kernel<D, 2>(units) : step_kernel<D, 4>(units),
+                       blocks, 256, stream, x));
+    if (x.splits == 1) return LRS_OK;
+    return launch_seq(nm, join_step<D>, (uint64_t)N * H, 128, stream, x);
+}
+
+template <class D>
+lrs_status attention_fill_entry(const char* nm, int64_t N, int64_t T, int64_t KV, int64_t slots, int64_t sinks,
+                                int64_t dk, int64_t dv, const D* k, const D* v, const int32_t* positions,
+                                D* key_cache, D* value_cache, const int64_t* strides, hipStream_t stream)
+{
+    LRS_REQUIRE(slots >= 1 && slots < (int64_t(1) << 31), "%s: slots must be 1 to 2^31 - 1 (got %lld)", nm,
+                (long long)slots);
+    LRS_TRY(check_attention(nm, N, T, T, KV, KV, dk, dv, slots - sinks, sinks, 1.0f));
+    constexpr int s = sizeof(D);
+    const SeqArg args[5] = {{k, KV, dk, s, false, true, "k"},
+                            {v, KV, dv, s, false, true, "v"},
+                            {positions, 1, 1, 4, false, true, "positions"},
+                            {key_cache, KV, dk, s, true, true, "key_cache", slots},
+                            {value_cache, KV, dv, s, true, true, "value_cache", slots}};
+    SeqView a[5];
+    LRS_TRY(check_seq_arrays(nm, N, T, args, strides, nullptr, 0, 0, a));
+    AttFillArgs x{a[0], a[1], a[3], a[4], a[2], N, (int32_t)T, (int32_t)KV, (int32_t)sinks,
+                  (int32_t)(slots - sinks), (int32_t)dk, (int32_t)dv};
+    constexpr int E = 16 / s;
+    const bool wide = dk % E == 0 && dv % E == 0 && rows_on(a[0], E, s) && rows_on(a[1], E, s) &&
+                      rows_on(a[3], E, s) && rows_on(a[4], E, s);
+    const uint64_t blocks = ((uint64_t)N * slots + 3) / 4;
+    LRS_REQUIRE(blocks <= kMaxGrid, "%s: num_envs * slots is too large", nm);
+    return launch_seq(nm, fill_slots<D>, blocks, 256, stream, x, (uint32_t)wide);
+}
+
+}  // namespace lrs
