@@ -12,7 +12,9 @@ size_t lrs_windowed_attention_workspace_bytes(int64_t num_envs, int64_t query_st
     if (!valid_sizes(num_envs, query_steps) || !valid_sizes(num_envs, key_steps) || key_steps < query_steps ||
         !att_sizes_ok(heads, kv_heads, key_dim, value_dim) || window < 1 || sinks < 0)
         return 0;
-    return att_workspace(num_envs, query_steps, key_steps, heads, has_reset != 0, backward != 0);
+    return att_workspace(num_envs, query_steps, key_steps, heads, kv_heads, key_dim, value_dim, window, sinks,
+                         has_reset != 0, backward != 0)
+        .bytes;
 }
 
 size_t lrs_windowed_attention_step_workspace_bytes(int64_t num_envs, int64_t heads, int64_t kv_heads,

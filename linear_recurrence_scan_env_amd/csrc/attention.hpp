@@ -37,9 +37,11 @@ struct AttArgs {
     SeqView dout, dq, dk, dv;
     const int32_t* starts;      // [N, TK]: the first step of each key step's episode; null: 0
     float* delta;               // D, [N, H, T]
+    float* far_part;            // [N, KV, far_chunks, sinks, 2 W] sums of attend_far; null: it does not run
     int64_t N;
     int32_t T, TK, H, group, window, sinks, dim_k, dim_v;
     int32_t hpb, tiles;         // heads per block, blocks per row of steps
+    int32_t far_chunks;
     uint8_t sum_delta;          // whether dq sums D itself
     float scale, c;             // c = |scale| log2(e)
 };
@@ -169,29 +171,44 @@ struct AttTile {
     }
 };
 
-// Rows of memory on their way into a tile of kRows rows, by all threads of a block
-// of 256.  Rows from `count` on and elements beyond the dimension become zeros.
-template <class D, int W, int kRows>
+// Rows of memory on their way into a tile of kRows rows, by a block of 256 threads
+// or by a wave.  kWide: rows are whole 16-byte units, and loads go out without a branch
+// between them, or each would be waited for where the branches meet.  What lies
+// beyond the last row or the dimension is then read from within them: it meets
+// weights of 0, or zeros of the other operand.  Otherwise it becomes zeros.
+template <class D, int W, int kRows, bool kWide, int kThreads = 256>
 struct AttStage {
-    static constexpr int kUnits = kRows * (W / 8) / 256;
+    static constexpr int kUnits = kRows * (W / 8) / kThreads, kApart = kThreads / (W / 8);
     Raw8<D> r[kUnits];
 
     __device__ __forceinline__ void fetch(const SeqView& v, int64_t n, int h, int64_t t0, int count, int dim)
     {
-        const int row = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+        const int me = threadIdx.x % kThreads, row = me / (W / 8), c = me % (W / 8) * 8;
         const D* const from = seq_row<D>(v, n, t0, h);
+        if constexpr (kWide) {
+            const uint32_t col = c < dim ? c : 0;
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int at = row + u * (256 / (W / 8));
-            r[u] = Raw8<D>{};
-            if (at < count && c < dim) r[u] = load8<D>(from + (int64_t)at * v.step, c, dim, v.vec);
+            for (int u = 0; u < kUnits; ++u) {
+                const uint32_t at = (uint32_t)min(row + u * kApart, count - 1) * (uint32_t)v.step + col;
+#pragma unroll
+                for (int k = 0; k < (int)sizeof(D) / 2; ++k)
+                    r[u].w[k] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(from) +
+                                                                (at * (uint32_t)sizeof(D) + 16u * k));
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int at = row + u * kApart;
+                r[u] = Raw8<D>{};
+                if (at < count && c < dim) r[u] = load8<D>(from + (int64_t)at * v.step, c, dim, v.vec);
+            }
         }
     }
     __device__ __forceinline__ void put(char* tile) const
     {
-        const int row = threadIdx.x / (W / 8), c8 = threadIdx.x % (W / 8);
+        const int me = threadIdx.x % kThreads, row = me / (W / 8), c8 = me % (W / 8);
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) AttTile<D, W>::put(tile, row + u * (256 / (W / 8)), c8, r[u]);
+        for (int u = 0; u < kUnits; ++u) AttTile<D, W>::put(tile, row + u * kApart, c8, r[u]);
     }
 };
 
@@ -417,7 +434,7 @@ __device__ __forceinline__ void careful_dkv(const AttArgs& x, int64_t n, int kvh
 // -------------------------------------------------------------- fast kernels
 
 // 32 rows (queries or keys, a lane's own) as operands: element 16 ks + 8 h + e.
-template <class D, int W>
+template <class D, int W, bool kWide>
 struct OwnRows {
     AFrag<D> f[W / 16];
 
@@ -429,7 +446,14 @@ struct OwnRows {
         for (int ks = 0; ks < W / 16; ++ks) {
             const int c = 16 * ks + 8 * (lane >> 5);
             f[ks] = AFrag<D>{};
-            if (valid && c < dim) f[ks] = load8<D>(row, c, dim, v.vec);
+            if (!valid || c >= dim) continue;
+            if constexpr (kWide) {
+#pragma unroll
+                for (int k = 0; k < (int)sizeof(D) / 2; ++k)
+                    f[ks].w[k] = *reinterpret_cast<const u32x4*>(row + c + k * (16 / (int)sizeof(D)));
+            } else {
+                f[ks] = load8<D>(row, c, dim, v.vec);
+            }
         }
     }
     // Every value's sign turned over where `turn`.
@@ -443,10 +467,36 @@ struct OwnRows {
     }
 };
 
+// The products of a lane's own rows with others of the same place, summed.
+template <class D, int W, bool kWide>
+__device__ __forceinline__ float own_dot(const SeqView& v, int64_t n, int64_t t, int head, int dim, bool valid,
+                                         int lane, const OwnRows<D, W, kWide>& with)
+{
+    OwnRows<D, W, kWide> o;
+    o.load(v, n, t, head, dim, valid, lane);
+    float sum = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < W / 16; ++ks)
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(D) / 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(D) == 4) {
+                    sum = fmaf(__uint_as_float(o.f[ks].w[k][e]), __uint_as_float(with.f[ks].w[k][e]), sum);
+                } else {
+                    float a0, a1, b0, b1;
+                    unpack2<D>(o.f[ks].w[k][e], a0, a1);
+                    unpack2<D>(with.f[ks].w[k][e], b0, b1);
+                    sum = fmaf(a1, b1, fmaf(a0, b0, sum));
+                }
+            }
+    return sum + __shfl_xor(sum, 32);
+}
+
 // Writes a product whose columns are the wave's rows (a lane's own: `row`) and
 // whose rows are elements; rows of memory get four elements at a time.
-template <class D, int kTiles>
-__device__ __forceinline__ void store_own(D* row, const f32x16 (&acc)[kTiles], float by, int dim, int vec, int h)
+template <class D, bool kWide, int kTiles>
+__device__ __forceinline__ void store_own(D* row, const f32x16 (&acc)[kTiles], float by, int dim, int h)
 {
 #pragma unroll
     for (int dt = 0; dt < kTiles; ++dt)
@@ -455,7 +505,8 @@ __device__ __forceinline__ void store_own(D* row, const f32x16 (&acc)[kTiles], f
             const int c = 32 * dt + 8 * r4 + 4 * h;
             const float v[4] = {acc[dt][4 * r4] * by, acc[dt][4 * r4 + 1] * by, acc[dt][4 * r4 + 2] * by,
                                 acc[dt][4 * r4 + 3] * by};
-            if (vec == 16 && c + 4 <= dim) {
+            if (kWide) {
+                if (c >= dim) continue;
                 if constexpr (sizeof(D) == 4)
                     *reinterpret_cast<f32x4*>(row + c) = f32x4{v[0], v[1], v[2], v[3]};
                 else
@@ -505,7 +556,7 @@ struct AttBlock {
     }
 };
 
-template <class D, int W>
+template <class D, int W, bool kWide>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
@@ -515,11 +566,11 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
     const AttBlock b(x);
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
     const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
-    OwnRows<D, W> q;
+    OwnRows<D, W, kWide> q;
     q.load(x.q, b.n, wq.i - (x.TK - x.T), b.head, x.dim_k, wq.valid, lane);
     q.signs(x.scale < 0.0f);
 
-    AttStage<D, W, BK> sk, sv;
+    AttStage<D, W, BK, kWide> sk, sv;
     auto fetch = [&](int it) {
         int j0, j1;
         kt.get(it, BK, j0, j1);
@@ -604,7 +655,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
     const int t = wq.i - (x.TK - x.T);
     const bool fine = finite(o) && by < INFINITY && fabsf(lse) < INFINITY;
     if (wq.valid) {
-        store_own<D>(seq_row_out<D>(x.o, b.n, t, b.head), o, by, x.dim_v, x.o.vec, h);
+        store_own<D, kWide>(seq_row_out<D>(x.o, b.n, t, b.head), o, by, x.dim_v, h);
         if (h == 0 && x.lse.p != nullptr) *seq_row_out<float>(x.lse, b.n, t, b.head) = lse;
     }
     uint64_t again = __ballot(wq.valid && !fine);
@@ -612,7 +663,8 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
         careful_forward<D>(x, b.n, b.head, wq.first + __builtin_ctzll(again), lane);
 }
 
-template <class D, int W>
+// kSum: the pass before, for short windows, which only sums D as sum_j p_ij do_i . v_j.
+template <class D, int W, bool kWide, bool kSum>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
@@ -623,107 +675,93 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
     const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
     const int t = wq.i - (x.TK - x.T);
-    OwnRows<D, W> q, d_o;
+    OwnRows<D, W, kWide> q, d_o;
     q.load(x.q, b.n, t, b.head, x.dim_k, wq.valid, lane);
     q.signs(x.scale < 0.0f);
     d_o.load(x.dout, b.n, t, b.head, x.dim_v, wq.valid, lane);
-    float delta = 0.0f;
-    {
-        OwnRows<D, W> o;
-        o.load(x.o, b.n, t, b.head, x.dim_v, wq.valid, lane);
-#pragma unroll
-        for (int ks = 0; ks < W / 16; ++ks)
-#pragma unroll
-            for (int k = 0; k < (int)sizeof(D) / 2; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (sizeof(D) == 4) {
-                        delta = fmaf(__uint_as_float(o.f[ks].w[k][e]), __uint_as_float(d_o.f[ks].w[k][e]), delta);
-                    } else {
-                        float a0, a1, b0, b1;
-                        unpack2<D>(o.f[ks].w[k][e], a0, a1);
-                        unpack2<D>(d_o.f[ks].w[k][e], b0, b1);
-                        delta = fmaf(a1, b1, fmaf(a0, b0, delta));
-                    }
-                }
-    }
-    delta += __shfl_xor(delta, 32);
     const float lse2 = (wq.valid ? *seq_row<float>(x.lse, b.n, t, b.head) : 0.0f) * kAttLog2e;
+    float* const delta_at = x.delta + (b.n * x.H + b.head) * x.T + t;
+    float delta = 0.0f;
+    if (x.sum_delta) {
+        if (!kSum && wq.valid) delta = *delta_at;
+    } else {
+        delta = own_dot<D, W, kWide>(x.o, b.n, t, b.head, x.dim_v, wq.valid, lane, d_o);
+        if (wq.valid && h == 0) *delta_at = delta;
+    }
 
-    AttStage<D, W, BK> sk, sv;
+    AttStage<D, W, BK, kWide> sk, sv;
     auto fetch = [&](int it) {
         int j0, j1;
         kt.get(it, BK, j0, j1);
         sk.fetch(x.k, b.n, b.kvh, j0, j1 - j0, x.dim_k);
         sv.fetch(x.v, b.n, b.kvh, j0, j1 - j0, x.dim_v);
     };
+    fetch(0);
+    sk.put(lds[0][0]);
+    sv.put(lds[0][1]);
+    if (kt.tiles > 1) fetch(1);
+
     f32x16 dq[W / 32] = {};
-    // the first pass, for short windows, is for D alone, as sum_j p_ij do_i . v_j
-    for (int pass = x.sum_delta ? 0 : 1; pass < 2; ++pass) {
-        float sum = 0.0f;
-        fetch(0);
+    float sum = 0.0f;
+    for (int it = 0; it < kt.tiles; ++it) {
         __syncthreads();
-        sk.put(lds[0][0]);
-        sv.put(lds[0][1]);
-        if (kt.tiles > 1) fetch(1);
-        for (int it = 0; it < kt.tiles; ++it) {
-            __syncthreads();
-            const char *const tk = lds[it & 1][0], *const tv = lds[it & 1][1];
-            int j0, j1;
-            kt.get(it, BK, j0, j1);
-            const bool is_far = it < kt.far_tiles;
-            if (wq.touches(kt, is_far, j0, j1)) {
-                f32x16 s = {}, dp = {};
+        const char *const tk = lds[it & 1][0], *const tv = lds[it & 1][1];
+        int j0, j1;
+        kt.get(it, BK, j0, j1);
+        const bool is_far = it < kt.far_tiles;
+        if (wq.touches(kt, is_far, j0, j1)) {
+            f32x16 s = {}, dp = {};
 #pragma unroll
-                for (int ks = 0; ks < W / 16; ++ks) {
-                    s = mma32<D>(Tile::rows(tk, 0, ks, lane), q.f[ks], s);
-                    dp = mma32<D>(Tile::rows(tv, 0, ks, lane), d_o.f[ks], dp);
+            for (int ks = 0; ks < W / 16; ++ks) {
+                s = mma32<D>(Tile::rows(tk, 0, ks, lane), q.f[ks], s);
+                dp = mma32<D>(Tile::rows(tv, 0, ks, lane), d_o.f[ks], dp);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2)) * (dp[r] - delta);
+            if (!wq.whole(is_far, j0, j1, BK)) {
+                Seen see = wq.seen;
+                if (is_far) {
+                    see.near_len = 0;
+                    see.far_len = min(see.far_len, max(0, j1 - see.far));
                 }
-                const float less = pass == 0 ? 0.0f : delta;
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2)) * (dp[r] - less);
-                if (!wq.whole(is_far, j0, j1, BK)) {
-                    Seen see = wq.seen;
-                    if (is_far) {
-                        see.near_len = 0;
-                        see.far_len = min(see.far_len, max(0, j1 - see.far));
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (!sees(see, j0 + acc_row(r, h))) dp[r] = 0.0f;
-                }
-                if (pass == 0) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) sum += dp[r];
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const AFrag<D> ds = operand<D>(dp, u);
-                        AFrag<D> rest;
-                        if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
-#pragma unroll
-                        for (int dt = 0; dt < W / 32; ++dt) {
-                            const AFrag<D> k = Tile::columns(tk, 16 * u, 32 * dt, lane);
-                            dq[dt] = mma32<D>(k, ds, dq[dt]);
-                            if constexpr (sizeof(D) == 2) dq[dt] = mma32<D>(k, rest, dq[dt]);
-                        }
-                    }
-                }
+                    if (!sees(see, j0 + acc_row(r, h))) dp[r] = 0.0f;
             }
-            if (it + 1 < kt.tiles) {
-                sk.put(lds[(it + 1) & 1][0]);
-                sv.put(lds[(it + 1) & 1][1]);
-                if (it + 2 < kt.tiles) fetch(it + 2);
+            if constexpr (kSum) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sum += dp[r];
+            } else {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const AFrag<D> ds = operand<D>(dp, u);
+                    AFrag<D> rest;
+                    if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
+#pragma unroll
+                    for (int dt = 0; dt < W / 32; ++dt) {
+                        const AFrag<D> k = Tile::columns(tk, 16 * u, 32 * dt, lane);
+                        dq[dt] = mma32<D>(k, ds, dq[dt]);
+                        if constexpr (sizeof(D) == 2) dq[dt] = mma32<D>(k, rest, dq[dt]);
+                    }
+                }
             }
         }
-        if (pass == 0) delta = sum + __shfl_xor(sum, 32);
+        if (it + 1 < kt.tiles) {
+            sk.put(lds[(it + 1) & 1][0]);
+            sv.put(lds[(it + 1) & 1][1]);
+            if (it + 2 < kt.tiles) fetch(it + 2);
+        }
     }
-    if (wq.valid && h == 0) x.delta[(b.n * x.H + b.head) * x.T + t] = delta;
+    if constexpr (kSum) {
+        sum += __shfl_xor(sum, 32);
+        if (wq.valid && h == 0) *delta_at = sum;
+        return;
+    }
     if (!wq.any()) return;
     const bool fine = finite(dq);
     if (wq.valid)
-        store_own<D>(seq_row_out<D>(x.dq, b.n, t, b.head), dq, x.scale, x.dim_k, x.dq.vec, h);
+        store_own<D, kWide>(seq_row_out<D>(x.dq, b.n, t, b.head), dq, x.scale, x.dim_k, h);
     uint64_t again = __ballot(wq.valid && !fine);
     for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
         careful_dq<D>(x, b.n, b.head, wq.first + __builtin_ctzll(again), lane);
@@ -734,155 +772,289 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
 template <class D>
 constexpr float kWeightBits = std::is_same<D, f16_t>::value ? 10.0f : 0.0f;
 
+// What goes with a tile of 32 queries: their lse (in powers of two, as the weights
+// take it), D, and first steps.
+struct QueryRows {
+    alignas(16) float lse2[32], delta[32];
+    alignas(16) int32_t start[32];
+};
+
+// A tile of 32 queries and their gradients on its way to LDS, from query step i (of
+// the keys' steps) on.
+template <class D, int W, bool kWide, int kThreads>
+struct QueryStage {
+    static constexpr float kLess = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
+    AttStage<D, W, 32, kWide, kThreads> q, d_o;
+    float lse, delta;
+    int start;
+    bool in;
+
+    __device__ __forceinline__ void fetch(const AttArgs& x, int64_t n, int head, int i, int end)
+    {
+        const int past = x.TK - x.T, count = min(32, end - i);
+        q.fetch(x.q, n, head, i - past, count, x.dim_k);
+        d_o.fetch(x.dout, n, head, i - past, count, x.dim_v);
+        // by every thread alike, and used only in put(): a use here would wait for all loads
+        const int a = threadIdx.x & 31, at = min(i + a, end - 1);
+        in = a < count;
+        lse = *seq_row<float>(x.lse, n, at - past, head);
+        delta = x.delta[(n * x.H + head) * x.T + at - past];
+        start = episode_start(x, n, at);
+    }
+    __device__ __forceinline__ void put(char* tq, char* to, QueryRows& rows) const
+    {
+        q.put(tq);
+        d_o.put(to);
+        if (threadIdx.x % kThreads < 32) {
+            const int a = threadIdx.x & 31;
+            // queries behind the end have no weights
+            rows.lse2[a] = in ? fmaf(lse, kAttLog2e, -kWeightBits<D>) : INFINITY;
+            rows.delta[a] = in ? delta * kLess : 0.0f;
+            rows.start[a] = start;
+        }
+    }
+};
+
+// Adds what 32 queries in LDS give to the gradients of the wave's keys.  sees(row,
+// start): whether a query sees the lane's key; not asked where `whole`.
+template <class D, int W, bool kWide, class Sees>
+__device__ __forceinline__ void add_queries(const AttArgs& x, const char* tq, const char* to, const QueryRows& row,
+                                            const OwnRows<D, W, kWide>& k, const OwnRows<D, W, kWide>& v, bool whole,
+                                            Sees sees, int lane, f32x16 (&dk)[W / 32], f32x16 (&dv)[W / 32])
+{
+    using Tile = AttTile<D, W>;
+    constexpr float kLess = QueryStage<D, W, kWide, 256>::kLess;
+    const int h = lane >> 5;
+    f32x16 s = {}, dp = {};
+#pragma unroll
+    for (int ks = 0; ks < W / 16; ++ks) {
+        s = mma32<D>(Tile::rows(tq, 0, ks, lane), k.f[ks], s);
+        dp = mma32<D>(Tile::rows(to, 0, ks, lane), v.f[ks], dp);
+    }
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+        const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&row.lse2[8 * r4 + 4 * h]);
+        const f32x4 delta = *reinterpret_cast<const f32x4*>(&row.delta[8 * r4 + 4 * h]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 4 * r4 + e;
+            s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2[e]));
+            dp[r] = s[r] * (kLess == 1.0f ? dp[r] - delta[e] : fmaf(dp[r], kLess, -delta[e]));
+        }
+    }
+    if (!whole) {
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const u32x4 st = *reinterpret_cast<const u32x4*>(&row.start[8 * r4 + 4 * h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!sees(8 * r4 + 4 * h + e, (int)st[e])) s[4 * r4 + e] = dp[4 * r4 + e] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const AFrag<D> p = operand<D>(s, u), ds = operand<D>(dp, u);
+        AFrag<D> rest;
+        if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
+#pragma unroll
+        for (int dt = 0; dt < W / 32; ++dt) {
+            dv[dt] = mma32<D>(Tile::columns(to, 16 * u, 32 * dt, lane), p, dv[dt]);
+            const AFrag<D> q = Tile::columns(tq, 16 * u, 32 * dt, lane);
+            dk[dt] = mma32<D>(q, ds, dk[dt]);
+            if constexpr (sizeof(D) == 2) dk[dt] = mma32<D>(q, rest, dk[dt]);
+        }
+    }
+}
+
+// The first step from lo on whose episode begins at `from` or later, hi if there is
+// none: starts ascend, and 64 of them are looked at at once.
+__device__ __forceinline__ int first_start(const AttArgs& x, int64_t n, int lo, int hi, int from, int lane)
+{
+    if (x.starts == nullptr) return max(lo, hi);
+    while (lo < hi) {
+        const int step = (hi - lo + kWave - 1) / kWave;
+        const int at = min(lo + lane * step + step - 1, hi - 1);
+        const uint64_t past = __ballot(x.starts[n * x.TK + at] >= from);
+        if (past == 0) return hi;
+        const int f = __builtin_ctzll(past);
+        const int end = min(lo + f * step + step - 1, hi - 1);  // the first looked at that is past
+        lo = lo + f * step;
+        hi = end;
+    }
+    return lo;
+}
+
+// First steps of an episode are seen by all of its queries.  Those beyond the end of
+// the chunk of kFarChunk steps that the episode begins in are left to a kernel of
+// their own (attend_far), a wave to a chunk, which keeps the sums of each chunk
+// apart for attend_dkv to join: or one block would walk the whole episode.
+constexpr int kFarChunk = 256;
+constexpr int kFarSinks = 64;  // with more first steps than this attend_dkv does it all
+
+// Where a chunk's sums of first step s are: W of its key's gradient, W of its value's.
+template <int W>
+__device__ __forceinline__ float* far_sums(const AttArgs& x, int64_t row, int chunk, int s)
+{
+    return x.far_part + ((row * x.far_chunks + chunk) * x.sinks + s) * (2 * W);
+}
+
 // Keys are the columns: a wave holds 32 of them and their values, a block 128;
 // queries and their gradients come in tiles of 32, head after head of the group.
-template <class D, int W>
+template <class D, int W, bool kWide>
 __global__ __launch_bounds__(256, 1) void attend_dkv(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
-    constexpr int BQ = 32, kBytes = BQ * Tile::kRow;
-    constexpr float kLess = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
-    struct Rows {
-        alignas(16) float lse2[BQ], delta[BQ];
-        alignas(16) int32_t start[BQ];
-    };
-    __shared__ alignas(16) char lds[2][2][kBytes];
-    __shared__ Rows rows[2];
+    constexpr int BQ = 32;
+    __shared__ alignas(16) char lds[2][2][BQ * Tile::kRow];
+    __shared__ QueryRows rows[2];
     const int lane = threadIdx.x % kWave, h = lane >> 5, wave = threadIdx.x / kWave;
     const int past = x.TK - x.T, kv = x.H / x.group;
     const uint32_t id = by_xcd(blockIdx.x, gridDim.x);
     const int kvh = id / x.tiles % kv;
     const int64_t n = id / x.tiles / kv;
     const int j0 = (int)(id % x.tiles) * 128, j1 = min(j0 + 128, x.TK);
-    const int mine0 = j0 + 32 * wave, j = mine0 + (lane & 31);
+    const int mine0 = j0 + 32 * wave, mine1 = min(mine0 + 32, x.TK), j = mine0 + (lane & 31);
     const bool valid = j < x.TK;
-    OwnRows<D, W> k, v;
+    OwnRows<D, W, kWide> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
     k.signs(x.scale < 0.0f);
     v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
 
-    // Tiles of queries from `begin` on; more() says whether any from i on sees a key here.
-    const int begin = max(j0, past);
-    auto more = [&](int i) {
-        if (i >= x.TK) return false;
-        const int start = episode_start(x, n, i);
-        if (start >= j1) return false;
-        return i - x.window + 1 < j1 || start + x.sinks > j0;
-    };
-    AttStage<D, W, BQ> sq, so;
-    float r_lse = 0.0f, r_delta = 0.0f;
-    int r_start = 0;
-    auto fetch = [&](int head, int i) {
-        const int count = min(BQ, x.TK - i);
-        sq.fetch(x.q, n, head, i - past, count, x.dim_k);
-        so.fetch(x.dout, n, head, i - past, count, x.dim_v);
-        if ((int)threadIdx.x < BQ) {
-            const bool in = (int)threadIdx.x < count;
-            const int at = min(i + (int)threadIdx.x, x.TK - 1);
-            r_lse = in ? fmaf(*seq_row<float>(x.lse, n, at - past, head), kAttLog2e, -kWeightBits<D>) : INFINITY;
-            r_delta = in ? x.delta[(n * x.H + head) * x.T + at - past] * kLess : 0.0f;
-            r_start = episode_start(x, n, at);
-        }
-    };
-    auto put = [&](int to) {
-        sq.put(lds[to][0]);
-        so.put(lds[to][1]);
-        if ((int)threadIdx.x < BQ) {
-            rows[to].lse2[threadIdx.x] = r_lse;
-            rows[to].delta[threadIdx.x] = r_delta;
-            rows[to].start[threadIdx.x] = r_start;
-        }
-    };
+    // The queries that see a key here: from begin to end.  first: the episode of the
+    // last key, the only one that goes on beyond the block.
+    const int begin = max(j0, past), first = episode_start(x, n, j1 - 1);
+    const bool has_first = first + x.sinks > j0 && x.sinks > 0;
+    const int chunk_end = x.far_part != nullptr ? (first / kFarChunk + 1) * kFarChunk : x.TK;
+    int end = min(j1 - 1 + x.window, x.TK);
+    if (has_first) end = max(end, min(chunk_end, x.TK));
+    end = first_start(x, n, max(j1, past), max(end, past), j1, lane);
+
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
-    if (more(begin)) {
-        int head = kvh * x.group, i = begin;           // being computed
-        int nhead = head, ni = i;                      // fetched next
-        const int end_head = (kvh + 1) * x.group;
-        auto advance = [&](int& hd, int& at) {
-            at += BQ;
-            if (!more(at)) {
-                at = begin;
-                ++hd;
+    const int tiles = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = tiles * x.group;
+    if (total > 0) {
+        QueryStage<D, W, kWide, 256> stage;
+        int head = kvh * x.group, tile = 0, next_head = head, next = 0;
+        auto fetch = [&]() {
+            stage.fetch(x, n, next_head, begin + next * BQ, end);
+            if (++next == tiles) {
+                next = 0;
+                ++next_head;
             }
         };
-        fetch(nhead, ni);
-        put(0);
-        advance(nhead, ni);
-        if (nhead < end_head) fetch(nhead, ni);
-        for (int it = 0; head < end_head; ++it) {
+        fetch();
+        stage.put(lds[0][0], lds[0][1], rows[0]);
+        if (total > 1) fetch();
+        for (int it = 0; it < total; ++it) {
             __syncthreads();
-            const char *const tq = lds[it & 1][0], *const to = lds[it & 1][1];
-            const Rows& row = rows[it & 1];
-            const int i_last = min(i + BQ, x.TK) - 1;
-            // the wave's keys: those up to the last query that some query still reaches
-            const int mine1 = min(mine0 + 32, x.TK);
-            const int s0 = row.start[0];
-            const bool touches = mine0 <= i_last && mine1 > s0 &&
-                                 (mine1 > i - x.window + 1 || mine0 < row.start[BQ - 1] + x.sinks);
-            if (touches) {
-                f32x16 s = {}, dp = {};
-#pragma unroll
-                for (int ks = 0; ks < W / 16; ++ks) {
-                    s = mma32<D>(Tile::rows(tq, 0, ks, lane), k.f[ks], s);
-                    dp = mma32<D>(Tile::rows(to, 0, ks, lane), v.f[ks], dp);
-                }
+            const QueryRows& row = rows[it & 1];
+            const int i = begin + tile * BQ, i_last = min(i + BQ, end) - 1;
+            const int least = row.start[0], most = row.start[BQ - 1];
+            if (mine0 <= i_last && mine1 > least && (mine1 > i - x.window + 1 || mine0 < most + x.sinks)) {
                 // whole: every query of the tile sees every key of the wave
-                const bool whole = i + BQ <= x.TK && mine0 + 32 <= x.TK && mine0 + 31 <= i &&
-                                   row.start[BQ - 1] <= mine0 && mine0 > i + BQ - 1 - x.window;
-#pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&row.lse2[8 * r4 + 4 * h]);
-                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&row.delta[8 * r4 + 4 * h]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 4 * r4 + e;
-                        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2[e]));
-                        dp[r] = s[r] * (kLess == 1.0f ? dp[r] - delta[e] : fmaf(dp[r], kLess, -delta[e]));
-                    }
-                }
-                if (!whole) {
-#pragma unroll
-                    for (int r4 = 0; r4 < 4; ++r4) {
-                        const u32x4 st = *reinterpret_cast<const u32x4*>(&row.start[8 * r4 + 4 * h]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = 4 * r4 + e, qi = i + 8 * r4 + 4 * h + e, start = (int)st[e];
-                            const bool see = j <= qi && j >= start && qi < x.TK && valid &&
-                                             (j > qi - x.window || j < start + x.sinks);
-                            if (!see) s[r] = dp[r] = 0.0f;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const AFrag<D> p = operand<D>(s, u), ds = operand<D>(dp, u);
-                    AFrag<D> rest;
-                    if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
-#pragma unroll
-                    for (int dt = 0; dt < W / 32; ++dt) {
-                        dv[dt] = mma32<D>(Tile::columns(to, 16 * u, 32 * dt, lane), p, dv[dt]);
-                        const AFrag<D> q = Tile::columns(tq, 16 * u, 32 * dt, lane);
-                        dk[dt] = mma32<D>(q, ds, dk[dt]);
-                        if constexpr (sizeof(D) == 2) dk[dt] = mma32<D>(q, rest, dk[dt]);
-                    }
-                }
+                const bool whole = i + BQ <= end && mine0 + 32 <= x.TK && mine0 + 31 <= i && most <= mine0 &&
+                                   mine0 > i + BQ - 1 - x.window;
+                add_queries<D, W, kWide>(
+                    x, lds[it & 1][0], lds[it & 1][1], row, k, v, whole,
+                    [&](int r, int start) {
+                        const int qi = i + r;
+                        return j <= qi && j >= start && qi < end && valid &&
+                               (j > qi - x.window || (j < start + x.sinks && qi < chunk_end));
+                    },
+                    lane, dk, dv);
             }
-            advance(head, i);
-            if (nhead < end_head) {
-                put((it + 1) & 1);
-                advance(nhead, ni);
-                if (nhead < end_head) fetch(nhead, ni);
+            if (++tile == tiles) {
+                tile = 0;
+                ++head;
             }
+            if (it + 1 < total) {
+                stage.put(lds[(it + 1) & 1][0], lds[(it + 1) & 1][1], rows[(it + 1) & 1]);
+                if (it + 2 < total) fetch();
+            }
+        }
+    }
+    constexpr float kLess = QueryStage<D, W, kWide, 256>::kLess;
+    if (has_first && x.far_part != nullptr) {
+        // the chunks after the first, up to the episode's end
+        const int last = first_start(x, n, max(j1, past), x.TK, j1, lane) - 1;
+        const int s = j - first;
+        const bool mine = valid && s >= 0 && s < x.sinks;
+        for (int c = first / kFarChunk + 1; c <= last / kFarChunk; ++c) {
+            if (c * kFarChunk + kFarChunk <= past || !mine) continue;
+            const float* const from = far_sums<W>(x, n * kv + kvh, c, s);
+#pragma unroll
+            for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    dk[dt][r] += from[32 * dt + acc_row(r, h)];
+                    dv[dt][r] += from[W + 32 * dt + acc_row(r, h)];
+                }
         }
     }
     const bool fine = finite(dk) && finite(dv);
     if (valid) {
-        store_own<D>(seq_row_out<D>(x.dk, n, j, kvh), dk, x.scale, x.dim_k, x.dk.vec, h);
-        store_own<D>(seq_row_out<D>(x.dv, n, j, kvh), dv, kLess, x.dim_v, x.dv.vec, h);
+        store_own<D, kWide>(seq_row_out<D>(x.dk, n, j, kvh), dk, x.scale, x.dim_k, h);
+        store_own<D, kWide>(seq_row_out<D>(x.dv, n, j, kvh), dv, kLess, x.dim_v, h);
     }
     uint64_t again = __ballot(valid && !fine);
     for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
         careful_dkv<D>(x, n, kvh, mine0 + __builtin_ctzll(again), lane);
+}
+
+// What the queries of one chunk beyond its window give to the first steps of the
+// episode that the chunk begins in the middle of, summed over the heads that share
+// them: a wave to 32 of those steps.
+template <class D, int W, bool kWide>
+__global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
+{
+    using Tile = AttTile<D, W>;
+    constexpr int BQ = 32, kBytes = BQ * Tile::kRow;
+    __shared__ alignas(16) char lds[4][2][kBytes];
+    __shared__ QueryRows rows[4];
+    const int lane = threadIdx.x % kWave, h = lane >> 5, wave = threadIdx.x / kWave;
+    const int past = x.TK - x.T, kv = x.H / x.group, chunks = x.far_chunks, parts = (x.sinks + 31) / 32;
+    int64_t id = (int64_t)blockIdx.x * 4 + wave;
+    const int part = id % parts;
+    id /= parts;
+    const int c = (int)(id % chunks);
+    id /= chunks;
+    if (id >= x.N * kv) return;  // (waves are on their own: there is no barrier)
+    const int64_t row_of = id;
+    const int kvh = (int)(id % kv);
+    const int64_t n = id / kv;
+    const int i0 = c * kFarChunk, i1 = min(i0 + kFarChunk, x.TK);
+    if (i1 <= past) return;
+    const int first = episode_start(x, n, i0);
+    const int s = 32 * part + (lane & 31), j = first + s;
+    if (first / kFarChunk == c) return;
+    const bool valid = s < x.sinks && j < x.TK;
+    OwnRows<D, W, kWide> k, v;
+    k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
+    k.signs(x.scale < 0.0f);
+    v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
+    const int begin = max(max(i0, past), first + 32 * part + x.window);
+    const int end = first_start(x, n, max(i0, past), i1, first + 1, lane);
+    f32x16 dk[W / 32] = {}, dv[W / 32] = {};
+    QueryStage<D, W, kWide, kWave> stage;
+    for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head)
+        for (int i = begin; i < end; i += BQ) {
+            stage.fetch(x, n, head, i, end);
+            stage.put(lds[wave][0], lds[wave][1], rows[wave]);
+            __builtin_amdgcn_wave_barrier();
+            add_queries<D, W, kWide>(
+                x, lds[wave][0], lds[wave][1], rows[wave], k, v, false,
+                [&](int r, int) { return valid && i + r < end && j <= i + r - x.window; }, lane, dk, dv);
+            __builtin_amdgcn_wave_barrier();
+        }
+    if (s >= x.sinks) return;
+    float* const to = far_sums<W>(x, row_of, c, s);
+#pragma unroll
+    for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int at = 32 * dt + 8 * r4 + 4 * h;
+            *reinterpret_cast<f32x4*>(to + at) = f32x4{dk[dt][4 * r4], dk[dt][4 * r4 + 1], dk[dt][4 * r4 + 2], dk[dt][4 * r4 + 3]};
+            *reinterpret_cast<f32x4*>(to + W + at) = f32x4{dv[dt][4 * r4], dv[dt][4 * r4 + 1], dv[dt][4 * r4 + 2], dv[dt][4 * r4 + 3]};
+        }
 }
 
 // The first step of each step's episode, [N, TK]: a running maximum of the steps
@@ -1219,16 +1391,34 @@ inline void set_vec(SeqView& v, int64_t dim, int s)
     v.vec = rows_on(v, 16 / s, s) && dim % 8 == 0 ? 16 : rows_on(v, 4 / s, s) && dim % (4 / s) == 0 ? 4 : s;
 }
 
-inline size_t att_workspace(int64_t N, int64_t T, int64_t TK, int64_t H, bool reset, bool backward)
+// Where the parts of a call's workspace lie, in bytes.
+struct AttWorkspace {
+    size_t delta, far_part, bytes;
+    int32_t far_chunks;
+};
+
+inline AttWorkspace att_workspace(int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV, int64_t dk, int64_t dv,
+                                  int64_t window, int64_t sinks, bool reset, bool backward)
 {
-    size_t b = 0;
-    if (reset) b += ((size_t)(N * TK) * 4 + 255) / 256 * 256;
-    if (backward) b += ((size_t)(N * T * H) * 4 + 255) / 256 * 256;
-    return b;
+    auto whole = [](size_t b) { return (b + 255) / 256 * 256; };
+    AttWorkspace w{};
+    if (reset) w.bytes += whole((size_t)(N * TK) * 4);
+    w.delta = w.bytes;
+    if (!backward) return w;
+    w.bytes += whole((size_t)(N * T * H) * 4);
+    w.far_part = w.bytes;
+    // a chunk after an episode's first has queries that see its first steps by these alone
+    if (sinks > 0 && sinks <= kFarSinks && window < TK && TK > kFarChunk) {
+        w.far_chunks = (int32_t)((TK + kFarChunk - 1) / kFarChunk);
+        w.bytes += whole((size_t)(N * KV) * w.far_chunks * (size_t)std::min(sinks, TK) *
+                         (std::max(dk, dv) <= 64 ? 128 : 256) * 4);
+    }
+    return w;
 }
 
-inline void fill_attention(AttArgs& x, int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV, int64_t dk,
-                           int64_t dv, int64_t window, int64_t sinks, float scale, const void* reset, void* ws)
+inline void fill_attention(AttArgs& x, const AttWorkspace& w, int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV,
+                           int64_t dk, int64_t dv, int64_t window, int64_t sinks, float scale, const void* reset,
+                           void* ws)
 {
     x.N = N;
     x.T = (int32_t)T;
@@ -1246,10 +1436,11 @@ inline void fill_attention(AttArgs& x, int64_t N, int64_t T, int64_t TK, int64_t
     // at a window of 2, 1.4 times at 4, by nothing to be seen from 30 on.
     x.sum_delta = x.window <= 16;
     x.hpb = x.group % 4 == 0 ? 4 : x.group % 2 == 0 ? 2 : 1;
-    char* at = static_cast<char*>(ws);
+    char* const at = static_cast<char*>(ws);
     x.starts = reset != nullptr ? reinterpret_cast<const int32_t*>(at) : nullptr;
-    if (reset != nullptr) at += ((size_t)(N * TK) * 4 + 255) / 256 * 256;
-    x.delta = reinterpret_cast<float*>(at);
+    x.delta = reinterpret_cast<float*>(at + w.delta);
+    x.far_chunks = w.far_chunks;
+    x.far_part = w.far_chunks > 0 ? reinterpret_cast<float*>(at + w.far_part) : nullptr;
 }
 
 inline lrs_status launch_starts(const char* nm, const AttArgs& x, const SeqView& reset, hipStream_t stream)
@@ -1274,6 +1465,29 @@ inline uint64_t key_blocks(AttArgs& x)
     return (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.tiles;
 }
 
+// Whether the kernels may take rows by 16-byte units: dims of whole units of eight
+// elements, and a tile's rows within 32-bit offsets.
+inline bool all_wide(std::initializer_list<const SeqView*> views, int64_t dk, int64_t dv)
+{
+    bool wide = dk % 8 == 0 && dv % 8 == 0;
+    for (const SeqView* v : views) wide = wide && v->vec == 16 && v->step < (int64_t(1) << 22);
+    return wide;
+}
+
+template <class D, int W, bool kWide>
+lrs_status launch_backward(const char* nm, AttArgs x, hipStream_t stream)
+{
+    uint64_t blocks = query_blocks(x);
+    if (x.sum_delta) LRS_TRY(launch_seq(nm, attend_dq<D, W, kWide, true>, blocks, 256, stream, x));
+    LRS_TRY(launch_seq(nm, attend_dq<D, W, kWide, false>, blocks, 256, stream, x));
+    if (x.far_part != nullptr) {
+        const int64_t waves = x.N * (x.H / x.group) * x.far_chunks * ((x.sinks + 31) / 32);
+        LRS_TRY(launch_seq(nm, attend_far<D, W, kWide>, (uint64_t)((waves + 3) / 4), 256, stream, x));
+    }
+    blocks = key_blocks(x);
+    return launch_seq(nm, attend_dkv<D, W, kWide>, blocks, 256, stream, x);
+}
+
 template <class D>
 lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int64_t H, int64_t KV, int64_t dk,
                            int64_t dv, int64_t window, int64_t sinks, const D* q, const D* k, const D* v,
@@ -1291,9 +1505,10 @@ lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int
     const Span more[] = {{ws, ws_bytes}};
     SeqView a[6];
     LRS_TRY(check_seq_arrays(nm, N, T, args, strides, more, 1, 1, a));
-    LRS_TRY(check_workspace(nm, att_workspace(N, T, TK, H, reset != nullptr, false), ws, ws_bytes));
+    const AttWorkspace w = att_workspace(N, T, TK, H, KV, dk, dv, window, sinks, reset != nullptr, false);
+    LRS_TRY(check_workspace(nm, w.bytes, ws, ws_bytes));
     AttArgs x{};
-    fill_attention(x, N, T, TK, H, KV, dk, dv, window, sinks, scale, reset, ws);
+    fill_attention(x, w, N, T, TK, H, KV, dk, dv, window, sinks, scale, reset, ws);
     x.q = a[0];
     x.k = a[1];
     x.v = a[2];
@@ -1306,8 +1521,10 @@ lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int
     const uint64_t blocks = query_blocks(x);
     LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N <= kMaxGrid, "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[3], stream));
-    return launch_seq(nm, std::max(dk, dv) <= 64 ? attend_forward<D, 64> : attend_forward<D, 128>, blocks, 256,
-                      stream, x);
+    const bool narrow = std::max(dk, dv) <= 64, wide = all_wide({&x.q, &x.k, &x.v, &x.o}, dk, dv);
+    return launch_seq(nm, wide ? (narrow ? attend_forward<D, 64, true> : attend_forward<D, 128, true>)
+                               : (narrow ? attend_forward<D, 64, false> : attend_forward<D, 128, false>),
+                      blocks, 256, stream, x);
 }
 
 template <class D>
@@ -1332,9 +1549,10 @@ lrs_status attention_backward_entry(const char* nm, int64_t N, int64_t T, int64_
     const Span more[] = {{ws, ws_bytes}};
     SeqView a[10];
     LRS_TRY(check_seq_arrays(nm, N, T, args, strides, more, 1, 1, a));
-    LRS_TRY(check_workspace(nm, att_workspace(N, T, TK, H, reset != nullptr, true), ws, ws_bytes));
+    const AttWorkspace w = att_workspace(N, T, TK, H, KV, dk, dv, window, sinks, reset != nullptr, true);
+    LRS_TRY(check_workspace(nm, w.bytes, ws, ws_bytes));
     AttArgs x{};
-    fill_attention(x, N, T, TK, H, KV, dk, dv, window, sinks, scale, reset, ws);
+    fill_attention(x, w, N, T, TK, H, KV, dk, dv, window, sinks, scale, reset, ws);
     x.dout = a[0];
     x.q = a[1];
     x.k = a[2];
@@ -1348,12 +1566,11 @@ lrs_status attention_backward_entry(const char* nm, int64_t N, int64_t T, int64_
     for (SeqView* w : {&x.v, &x.o, &x.dout, &x.dv}) set_vec(*w, dv, s);
     LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && (uint64_t)N <= kMaxGrid,
                 "%s: num_envs * heads * steps is too large", nm);
-    const bool narrow = std::max(dk, dv) <= 64;
     LRS_TRY(launch_starts(nm, x, a[4], stream));
-    uint64_t blocks = query_blocks(x);
-    LRS_TRY(launch_seq(nm, narrow ? attend_dq<D, 64> : attend_dq<D, 128>, blocks, 256, stream, x));
-    blocks = key_blocks(x);
-    return launch_seq(nm, narrow ? attend_dkv<D, 64> : attend_dkv<D, 128>, blocks, 256, stream, x);
+    const bool wide = all_wide({&x.q, &x.k, &x.v, &x.o, &x.dout, &x.dq, &x.dk, &x.dv}, dk, dv);
+    if (std::max(dk, dv) <= 64)
+        return wide ? launch_backward<D, 64, true>(nm, x, stream) : launch_backward<D, 64, false>(nm, x, stream);
+    return wide ? launch_backward<D, 128, true>(nm, x, stream) : launch_backward<D, 128, false>(nm, x, stream);
 }
 
 // The splits of a step's slots: as many as make four blocks for each of 256 CUs, of

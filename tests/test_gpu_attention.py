@@ -48,6 +48,11 @@ CASES = [
     (3, 65, 8, 2, 64, 64, 0, 16, 33, 0.2),    # short episodes, more first steps than they have
     (1, 520, 1, 1, 64, 64, 0, 30, 70, None),  # first steps over more than a tile
     (1, 700, 2, 1, 128, 128, 3, 129, 4, 0.004),
+    # first steps whose queries go on over chunks of 256 steps, with episodes across their borders
+    (1, 1300, 2, 1, 64, 64, 0, 20, 4, 0.003),
+    (2, 900, 1, 1, 32, 16, 300, 10, 64, 0.004),
+    (1, 800, 4, 2, 128, 64, 0, 100, 40, None),
+    (1, 1000, 1, 1, 64, 64, 40, 5, 65, 0.002),
 ]
 
 
@@ -56,6 +61,16 @@ CASES = [
 def test_against_definition(dt, case):
     n, t, heads, kv, dk, dv, past, window, sinks, reset_p = case
     q, k, v, do, reset = inputs(1, dt, n, t, heads, kv, dk, dv, past, reset_p)
+    got = run_all(q, k, v, do, window=window, sinks=sinks, reset=reset)
+    compare(got, ref.attention(q, k, v, window, sinks, reset, do=do))
+
+
+@pytest.mark.parametrize("begins", [[250, 330], [255], [256], [257, 511, 512], [200, 300], [192, 700]])
+@pytest.mark.parametrize("window,sinks", [(7, 33), (100, 64), (300, 3)])
+def test_first_steps_around_chunks(begins, window, sinks):
+    q, k, v, do, _ = inputs(14, "f32", 1, 790, 2, 1, 32, 32)
+    reset = torch.zeros(1, 790, dtype=torch.bool, device="cuda")
+    reset[0, begins] = True
     got = run_all(q, k, v, do, window=window, sinks=sinks, reset=reset)
     compare(got, ref.attention(q, k, v, window, sinks, reset, do=do))
 
