@@ -26,6 +26,21 @@
 
 #include "sequence.hpp"
 
+#ifndef LRS_ORDER
+#define LRS_ORDER 0
+#endif
+#if LRS_ORDER
+#define LRS_KEEP_ORDER() __builtin_amdgcn_sched_barrier(0)
+#else
+#define LRS_KEEP_ORDER()
+#endif
+
+#ifdef LRS_PRIO
+#define LRS_SETPRIO(v) __builtin_amdgcn_s_setprio(v)
+#else
+#define LRS_SETPRIO(v)
+#endif
+
 namespace lrs {
 
 constexpr int kMaxAttDim = 128;
@@ -36,6 +51,7 @@ struct AttArgs {
     SeqView q, k, v, o, lse;    // lse float32 [N, T, H], nullable in the forward
     SeqView dout, dq, dk, dv;
     const int32_t* starts;      // [N, TK]: the first step of each key step's episode; null: 0
+    const int32_t* ends;        // [N, TK]: the step behind its last; null: TK
     float* delta;               // D, [N, H, T]
     float* far_part;            // [N, KV, far_chunks, sinks, 2 W] sums of attend_far; null: it does not run
     int64_t N;
@@ -216,6 +232,7 @@ struct AttStage {
 // The two ranges of keys of one query, as first key and length.
 struct Seen {
     int near, near_len, far, far_len;
+    bool far_any;  // whether any query has first steps before its near range: of the call
 };
 
 __device__ __forceinline__ int episode_start(const AttArgs& x, int64_t n, int j)
@@ -230,12 +247,29 @@ __device__ __forceinline__ Seen seen_by(const AttArgs& x, int i, int start)
     s.near_len = i - s.near + 1;
     s.far = start;
     s.far_len = min(x.sinks, s.near - start);
+    s.far_any = x.sinks > 0;
     return s;
 }
 
 __device__ __forceinline__ bool sees(const Seen& s, int j)
 {
-    return (unsigned)(j - s.near) < (unsigned)s.near_len || (unsigned)(j - s.far) < (unsigned)s.far_len;
+    // (without a branch between the two)
+    return (bool)(((unsigned)(j - s.near) < (unsigned)s.near_len) | ((unsigned)(j - s.far) < (unsigned)s.far_len));
+}
+
+// Rows begin .. end - 1 of a product whose first row is step j0, as the bits of what
+// register r of a lane of half h holds: bit acc_row(r, 0).
+__device__ __forceinline__ uint32_t row_bits(int begin, int end, int j0, int h)
+{
+    const int lo = min(max(begin - j0, 0), 32), hi = min(max(end - j0, 0), 32);
+    const uint64_t bits = ((uint64_t(1) << hi) - 1) & ~((uint64_t(1) << lo) - 1);
+    return (uint32_t)bits >> (4 * h);
+}
+// v where the bit of register r is set, else `other`: two instructions, and no compare.
+__device__ __forceinline__ float where_bit(uint32_t bits, int r, float v, float other)
+{
+    const uint32_t all = (uint32_t)__builtin_amdgcn_sbfe((int)bits, acc_row(r, 0), 1);
+    return __uint_as_float((all & __float_as_uint(v)) | (~all & __float_as_uint(other)));
 }
 
 // What a block's queries see: tiles of kTile keys, the far range's first.
@@ -279,12 +313,19 @@ struct WaveQueries {
         seen = seen_by(x, i, episode_start(x, n, i));
         // first steps that lie among the block's near keys come with their tiles
         const int least = seen.far + x.sinks > block_near ? max(seen.far, block_near) : seen.near;
-        lo_least = __shfl(least, 0);
-        lo_most = __shfl(seen.near, 31);
+        lo_least = __builtin_amdgcn_readlane(least, 0);
+        lo_most = __builtin_amdgcn_readlane(seen.near, 31);
         // steps ascend and so do starts: lane 31 (clamped to the last step) has the most
         if (!valid) seen.near_len = seen.far_len = 0;
     }
     __device__ __forceinline__ bool any() const { return first <= last; }
+    // The rows of a product from key j0 on that the lane's query sees, of a tile that ends at j1.
+    __device__ __forceinline__ uint32_t bits(bool is_far, int j0, int j1, int h) const
+    {
+        uint32_t b = is_far ? 0 : row_bits(seen.near, seen.near + seen.near_len, j0, h);
+        if (seen.far_any) b |= row_bits(seen.far, min(seen.far + seen.far_len, j1), j0, h);
+        return b;
+    }
     // Whether some query may see keys j0 .. j1 - 1 of a tile, and whether all see all.
     __device__ __forceinline__ bool touches(const KeyTiles& kt, bool is_far, int j0, int j1) const
     {
@@ -388,7 +429,7 @@ __device__ __forceinline__ void careful_dq(const AttArgs& x, int64_t n, int head
         if (lane + e * kWave < x.dim_k) out[lane + e * kWave] = from_f32<D>(acc[e]);
 }
 
-template <class D>
+template <class D, bool kK, bool kV>
 __device__ __forceinline__ void careful_dkv(const AttArgs& x, int64_t n, int kvh, int j, int lane)
 {
     const int past = x.TK - x.T;
@@ -426,8 +467,8 @@ __device__ __forceinline__ void careful_dkv(const AttArgs& x, int64_t n, int kvh
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int c = lane + e * kWave;
-        if (c < x.dim_k) seq_row_out<D>(x.dk, n, j, kvh)[c] = from_f32<D>(dk[e]);
-        if (c < x.dim_v) seq_row_out<D>(x.dv, n, j, kvh)[c] = from_f32<D>(dv[e]);
+        if (kK && c < x.dim_k) seq_row_out<D>(x.dk, n, j, kvh)[c] = from_f32<D>(dk[e]);
+        if (kV && c < x.dim_v) seq_row_out<D>(x.dv, n, j, kvh)[c] = from_f32<D>(dv[e]);
     }
 }
 
@@ -493,6 +534,40 @@ __device__ __forceinline__ float own_dot(const SeqView& v, int64_t n, int64_t t,
     return sum + __shfl_xor(sum, 32);
 }
 
+// The products of 32 rows of tile `ta` (and of `tb`) with the wave's own rows, over
+// all W elements.  Fragments of LDS are read ahead of the products in groups: left
+// to itself the compiler reads one, waits for it, and multiplies.
+template <class D, int W, bool kTwo, bool kWide>
+__device__ __forceinline__ void row_products(const char* ta, const OwnRows<D, W, kWide>& a, const char* tb,
+                                             const OwnRows<D, W, kWide>& b, int row, int lane, f32x16& s, f32x16& t)
+{
+    using Tile = AttTile<D, W>;
+    #ifndef LRS_G
+#define LRS_G 2
+#endif
+    constexpr int G = sizeof(D) == 4 ? 1 : LRS_G, N = W / 16 / G;
+    AFrag<D> fa[2][G], fb[2][G];
+    auto load = [&](int g) {
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+            fa[g & 1][e] = Tile::rows(ta, row, g * G + e, lane);
+            if constexpr (kTwo) fb[g & 1][e] = Tile::rows(tb, row, g * G + e, lane);
+        }
+    };
+    load(0);
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+        LRS_KEEP_ORDER();
+        if (g + 1 < N) load(g + 1);
+        LRS_KEEP_ORDER();
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+            s = mma32<D>(fa[g & 1][e], a.f[g * G + e], s);
+            if constexpr (kTwo) t = mma32<D>(fb[g & 1][e], b.f[g * G + e], t);
+        }
+    }
+}
+
 // Writes a product whose columns are the wave's rows (a lane's own: `row`) and
 // whose rows are elements; rows of memory get four elements at a time.
 template <class D, bool kWide, int kTiles>
@@ -534,6 +609,8 @@ __device__ __forceinline__ bool finite(const f32x16 (&acc)[kTiles])
 template <class D, int W>
 constexpr int kKeyTile = sizeof(D) == 4 ? 32 : 64;
 template <class D, int W>
+constexpr int kGradTile = sizeof(D) == 4 && W == 128 ? 32 : 64;
+template <class D, int W>
 constexpr int kAttBlocks = sizeof(D) == 4 && W == 128 ? 1 : 2;  // blocks per CU
 
 // A block's place: its heads, and the steps of its four waves.
@@ -547,7 +624,7 @@ struct AttBlock {
         const int hblocks = x.H / x.hpb, rows = 4 / x.hpb * 32;
         const uint32_t tile = id % x.tiles, hb = id / x.tiles % hblocks;
         n = id / x.tiles / hblocks;
-        const int wave = threadIdx.x / kWave;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         head = hb * x.hpb + wave % x.hpb;
         kvh = head / x.group;
         step0 = tile * rows + wave / x.hpb * 32;
@@ -592,21 +669,19 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
         const bool is_far = it < kt.far_tiles;
         if (wq.touches(kt, is_far, j0, j1)) {
             f32x16 s[S] = {};
+            LRS_SETPRIO(1);
 #pragma unroll
             for (int ks = 0; ks < W / 16; ++ks)
 #pragma unroll
                 for (int a = 0; a < S; ++a) s[a] = mma32<D>(Tile::rows(tk, 32 * a, ks, lane), q.f[ks], s[a]);
+            LRS_SETPRIO(0);
             if (!wq.whole(is_far, j0, j1, BK)) {
-                Seen see = wq.seen;
-                if (is_far) {
-                    see.near_len = 0;
-                    see.far_len = min(see.far_len, max(0, j1 - see.far));
+#pragma unroll
+                for (int a = 0; a < S; ++a) {
+                    const uint32_t bits = wq.bits(is_far, j0 + 32 * a, j1, h);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[a][r] = where_bit(bits, r, s[a][r], -INFINITY);
                 }
-#pragma unroll
-                for (int a = 0; a < S; ++a)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (!sees(see, j0 + 32 * a + acc_row(r, h))) s[a][r] = -INFINITY;
             }
             float top = s[0][0];
 #pragma unroll
@@ -668,7 +743,7 @@ template <class D, int W, bool kWide, bool kSum>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
-    constexpr int BK = 32, kBytes = BK * Tile::kRow;
+    constexpr int BK = kGradTile<D, W>, kBytes = BK * Tile::kRow;
     __shared__ alignas(16) char lds[2][2][kBytes];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
     const AttBlock b(x);
@@ -709,25 +784,28 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
         int j0, j1;
         kt.get(it, BK, j0, j1);
         const bool is_far = it < kt.far_tiles;
-        if (wq.touches(kt, is_far, j0, j1)) {
-            f32x16 s = {}, dp = {};
 #pragma unroll
-            for (int ks = 0; ks < W / 16; ++ks) {
-                s = mma32<D>(Tile::rows(tk, 0, ks, lane), q.f[ks], s);
-                dp = mma32<D>(Tile::rows(tv, 0, ks, lane), d_o.f[ks], dp);
-            }
+        for (int at = 0; at < BK; at += 32) {
+            const int ja = j0 + at, jb = min(ja + 32, j1);
+            if (ja >= j1 || !wq.touches(kt, is_far, ja, jb)) continue;
+            f32x16 s = {}, dp = {};
+            row_products<D, W, true>(tk, q, tv, d_o, at, lane, s, dp);
+            constexpr int N = W / 32;
+            AFrag<D> ck[2][N];
+            auto load = [&](int u) {
+#pragma unroll
+                for (int dt = 0; dt < N; ++dt) ck[u][dt] = Tile::columns(tk, at + 16 * u, 32 * dt, lane);
+            };
+            LRS_KEEP_ORDER();
+            if constexpr (!kSum) load(0);
+            LRS_KEEP_ORDER();
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2)) * (dp[r] - delta);
-            if (!wq.whole(is_far, j0, j1, BK)) {
-                Seen see = wq.seen;
-                if (is_far) {
-                    see.near_len = 0;
-                    see.far_len = min(see.far_len, max(0, j1 - see.far));
-                }
+            if (!wq.whole(is_far, ja, jb, 32)) {
+                const uint32_t bits = wq.bits(is_far, ja, j1, h);
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (!sees(see, j0 + acc_row(r, h))) dp[r] = 0.0f;
+                for (int r = 0; r < 16; ++r) dp[r] = where_bit(bits, r, dp[r], 0.0f);
             }
             if constexpr (kSum) {
 #pragma unroll
@@ -735,14 +813,16 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
             } else {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
+                    LRS_KEEP_ORDER();
+                    if (u == 0) load(1);
+                    LRS_KEEP_ORDER();
                     const AFrag<D> ds = operand<D>(dp, u);
-                    AFrag<D> rest;
-                    if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
 #pragma unroll
-                    for (int dt = 0; dt < W / 32; ++dt) {
-                        const AFrag<D> k = Tile::columns(tk, 16 * u, 32 * dt, lane);
-                        dq[dt] = mma32<D>(k, ds, dq[dt]);
-                        if constexpr (sizeof(D) == 2) dq[dt] = mma32<D>(k, rest, dq[dt]);
+                    for (int dt = 0; dt < N; ++dt) dq[dt] = mma32<D>(ck[u][dt], ds, dq[dt]);
+                    if constexpr (sizeof(D) == 2) {
+                        const AFrag<D> rest = operand_rest<D>(dp, u, ds);
+#pragma unroll
+                        for (int dt = 0; dt < N; ++dt) dq[dt] = mma32<D>(ck[u][dt], rest, dq[dt]);
                     }
                 }
             }
@@ -772,116 +852,112 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
 template <class D>
 constexpr float kWeightBits = std::is_same<D, f16_t>::value ? 10.0f : 0.0f;
 
-// What goes with a tile of 32 queries: their lse (in powers of two, as the weights
-// take it), D, and first steps.
+// What goes with a tile of queries: their lse (in powers of two, as the weights take
+// it) and D.
+template <int kRows>
 struct QueryRows {
-    alignas(16) float lse2[32], delta[32];
-    alignas(16) int32_t start[32];
+    alignas(16) float lse2[kRows], delta[kRows];
 };
 
-// A tile of 32 queries and their gradients on its way to LDS, from query step i (of
-// the keys' steps) on.
-template <class D, int W, bool kWide, int kThreads>
+template <class D>
+constexpr float kLessWeight = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
+
+// A tile of queries and their gradients on its way to LDS, from query step i (of the
+// keys' steps) on.
+template <class D, int W, bool kWide, int kRows, int kThreads>
 struct QueryStage {
-    static constexpr float kLess = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
-    AttStage<D, W, 32, kWide, kThreads> q, d_o;
+    AttStage<D, W, kRows, kWide, kThreads> q, d_o;
     float lse, delta;
-    int start;
     bool in;
 
     __device__ __forceinline__ void fetch(const AttArgs& x, int64_t n, int head, int i, int end)
     {
-        const int past = x.TK - x.T, count = min(32, end - i);
+        const int past = x.TK - x.T, count = min(kRows, end - i);
         q.fetch(x.q, n, head, i - past, count, x.dim_k);
         d_o.fetch(x.dout, n, head, i - past, count, x.dim_v);
         // by every thread alike, and used only in put(): a use here would wait for all loads
-        const int a = threadIdx.x & 31, at = min(i + a, end - 1);
+        const int a = (int)(threadIdx.x % kRows), at = min(i + a, end - 1);
         in = a < count;
         lse = *seq_row<float>(x.lse, n, at - past, head);
         delta = x.delta[(n * x.H + head) * x.T + at - past];
-        start = episode_start(x, n, at);
     }
-    __device__ __forceinline__ void put(char* tq, char* to, QueryRows& rows) const
+    __device__ __forceinline__ void put(char* tq, char* to, QueryRows<kRows>& rows) const
     {
         q.put(tq);
         d_o.put(to);
-        if (threadIdx.x % kThreads < 32) {
-            const int a = threadIdx.x & 31;
+        if (threadIdx.x % kThreads < kRows) {
+            const int a = threadIdx.x % kRows;
             // queries behind the end have no weights
             rows.lse2[a] = in ? fmaf(lse, kAttLog2e, -kWeightBits<D>) : INFINITY;
-            rows.delta[a] = in ? delta * kLess : 0.0f;
-            rows.start[a] = start;
+            rows.delta[a] = in ? delta * kLessWeight<D> : 0.0f;
         }
     }
 };
 
-// Adds what 32 queries in LDS give to the gradients of the wave's keys.  sees(row,
-// start): whether a query sees the lane's key; not asked where `whole`.
-template <class D, int W, bool kWide, class Sees>
-__device__ __forceinline__ void add_queries(const AttArgs& x, const char* tq, const char* to, const QueryRows& row,
+// Adds what 32 queries in LDS give to the gradients of the wave's keys: of the keys
+// (kK), of the values (kV).  bits: the rows whose queries see the lane's key; not
+// looked at where `whole`.
+template <class D, int W, bool kWide, bool kK, bool kV, class Rows>
+__device__ __forceinline__ void add_queries(const AttArgs& x, const char* tq, const char* to, const Rows& row, int at,
                                             const OwnRows<D, W, kWide>& k, const OwnRows<D, W, kWide>& v, bool whole,
-                                            Sees sees, int lane, f32x16 (&dk)[W / 32], f32x16 (&dv)[W / 32])
+                                            uint32_t bits, int lane, f32x16 (&dk)[W / 32], f32x16 (&dv)[W / 32])
 {
     using Tile = AttTile<D, W>;
-    constexpr float kLess = QueryStage<D, W, kWide, 256>::kLess;
+    constexpr float kLess = kLessWeight<D>;
+    constexpr int N = W / 32;
     const int h = lane >> 5;
     f32x16 s = {}, dp = {};
+    row_products<D, W, kK>(tq, k, to, v, at, lane, s, dp);
+    LRS_KEEP_ORDER();
+    AFrag<D> cq[2][N], co[2][N];
+    auto load = [&](int u) {
 #pragma unroll
-    for (int ks = 0; ks < W / 16; ++ks) {
-        s = mma32<D>(Tile::rows(tq, 0, ks, lane), k.f[ks], s);
-        dp = mma32<D>(Tile::rows(to, 0, ks, lane), v.f[ks], dp);
-    }
+        for (int dt = 0; dt < N; ++dt) {
+            if constexpr (kV) co[u][dt] = Tile::columns(to, at + 16 * u, 32 * dt, lane);
+            if constexpr (kK) cq[u][dt] = Tile::columns(tq, at + 16 * u, 32 * dt, lane);
+        }
+    };
+    load(0);
+    LRS_KEEP_ORDER();
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
-        const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&row.lse2[8 * r4 + 4 * h]);
-        const f32x4 delta = *reinterpret_cast<const f32x4*>(&row.delta[8 * r4 + 4 * h]);
+        const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&row.lse2[at + 8 * r4 + 4 * h]);
+        const f32x4 delta = *reinterpret_cast<const f32x4*>(&row.delta[at + 8 * r4 + 4 * h]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = 4 * r4 + e;
             s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2[e]));
-            dp[r] = s[r] * (kLess == 1.0f ? dp[r] - delta[e] : fmaf(dp[r], kLess, -delta[e]));
+            if constexpr (kK) dp[r] = s[r] * (kLess == 1.0f ? dp[r] - delta[e] : fmaf(dp[r], kLess, -delta[e]));
         }
     }
     if (!whole) {
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-            const u32x4 st = *reinterpret_cast<const u32x4*>(&row.start[8 * r4 + 4 * h]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!sees(8 * r4 + 4 * h + e, (int)st[e])) s[4 * r4 + e] = dp[4 * r4 + e] = 0.0f;
+        for (int r = 0; r < 16; ++r) {
+            s[r] = where_bit(bits, r, s[r], 0.0f);
+            if constexpr (kK) dp[r] = where_bit(bits, r, dp[r], 0.0f);
         }
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const AFrag<D> p = operand<D>(s, u), ds = operand<D>(dp, u);
-        AFrag<D> rest;
-        if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
+        LRS_KEEP_ORDER();
+        if (u == 0) load(1);
+        LRS_KEEP_ORDER();
+        if constexpr (kV) {
+            const AFrag<D> p = operand<D>(s, u);
 #pragma unroll
-        for (int dt = 0; dt < W / 32; ++dt) {
-            dv[dt] = mma32<D>(Tile::columns(to, 16 * u, 32 * dt, lane), p, dv[dt]);
-            const AFrag<D> q = Tile::columns(tq, 16 * u, 32 * dt, lane);
-            dk[dt] = mma32<D>(q, ds, dk[dt]);
-            if constexpr (sizeof(D) == 2) dk[dt] = mma32<D>(q, rest, dk[dt]);
+            for (int dt = 0; dt < N; ++dt) dv[dt] = mma32<D>(co[u][dt], p, dv[dt]);
+        }
+        if constexpr (kK) {
+            const AFrag<D> ds = operand<D>(dp, u);
+#pragma unroll
+            for (int dt = 0; dt < N; ++dt) dk[dt] = mma32<D>(cq[u][dt], ds, dk[dt]);
+            if constexpr (sizeof(D) == 2) {
+                const AFrag<D> rest = operand_rest<D>(dp, u, ds);
+#pragma unroll
+                for (int dt = 0; dt < N; ++dt) dk[dt] = mma32<D>(cq[u][dt], rest, dk[dt]);
+            }
         }
     }
-}
-
-// The first step from lo on whose episode begins at `from` or later, hi if there is
-// none: starts ascend, and 64 of them are looked at at once.
-__device__ __forceinline__ int first_start(const AttArgs& x, int64_t n, int lo, int hi, int from, int lane)
-{
-    if (x.starts == nullptr) return max(lo, hi);
-    while (lo < hi) {
-        const int step = (hi - lo + kWave - 1) / kWave;
-        const int at = min(lo + lane * step + step - 1, hi - 1);
-        const uint64_t past = __ballot(x.starts[n * x.TK + at] >= from);
-        if (past == 0) return hi;
-        const int f = __builtin_ctzll(past);
-        const int end = min(lo + f * step + step - 1, hi - 1);  // the first looked at that is past
-        lo = lo + f * step;
-        hi = end;
-    }
-    return lo;
 }
 
 // First steps of an episode are seen by all of its queries.  Those beyond the end of
@@ -900,39 +976,69 @@ __device__ __forceinline__ float* far_sums(const AttArgs& x, int64_t row, int ch
 
 // Keys are the columns: a wave holds 32 of them and their values, a block 128;
 // queries and their gradients come in tiles of 32, head after head of the group.
-template <class D, int W, bool kWide>
-__global__ __launch_bounds__(256, 1) void attend_dkv(const AttArgs x)
+// Rows of more than 128 bytes take a kernel for the gradient of the keys (kK) and one
+// for that of the values (kV): together they need more registers than two waves on a
+// SIMD have, and one wave alone waits through its softmax.
+template <class D, int W>
+#ifndef LRS_BQ
+#define LRS_BQ 32
+#endif
+constexpr int kQueryTile = W == 128 ? LRS_BQ : 64;
+
+template <class D, int W>
+constexpr bool kSplitGrads = W * (int)sizeof(D) > 128;
+
+// The queries that see key j are those from j to here (in attend_dkv: without those of
+// later chunks, which attend_far does).
+__device__ __forceinline__ int seen_until(const AttArgs& x, int64_t n, int j)
+{
+    const int start = episode_start(x, n, j), end = x.ends != nullptr ? x.ends[n * x.TK + j] : x.TK;
+    int until = j + min(x.window, x.TK - j);
+    if (j < start + x.sinks)
+        until = max(until, x.far_part != nullptr ? (start / kFarChunk + 1) * kFarChunk : x.TK);
+    return min(until, end);
+}
+
+template <class D, int W, bool kWide, bool kK, bool kV>
+__global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void attend_dkv(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
-    constexpr int BQ = 32;
+    constexpr int BQ = kQueryTile<D, W>;
     __shared__ alignas(16) char lds[2][2][BQ * Tile::kRow];
-    __shared__ QueryRows rows[2];
-    const int lane = threadIdx.x % kWave, h = lane >> 5, wave = threadIdx.x / kWave;
+    __shared__ QueryRows<BQ> rows[2];
+    const int lane = threadIdx.x % kWave, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int past = x.TK - x.T, kv = x.H / x.group;
     const uint32_t id = by_xcd(blockIdx.x, gridDim.x);
     const int kvh = id / x.tiles % kv;
     const int64_t n = id / x.tiles / kv;
     const int j0 = (int)(id % x.tiles) * 128, j1 = min(j0 + 128, x.TK);
-    const int mine0 = j0 + 32 * wave, mine1 = min(mine0 + 32, x.TK), j = mine0 + (lane & 31);
+    const int mine0 = j0 + 32 * wave, j = mine0 + (lane & 31);
     const bool valid = j < x.TK;
     OwnRows<D, W, kWide> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
     k.signs(x.scale < 0.0f);
-    v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
+    if constexpr (kK) v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
 
-    // The queries that see a key here: from begin to end.  first: the episode of the
-    // last key, the only one that goes on beyond the block.
-    const int begin = max(j0, past), first = episode_start(x, n, j1 - 1);
-    const bool has_first = first + x.sinks > j0 && x.sinks > 0;
-    const int chunk_end = x.far_part != nullptr ? (first / kFarChunk + 1) * kFarChunk : x.TK;
-    int end = min(j1 - 1 + x.window, x.TK);
-    if (has_first) end = max(end, min(chunk_end, x.TK));
-    end = first_start(x, n, max(j1, past), max(end, past), j1, lane);
+    // The queries that see the lane's key, the wave's keys, and one of the block's.
+    const int until = valid ? seen_until(x, n, j) : 0;
+    int most = until, least = until;
+    for (int o = 16; o > 0; o >>= 1) {
+        most = max(most, __shfl_xor(most, o));
+        least = min(least, __shfl_xor(least, o));
+    }
+    most = __builtin_amdgcn_readfirstlane(most);
+    least = __builtin_amdgcn_readfirstlane(least);
+    int end = 0;
+    for (int a = j0 + lane; a < j1; a += kWave) end = max(end, seen_until(x, n, a));
+    for (int o = 32; o > 0; o >>= 1) end = max(end, __shfl_xor(end, o));
+    end = __builtin_amdgcn_readfirstlane(end);
+    const int begin = max(j0, past);
 
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
     const int tiles = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = tiles * x.group;
     if (total > 0) {
-        QueryStage<D, W, kWide, 256> stage;
+        QueryStage<D, W, kWide, BQ, 256> stage;
         int head = kvh * x.group, tile = 0, next_head = head, next = 0;
         auto fetch = [&]() {
             stage.fetch(x, n, next_head, begin + next * BQ, end);
@@ -946,21 +1052,16 @@ __global__ __launch_bounds__(256, 1) void attend_dkv(const AttArgs x)
         if (total > 1) fetch();
         for (int it = 0; it < total; ++it) {
             __syncthreads();
-            const QueryRows& row = rows[it & 1];
-            const int i = begin + tile * BQ, i_last = min(i + BQ, end) - 1;
-            const int least = row.start[0], most = row.start[BQ - 1];
-            if (mine0 <= i_last && mine1 > least && (mine1 > i - x.window + 1 || mine0 < most + x.sinks)) {
-                // whole: every query of the tile sees every key of the wave
-                const bool whole = i + BQ <= end && mine0 + 32 <= x.TK && mine0 + 31 <= i && most <= mine0 &&
-                                   mine0 > i + BQ - 1 - x.window;
-                add_queries<D, W, kWide>(
-                    x, lds[it & 1][0], lds[it & 1][1], row, k, v, whole,
-                    [&](int r, int start) {
-                        const int qi = i + r;
-                        return j <= qi && j >= start && qi < end && valid &&
-                               (j > qi - x.window || (j < start + x.sinks && qi < chunk_end));
-                    },
-                    lane, dk, dv);
+            const QueryRows<BQ>& row = rows[it & 1];
+#pragma unroll
+            for (int at = 0; at < BQ; at += 32) {
+                const int i = begin + tile * BQ + at;
+                if (i < most && mine0 <= i + 31) {
+                    // whole: every query of the tile sees every key of the wave
+                    const bool whole = mine0 + 31 <= i && i + 32 <= least;
+                    add_queries<D, W, kWide, kK, kV>(x, lds[it & 1][0], lds[it & 1][1], row, at, k, v, whole,
+                                                     whole ? 0 : row_bits(j, until, i, h), lane, dk, dv);
+                }
             }
             if (++tile == tiles) {
                 tile = 0;
@@ -972,44 +1073,51 @@ __global__ __launch_bounds__(256, 1) void attend_dkv(const AttArgs x)
             }
         }
     }
-    constexpr float kLess = QueryStage<D, W, kWide, 256>::kLess;
-    if (has_first && x.far_part != nullptr) {
+    constexpr float kLess = kLessWeight<D>;
+    const int first = episode_start(x, n, min(j, x.TK - 1));
+    if (x.far_part != nullptr && __any(valid && j < first + x.sinks)) {
         // the chunks after the first, up to the episode's end
-        const int last = first_start(x, n, max(j1, past), x.TK, j1, lane) - 1;
         const int s = j - first;
-        const bool mine = valid && s >= 0 && s < x.sinks;
-        for (int c = first / kFarChunk + 1; c <= last / kFarChunk; ++c) {
-            if (c * kFarChunk + kFarChunk <= past || !mine) continue;
-            const float* const from = far_sums<W>(x, n * kv + kvh, c, s);
+        const int last = valid && s < x.sinks ? (x.ends != nullptr ? x.ends[n * x.TK + j] : x.TK) - 1 : -1;
+        const int c0 = max(first / kFarChunk + 1, past / kFarChunk);
+        auto add = [&](f32x16(&acc)[W / 32], int from) {
 #pragma unroll
             for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    dk[dt][r] += from[32 * dt + acc_row(r, h)];
-                    dv[dt][r] += from[W + 32 * dt + acc_row(r, h)];
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int c = c0; c <= last / kFarChunk; ++c)
+                        sum += *reinterpret_cast<const f32x4*>(far_sums<W>(x, n * kv + kvh, c, s) + from + 32 * dt +
+                                                               8 * r4 + 4 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[dt][4 * r4 + e] += sum[e];
                 }
-        }
+        };
+        if constexpr (kK) add(dk, 0);
+        if constexpr (kV) add(dv, W);
     }
-    const bool fine = finite(dk) && finite(dv);
+    bool fine = true;
+    if constexpr (kK) fine = finite(dk);
+    if constexpr (kV) fine = fine && finite(dv);
     if (valid) {
-        store_own<D, kWide>(seq_row_out<D>(x.dk, n, j, kvh), dk, x.scale, x.dim_k, h);
-        store_own<D, kWide>(seq_row_out<D>(x.dv, n, j, kvh), dv, kLess, x.dim_v, h);
+        if constexpr (kK) store_own<D, kWide>(seq_row_out<D>(x.dk, n, j, kvh), dk, x.scale, x.dim_k, h);
+        if constexpr (kV) store_own<D, kWide>(seq_row_out<D>(x.dv, n, j, kvh), dv, kLess, x.dim_v, h);
     }
     uint64_t again = __ballot(valid && !fine);
     for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
-        careful_dkv<D>(x, n, kvh, mine0 + __builtin_ctzll(again), lane);
+        careful_dkv<D, kK, kV>(x, n, kvh, mine0 + __builtin_ctzll(again), lane);
 }
 
 // What the queries of one chunk beyond its window give to the first steps of the
 // episode that the chunk begins in the middle of, summed over the heads that share
 // them: a wave to 32 of those steps.
-template <class D, int W, bool kWide>
+template <class D, int W, bool kWide, bool kK, bool kV>
 __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
     constexpr int BQ = 32, kBytes = BQ * Tile::kRow;
     __shared__ alignas(16) char lds[4][2][kBytes];
-    __shared__ QueryRows rows[4];
+    __shared__ QueryRows<BQ> rows[4];
     const int lane = threadIdx.x % kWave, h = lane >> 5, wave = threadIdx.x / kWave;
     const int past = x.TK - x.T, kv = x.H / x.group, chunks = x.far_chunks, parts = (x.sinks + 31) / 32;
     int64_t id = (int64_t)blockIdx.x * 4 + wave;
@@ -1030,19 +1138,18 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
     OwnRows<D, W, kWide> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
     k.signs(x.scale < 0.0f);
-    v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
+    if constexpr (kK) v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
     const int begin = max(max(i0, past), first + 32 * part + x.window);
-    const int end = first_start(x, n, max(i0, past), i1, first + 1, lane);
+    const int end = x.ends != nullptr ? min(i1, x.ends[n * x.TK + first]) : i1;
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
-    QueryStage<D, W, kWide, kWave> stage;
+    QueryStage<D, W, kWide, BQ, kWave> stage;
     for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head)
         for (int i = begin; i < end; i += BQ) {
             stage.fetch(x, n, head, i, end);
             stage.put(lds[wave][0], lds[wave][1], rows[wave]);
             __builtin_amdgcn_wave_barrier();
-            add_queries<D, W, kWide>(
-                x, lds[wave][0], lds[wave][1], rows[wave], k, v, false,
-                [&](int r, int) { return valid && i + r < end && j <= i + r - x.window; }, lane, dk, dv);
+            add_queries<D, W, kWide, kK, kV>(x, lds[wave][0], lds[wave][1], rows[wave], 0, k, v, false,
+                                             valid ? row_bits(j + x.window, end, i, h) : 0, lane, dk, dv);
             __builtin_amdgcn_wave_barrier();
         }
     if (s >= x.sinks) return;
@@ -1052,22 +1159,25 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
             const int at = 32 * dt + 8 * r4 + 4 * h;
-            *reinterpret_cast<f32x4*>(to + at) = f32x4{dk[dt][4 * r4], dk[dt][4 * r4 + 1], dk[dt][4 * r4 + 2], dk[dt][4 * r4 + 3]};
-            *reinterpret_cast<f32x4*>(to + W + at) = f32x4{dv[dt][4 * r4], dv[dt][4 * r4 + 1], dv[dt][4 * r4 + 2], dv[dt][4 * r4 + 3]};
+            if constexpr (kK) *reinterpret_cast<f32x4*>(to + at) = f32x4{dk[dt][4 * r4], dk[dt][4 * r4 + 1], dk[dt][4 * r4 + 2], dk[dt][4 * r4 + 3]};
+            if constexpr (kV) *reinterpret_cast<f32x4*>(to + W + at) = f32x4{dv[dt][4 * r4], dv[dt][4 * r4 + 1], dv[dt][4 * r4 + 2], dv[dt][4 * r4 + 3]};
         }
 }
 
-// The first step of each step's episode, [N, TK]: a running maximum of the steps
-// where the reset mask is set, one block to a row.
-static __global__ __launch_bounds__(256) void episode_starts(const SeqView reset, int64_t N, int32_t TK, int32_t* out)
+// The first step of each step's episode and the step behind its last, [N, TK]: a
+// running maximum of the steps where the reset mask is set, and a running minimum of
+// those from the end, one block to a row.
+template <bool kEnds>
+__device__ __forceinline__ void episode_bounds(const SeqView& reset, int64_t n, int32_t TK, int32_t* out, int* part)
 {
-    __shared__ int part[4];
-    const int64_t n = blockIdx.x;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     int carry = 0;
     for (int t0 = 0; t0 < TK; t0 += 256) {
-        const int t = t0 + threadIdx.x;
-        int v = t < TK && *seq_row<uint8_t>(reset, n, t, 0) != 0 ? t : 0;
+        // ends: from the last step backwards, by how far the next first step lies before TK
+        const int t = kEnds ? TK - 1 - t0 - (int)threadIdx.x : t0 + (int)threadIdx.x;
+        const int at = kEnds ? t + 1 : t;
+        int v = 0;
+        if (at >= 0 && at < TK && *seq_row<uint8_t>(reset, n, at, 0) != 0) v = kEnds ? TK - at : at;
         for (int o = 1; o < kWave; o <<= 1) {
             const int u = __shfl_up(v, o);
             if (lane >= o) v = max(v, u);
@@ -1077,9 +1187,18 @@ static __global__ __launch_bounds__(256) void episode_starts(const SeqView reset
         v = max(v, carry);
         for (int w = 0; w < wave; ++w) v = max(v, part[w]);
         for (int w = 0; w < 4; ++w) carry = max(carry, part[w]);
-        if (t < TK) out[n * TK + t] = v;
+        if (t >= 0 && t < TK) out[n * TK + t] = kEnds ? TK - v : v;
         __syncthreads();
     }
+}
+
+static __global__ __launch_bounds__(256) void episodes(const SeqView reset, int64_t N, int32_t TK, int32_t* starts,
+                                                       int32_t* ends)
+{
+    __shared__ int part[4];
+    const int64_t n = blockIdx.x % N;
+    if (blockIdx.x < N) episode_bounds<false>(reset, n, TK, starts, part);
+    else episode_bounds<true>(reset, n, TK, ends, part);
 }
 
 // ------------------------------------------------------------- single steps
@@ -1393,7 +1512,7 @@ inline void set_vec(SeqView& v, int64_t dim, int s)
 
 // Where the parts of a call's workspace lie, in bytes.
 struct AttWorkspace {
-    size_t delta, far_part, bytes;
+    size_t ends, delta, far_part, bytes;
     int32_t far_chunks;
 };
 
@@ -1403,8 +1522,10 @@ inline AttWorkspace att_workspace(int64_t N, int64_t T, int64_t TK, int64_t H, i
     auto whole = [](size_t b) { return (b + 255) / 256 * 256; };
     AttWorkspace w{};
     if (reset) w.bytes += whole((size_t)(N * TK) * 4);
-    w.delta = w.bytes;
+    w.ends = w.bytes;
     if (!backward) return w;
+    if (reset) w.bytes += whole((size_t)(N * TK) * 4);
+    w.delta = w.bytes;
     w.bytes += whole((size_t)(N * T * H) * 4);
     w.far_part = w.bytes;
     // a chunk after an episode's first has queries that see its first steps by these alone
@@ -1438,6 +1559,7 @@ inline void fill_attention(AttArgs& x, const AttWorkspace& w, int64_t N, int64_t
     x.hpb = x.group % 4 == 0 ? 4 : x.group % 2 == 0 ? 2 : 1;
     char* const at = static_cast<char*>(ws);
     x.starts = reset != nullptr ? reinterpret_cast<const int32_t*>(at) : nullptr;
+    x.ends = reset != nullptr && w.delta > 0 ? reinterpret_cast<const int32_t*>(at + w.ends) : nullptr;
     x.delta = reinterpret_cast<float*>(at + w.delta);
     x.far_chunks = w.far_chunks;
     x.far_part = w.far_chunks > 0 ? reinterpret_cast<float*>(at + w.far_part) : nullptr;
@@ -1446,8 +1568,8 @@ inline void fill_attention(AttArgs& x, const AttWorkspace& w, int64_t N, int64_t
 inline lrs_status launch_starts(const char* nm, const AttArgs& x, const SeqView& reset, hipStream_t stream)
 {
     if (x.starts == nullptr) return LRS_OK;
-    return launch_seq(nm, episode_starts, (uint64_t)x.N, 256, stream, reset, x.N, x.TK,
-                      const_cast<int32_t*>(x.starts));
+    return launch_seq(nm, episodes, (uint64_t)x.N * (x.ends != nullptr ? 2 : 1), 256, stream, reset, x.N, x.TK,
+                      const_cast<int32_t*>(x.starts), const_cast<int32_t*>(x.ends));
 }
 
 constexpr uint64_t kMaxGrid = 0x7fffffffull;
@@ -1474,18 +1596,29 @@ inline bool all_wide(std::initializer_list<const SeqView*> views, int64_t dk, in
     return wide;
 }
 
+template <class D, int W, bool kWide, bool kK, bool kV>
+lrs_status launch_dkv(const char* nm, AttArgs x, hipStream_t stream)
+{
+    if (x.far_part != nullptr) {
+        const int64_t waves = x.N * (x.H / x.group) * x.far_chunks * ((x.sinks + 31) / 32);
+        LRS_TRY(launch_seq(nm, attend_far<D, W, kWide, kK, kV>, (uint64_t)((waves + 3) / 4), 256, stream, x));
+    }
+    const uint64_t blocks = key_blocks(x);
+    return launch_seq(nm, attend_dkv<D, W, kWide, kK, kV>, blocks, 256, stream, x);
+}
+
 template <class D, int W, bool kWide>
 lrs_status launch_backward(const char* nm, AttArgs x, hipStream_t stream)
 {
-    uint64_t blocks = query_blocks(x);
+    const uint64_t blocks = query_blocks(x);
     if (x.sum_delta) LRS_TRY(launch_seq(nm, attend_dq<D, W, kWide, true>, blocks, 256, stream, x));
     LRS_TRY(launch_seq(nm, attend_dq<D, W, kWide, false>, blocks, 256, stream, x));
-    if (x.far_part != nullptr) {
-        const int64_t waves = x.N * (x.H / x.group) * x.far_chunks * ((x.sinks + 31) / 32);
-        LRS_TRY(launch_seq(nm, attend_far<D, W, kWide>, (uint64_t)((waves + 3) / 4), 256, stream, x));
+    if constexpr (kSplitGrads<D, W>) {
+        LRS_TRY((launch_dkv<D, W, kWide, true, false>(nm, x, stream)));
+        return launch_dkv<D, W, kWide, false, true>(nm, x, stream);
+    } else {
+        return launch_dkv<D, W, kWide, true, true>(nm, x, stream);
     }
-    blocks = key_blocks(x);
-    return launch_seq(nm, attend_dkv<D, W, kWide>, blocks, 256, stream, x);
 }
 
 template <class D>
@@ -1519,7 +1652,7 @@ lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int
     set_vec(x.v, dv, s);
     set_vec(x.o, dv, s);
     const uint64_t blocks = query_blocks(x);
-    LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N <= kMaxGrid, "%s: num_envs * heads * steps is too large", nm);
+    LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N <= kMaxGrid / 2, "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[3], stream));
     const bool narrow = std::max(dk, dv) <= 64, wide = all_wide({&x.q, &x.k, &x.v, &x.o}, dk, dv);
     return launch_seq(nm, wide ? (narrow ? attend_forward<D, 64, true> : attend_forward<D, 128, true>)
@@ -1564,7 +1697,7 @@ lrs_status attention_backward_entry(const char* nm, int64_t N, int64_t T, int64_
     x.dv = a[9];
     for (SeqView* w : {&x.q, &x.k, &x.dq, &x.dk}) set_vec(*w, dk, s);
     for (SeqView* w : {&x.v, &x.o, &x.dout, &x.dv}) set_vec(*w, dv, s);
-    LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && (uint64_t)N <= kMaxGrid,
+    LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && (uint64_t)N <= kMaxGrid / 2,
                 "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[4], stream));
     const bool wide = all_wide({&x.q, &x.k, &x.v, &x.o, &x.dout, &x.dq, &x.dk, &x.dv}, dk, dv);
