@@ -26,21 +26,6 @@
 
 #include "sequence.hpp"
 
-#ifndef LRS_ORDER
-#define LRS_ORDER 0
-#endif
-#if LRS_ORDER
-#define LRS_KEEP_ORDER() __builtin_amdgcn_sched_barrier(0)
-#else
-#define LRS_KEEP_ORDER()
-#endif
-
-#ifdef LRS_PRIO
-#define LRS_SETPRIO(v) __builtin_amdgcn_s_setprio(v)
-#else
-#define LRS_SETPRIO(v)
-#endif
-
 namespace lrs {
 
 constexpr int kMaxAttDim = 128;
@@ -94,7 +79,7 @@ __device__ __forceinline__ f32x16 mma32(const AFrag<D>& a, const AFrag<D>& b, f3
 }
 
 // The row that register r of a product holds for a lane of half h.
-__device__ __forceinline__ int acc_row(int r, int h) { return 8 * (r / 4) + 4 * h + r % 4; }
+__device__ __forceinline__ constexpr int acc_row(int r, int h) { return 8 * (r / 4) + 4 * h + r % 4; }
 
 // Registers 8u .. 8u + 7 as an operand: 16-bit types round the weights here, once
 // (to 2^-9 or 2^-12 of each; they are summed in float32 before that).
@@ -129,8 +114,23 @@ __device__ __forceinline__ AFrag<D> operand_rest(const f32x16& v, int u, const A
 }
 
 // ------------------------------------------------------------- tiles in LDS
+typedef __attribute__((address_space(3))) char* lds_t;
+
+__device__ __forceinline__ uint32_t lds_address(void* p) { return (uint32_t)(uintptr_t)(lds_t)p; }
+template <class T>
+__device__ __forceinline__ T lds_load(uint32_t at)
+{
+    return *(const __attribute__((address_space(3))) T*)(lds_t)(uintptr_t)at;
+}
+__device__ __forceinline__ void lds_store(uint32_t at, const u32x4& v)
+{
+    *(__attribute__((address_space(3))) u32x4*)(lds_t)(uintptr_t)at = v;
+}
+
 // Rows of W elements without padding; 16-byte chunk c of row r lies at c ^ turn(r)
 // so that 16 rows at one chunk, and the reads by columns, spread over all banks.
+// turn() repeats every 16 rows, so a lane's address for one kind of read is one
+// number for the tile, turned over in some bits and moved by a constant.
 template <class D, int W>
 struct AttTile {
     static constexpr int kRow = W * (int)sizeof(D);
@@ -140,46 +140,49 @@ struct AttTile {
         else if constexpr (W == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
         else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
     }
-    static __device__ __forceinline__ int at(int r, int chunk) { return r * kRow + ((chunk ^ turn(r)) << 4); }
-
-    // Elements 8 c8 .. of row r.
-    static __device__ __forceinline__ void put(char* tile, int r, int c8, const Raw8<D>& v)
+    static __device__ __forceinline__ uint32_t at(int r, int chunk)
     {
-        constexpr int n = (int)sizeof(D) / 2;
-#pragma unroll
-        for (int k = 0; k < n; ++k) *reinterpret_cast<u32x4*>(tile + at(r, n * c8 + k)) = v.w[k];
+        return (uint32_t)(r * kRow + ((chunk ^ turn(r)) << 4));
     }
-    // Rows row + lane % 32, elements 16 ks + 8 (lane / 32) + 0..7.
-    static __device__ __forceinline__ AFrag<D> rows(const char* tile, int row, int ks, int lane)
+
+    // Rows row + lane % 32, elements 16 ks + 8 (lane / 32) + 0..7; `mine` from row_lane().
+    static __device__ __forceinline__ uint32_t row_lane(int lane)
     {
-        constexpr int n = (int)sizeof(D) / 2;
+        return at(lane & 31, (int)sizeof(D) / 2 * (lane >> 5));
+    }
+    static __device__ __forceinline__ AFrag<D> rows(uint32_t mine, int row, int ks)
+    {
         AFrag<D> f;
 #pragma unroll
-        for (int k = 0; k < n; ++k)
-            f.w[k] = *reinterpret_cast<const u32x4*>(
-                tile + at(row + (lane & 31), n * (2 * ks + (lane >> 5)) + k));
+        for (int k = 0; k < (int)sizeof(D) / 2; ++k)
+            f.w[k] = lds_load<u32x4>((mine ^ (uint32_t)(ks * 16 * (int)sizeof(D) + k * 16)) + row * kRow);
         return f;
     }
-    // Column col + lane % 32 of rows row + 8 (e / 4) + 4 (lane / 32) + e % 4, e = 0..7.
-    // A transposing read hands the 16 lanes of a group four rows of four groups of 4
-    // columns, 8 bytes read by each lane.
-    static __device__ __forceinline__ AFrag<D> columns(const char* tile, int row, int col, int lane)
+    // Column col + lane % 32 of rows row + 8 (e / 4) + 4 (lane / 32) + e % 4, e = 0..7
+    // (row a multiple of 16, col of 32); `mine` from column_lane().  A transposing read
+    // hands the 16 lanes of a group four rows of four groups of 4 columns, 8 bytes read
+    // by each lane.
+    static __device__ __forceinline__ uint32_t column_lane(int lane)
+    {
+        const int h = lane >> 5;
+        if constexpr (sizeof(D) == 4) return at(4 * h, (lane & 31) / 4) + 4 * (lane & 3);
+        const int c = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+        return at(4 * h + ((lane & 15) >> 2), c / 8) + 2 * (c % 8);
+    }
+    static __device__ __forceinline__ AFrag<D> columns(uint32_t mine, int row, int col)
     {
         AFrag<D> f;
-        const int h = lane >> 5;
         if constexpr (sizeof(D) == 4) {
-            const int c = col + (lane & 31);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                f.w[e / 4][e % 4] = *reinterpret_cast<const uint32_t*>(
-                    tile + at(row + 8 * (e / 4) + 4 * h + e % 4, c / 4) + 4 * (c % 4));
+                f.w[e / 4][e % 4] = lds_load<uint32_t>((mine ^ (uint32_t)(col * 4 | (e / 4) << 6 | (e % 4) << 4)) +
+                                                       (row + 8 * (e / 4) + e % 4) * kRow);
         } else {
-            typedef __attribute__((address_space(3))) as16x4* lds_ptr;
-            const int r = row + 4 * h + ((lane & 15) >> 2);
-            const int c = col + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-            const as16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at(r, c / 8) + 2 * (c % 8)));
-            const as16x4 hi =
-                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at(r + 8, c / 8) + 2 * (c % 8)));
+            typedef __attribute__((address_space(3))) as16x4* four;
+            const uint32_t a = (mine ^ (uint32_t)(col * 2)) + row * kRow;
+            const uint32_t b = (mine ^ (uint32_t)(col * 2 | 32)) + (row + 8) * kRow;
+            const as16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((four)(uintptr_t)a);
+            const as16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((four)(uintptr_t)b);
             typedef short s16x8 __attribute__((ext_vector_type(8)));
             f.w[0] = __builtin_bit_cast(u32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
@@ -188,43 +191,66 @@ struct AttTile {
 };
 
 // Rows of memory on their way into a tile of kRows rows, by a block of 256 threads
-// or by a wave.  kWide: rows are whole 16-byte units, and loads go out without a branch
-// between them, or each would be waited for where the branches meet.  What lies
-// beyond the last row or the dimension is then read from within them: it meets
-// weights of 0, or zeros of the other operand.  Otherwise it becomes zeros.
+// or by a wave.  What lies beyond the last row or the dimension becomes zeros.
+// kWide: rows are whole 16-byte units, loaded through a buffer descriptor whose
+// bounds make the zeros: one offset per lane, and no branch between the loads (where
+// branches meet each load would be waited for).
 template <class D, int W, int kRows, bool kWide, int kThreads = 256>
 struct AttStage {
     static constexpr int kUnits = kRows * (W / 8) / kThreads, kApart = kThreads / (W / 8);
+    static_assert(kApart % 16 == 0 || kThreads < 256, "rows of a thread's units lie alike");
     Raw8<D> r[kUnits];
+    uint32_t off;  // kWide: of this thread's first unit, in bytes
 
+    static __device__ __forceinline__ int row() { return (int)(threadIdx.x % kThreads) / (W / 8); }
+    static __device__ __forceinline__ int column() { return (int)(threadIdx.x % kThreads) % (W / 8) * 8; }
+
+    __device__ __forceinline__ void start(const SeqView& v, int dim)
+    {
+        // beyond every bound where the tile is wider than the rows
+        off = column() < dim ? ((uint32_t)row() * (uint32_t)v.step + column()) * (uint32_t)sizeof(D) : 0x7ffffff0u;
+    }
     __device__ __forceinline__ void fetch(const SeqView& v, int64_t n, int h, int64_t t0, int count, int dim)
     {
-        const int me = threadIdx.x % kThreads, row = me / (W / 8), c = me % (W / 8) * 8;
         const D* const from = seq_row<D>(v, n, t0, h);
         if constexpr (kWide) {
-            const uint32_t col = c < dim ? c : 0;
+            const int step = (int)v.step * (int)sizeof(D);
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
-                const uint32_t at = (uint32_t)min(row + u * kApart, count - 1) * (uint32_t)v.step + col;
+                const int left = count - u * kApart;  // rows from this unit's first on
+                const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
+                    (void*)(reinterpret_cast<const char*>(from) + (int64_t)u * kApart * step), (short)0,
+                    left > 0 ? (left - 1) * step + dim * (int)sizeof(D) : 0, 0x00020000);
 #pragma unroll
                 for (int k = 0; k < (int)sizeof(D) / 2; ++k)
-                    r[u].w[k] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(from) +
-                                                                (at * (uint32_t)sizeof(D) + 16u * k));
+                    r[u].w[k] = __builtin_amdgcn_raw_buffer_load_b128(rows, off + 16u * k, 0, 0);
             }
         } else {
+            const int c = column();
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
-                const int at = row + u * kApart;
+                const int at = row() + u * kApart;
                 r[u] = Raw8<D>{};
                 if (at < count && c < dim) r[u] = load8<D>(from + (int64_t)at * v.step, c, dim, v.vec);
             }
         }
     }
-    __device__ __forceinline__ void put(char* tile) const
+    // Where put() puts this thread's first unit of a tile at `tile`.
+    static __device__ __forceinline__ uint32_t lane(uint32_t tile)
     {
-        const int me = threadIdx.x % kThreads, row = me / (W / 8), c8 = me % (W / 8);
+        return tile + AttTile<D, W>::at(row(), (int)sizeof(D) / 2 * (column() / 8));
+    }
+    __device__ __forceinline__ void put(uint32_t mine) const
+    {
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) AttTile<D, W>::put(tile, row + u * kApart, c8, r[u]);
+        for (int u = 0; u < kUnits; ++u) {
+            // a wave's units lie fewer than 16 rows apart, each with a turn of its own
+            const uint32_t at = kApart % 16 == 0
+                ? mine + u * kApart * AttTile<D, W>::kRow
+                : mine - lane(0) + AttTile<D, W>::at(row() + u * kApart, (int)sizeof(D) / 2 * (column() / 8));
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(D) / 2; ++k) lds_store(at ^ (16u * k), r[u].w[k]);
+        }
     }
 };
 
@@ -266,10 +292,24 @@ __device__ __forceinline__ uint32_t row_bits(int begin, int end, int j0, int h)
     return (uint32_t)bits >> (4 * h);
 }
 // v where the bit of register r is set, else `other`: two instructions, and no compare.
-__device__ __forceinline__ float where_bit(uint32_t bits, int r, float v, float other)
+template <int r>
+__device__ __forceinline__ float where_bit(uint32_t bits, float v, float other)
 {
-    const uint32_t all = (uint32_t)__builtin_amdgcn_sbfe((int)bits, acc_row(r, 0), 1);
+    // (as an instruction: the compiler would make a test and a select of it)
+    uint32_t all;
+    asm("v_bfe_i32 %0, %1, %2, 1" : "=v"(all) : "v"(bits), "n"(acc_row(r, 0)));
     return __uint_as_float((all & __float_as_uint(v)) | (~all & __float_as_uint(other)));
+}
+
+template <int... r>
+__device__ __forceinline__ void keep_bits(uint32_t bits, f32x16& v, float other, std::integer_sequence<int, r...>)
+{
+    ((v[r] = where_bit<r>(bits, v[r], other)), ...);
+}
+// The rows whose bits are set, `other` in the rest.
+__device__ __forceinline__ void keep_bits(uint32_t bits, f32x16& v, float other)
+{
+    keep_bits(bits, v, other, std::make_integer_sequence<int, 16>());
 }
 
 // What a block's queries see: tiles of kTile keys, the far range's first.
@@ -535,36 +575,16 @@ __device__ __forceinline__ float own_dot(const SeqView& v, int64_t n, int64_t t,
 }
 
 // The products of 32 rows of tile `ta` (and of `tb`) with the wave's own rows, over
-// all W elements.  Fragments of LDS are read ahead of the products in groups: left
-// to itself the compiler reads one, waits for it, and multiplies.
+// all W elements.
 template <class D, int W, bool kTwo, bool kWide>
-__device__ __forceinline__ void row_products(const char* ta, const OwnRows<D, W, kWide>& a, const char* tb,
-                                             const OwnRows<D, W, kWide>& b, int row, int lane, f32x16& s, f32x16& t)
+__device__ __forceinline__ void row_products(uint32_t ta, const OwnRows<D, W, kWide>& a, uint32_t tb,
+                                             const OwnRows<D, W, kWide>& b, int row, f32x16& s, f32x16& t)
 {
     using Tile = AttTile<D, W>;
-    #ifndef LRS_G
-#define LRS_G 2
-#endif
-    constexpr int G = sizeof(D) == 4 ? 1 : LRS_G, N = W / 16 / G;
-    AFrag<D> fa[2][G], fb[2][G];
-    auto load = [&](int g) {
 #pragma unroll
-        for (int e = 0; e < G; ++e) {
-            fa[g & 1][e] = Tile::rows(ta, row, g * G + e, lane);
-            if constexpr (kTwo) fb[g & 1][e] = Tile::rows(tb, row, g * G + e, lane);
-        }
-    };
-    load(0);
-#pragma unroll
-    for (int g = 0; g < N; ++g) {
-        LRS_KEEP_ORDER();
-        if (g + 1 < N) load(g + 1);
-        LRS_KEEP_ORDER();
-#pragma unroll
-        for (int e = 0; e < G; ++e) {
-            s = mma32<D>(fa[g & 1][e], a.f[g * G + e], s);
-            if constexpr (kTwo) t = mma32<D>(fb[g & 1][e], b.f[g * G + e], t);
-        }
+    for (int ks = 0; ks < W / 16; ++ks) {
+        s = mma32<D>(Tile::rows(ta, row, ks), a.f[ks], s);
+        if constexpr (kTwo) t = mma32<D>(Tile::rows(tb, row, ks), b.f[ks], t);
     }
 }
 
@@ -638,7 +658,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
 {
     using Tile = AttTile<D, W>;
     constexpr int BK = kKeyTile<D, W>, kBytes = BK * Tile::kRow, S = BK / 32;
-    __shared__ alignas(16) char lds[2][2][kBytes];
+    __shared__ alignas(1024) char lds[2][2][kBytes];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
     const AttBlock b(x);
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
@@ -648,40 +668,41 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
     q.signs(x.scale < 0.0f);
 
     AttStage<D, W, BK, kWide> sk, sv;
+    sk.start(x.k, x.dim_k);
+    sv.start(x.v, x.dim_v);
     auto fetch = [&](int it) {
         int j0, j1;
         kt.get(it, BK, j0, j1);
         sk.fetch(x.k, b.n, b.kvh, j0, j1 - j0, x.dim_k);
         sv.fetch(x.v, b.n, b.kvh, j0, j1 - j0, x.dim_v);
     };
+    // the lane's places in the tiles of the first buffer, moved to the other and back
+    uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
+    uint32_t put_at = sk.lane(lds_address(lds));
+    auto put = [&]() {
+        sk.put(put_at);
+        sv.put(put_at + kBytes);
+    };
     fetch(0);
-    sk.put(lds[0][0]);
-    sv.put(lds[0][1]);
+    put();
     if (kt.tiles > 1) fetch(1);
 
     f32x16 o[W / 32] = {};
     float m = -INFINITY, l = 0.0f;  // m: the largest score; l: this half's sum
     for (int it = 0; it < kt.tiles; ++it) {
         __syncthreads();
-        const char *const tk = lds[it & 1][0], *const tv = lds[it & 1][1];
         int j0, j1;
         kt.get(it, BK, j0, j1);
         const bool is_far = it < kt.far_tiles;
         if (wq.touches(kt, is_far, j0, j1)) {
             f32x16 s[S] = {};
-            LRS_SETPRIO(1);
 #pragma unroll
             for (int ks = 0; ks < W / 16; ++ks)
 #pragma unroll
-                for (int a = 0; a < S; ++a) s[a] = mma32<D>(Tile::rows(tk, 32 * a, ks, lane), q.f[ks], s[a]);
-            LRS_SETPRIO(0);
+                for (int a = 0; a < S; ++a) s[a] = mma32<D>(Tile::rows(by_row, 32 * a, ks), q.f[ks], s[a]);
             if (!wq.whole(is_far, j0, j1, BK)) {
 #pragma unroll
-                for (int a = 0; a < S; ++a) {
-                    const uint32_t bits = wq.bits(is_far, j0 + 32 * a, j1, h);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[a][r] = where_bit(bits, r, s[a][r], -INFINITY);
-                }
+                for (int a = 0; a < S; ++a) keep_bits(wq.bits(is_far, j0 + 32 * a, j1, h), s[a], -INFINITY);
             }
             float top = s[0][0];
 #pragma unroll
@@ -715,12 +736,15 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
                     const AFrag<D> p = operand<D>(s[a], u);
 #pragma unroll
                     for (int dt = 0; dt < W / 32; ++dt)
-                        o[dt] = mma32<D>(Tile::columns(tv, 32 * a + 16 * u, 32 * dt, lane), p, o[dt]);
+                        o[dt] = mma32<D>(Tile::columns(by_col + kBytes, 32 * a + 16 * u, 32 * dt), p, o[dt]);
                 }
         }
+        const uint32_t move = it & 1 ? -2 * kBytes : 2 * kBytes;
+        by_row += move;
+        by_col += move;
+        put_at += move;
         if (it + 1 < kt.tiles) {
-            sk.put(lds[(it + 1) & 1][0]);
-            sv.put(lds[(it + 1) & 1][1]);
+            put();
             if (it + 2 < kt.tiles) fetch(it + 2);
         }
     }
@@ -744,7 +768,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
 {
     using Tile = AttTile<D, W>;
     constexpr int BK = kGradTile<D, W>, kBytes = BK * Tile::kRow;
-    __shared__ alignas(16) char lds[2][2][kBytes];
+    __shared__ alignas(1024) char lds[2][2][kBytes];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
     const AttBlock b(x);
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
@@ -765,22 +789,29 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
     }
 
     AttStage<D, W, BK, kWide> sk, sv;
+    sk.start(x.k, x.dim_k);
+    sv.start(x.v, x.dim_v);
     auto fetch = [&](int it) {
         int j0, j1;
         kt.get(it, BK, j0, j1);
         sk.fetch(x.k, b.n, b.kvh, j0, j1 - j0, x.dim_k);
         sv.fetch(x.v, b.n, b.kvh, j0, j1 - j0, x.dim_v);
     };
+    // the lane's places in the tiles of the first buffer, moved to the other and back
+    uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
+    uint32_t put_at = sk.lane(lds_address(lds));
+    auto put = [&]() {
+        sk.put(put_at);
+        sv.put(put_at + kBytes);
+    };
     fetch(0);
-    sk.put(lds[0][0]);
-    sv.put(lds[0][1]);
+    put();
     if (kt.tiles > 1) fetch(1);
 
     f32x16 dq[W / 32] = {};
     float sum = 0.0f;
     for (int it = 0; it < kt.tiles; ++it) {
         __syncthreads();
-        const char *const tk = lds[it & 1][0], *const tv = lds[it & 1][1];
         int j0, j1;
         kt.get(it, BK, j0, j1);
         const bool is_far = it < kt.far_tiles;
@@ -789,47 +820,36 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
             const int ja = j0 + at, jb = min(ja + 32, j1);
             if (ja >= j1 || !wq.touches(kt, is_far, ja, jb)) continue;
             f32x16 s = {}, dp = {};
-            row_products<D, W, true>(tk, q, tv, d_o, at, lane, s, dp);
+            row_products<D, W, true>(by_row, q, by_row + kBytes, d_o, at, s, dp);
             constexpr int N = W / 32;
-            AFrag<D> ck[2][N];
-            auto load = [&](int u) {
-#pragma unroll
-                for (int dt = 0; dt < N; ++dt) ck[u][dt] = Tile::columns(tk, at + 16 * u, 32 * dt, lane);
-            };
-            LRS_KEEP_ORDER();
-            if constexpr (!kSum) load(0);
-            LRS_KEEP_ORDER();
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], x.c, -lse2)) * (dp[r] - delta);
-            if (!wq.whole(is_far, ja, jb, 32)) {
-                const uint32_t bits = wq.bits(is_far, ja, j1, h);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) dp[r] = where_bit(bits, r, dp[r], 0.0f);
-            }
+            if (!wq.whole(is_far, ja, jb, 32)) keep_bits(wq.bits(is_far, ja, j1, h), dp, 0.0f);
             if constexpr (kSum) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) sum += dp[r];
             } else {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    LRS_KEEP_ORDER();
-                    if (u == 0) load(1);
-                    LRS_KEEP_ORDER();
                     const AFrag<D> ds = operand<D>(dp, u);
+                    AFrag<D> rest;
+                    if constexpr (sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
 #pragma unroll
-                    for (int dt = 0; dt < N; ++dt) dq[dt] = mma32<D>(ck[u][dt], ds, dq[dt]);
-                    if constexpr (sizeof(D) == 2) {
-                        const AFrag<D> rest = operand_rest<D>(dp, u, ds);
-#pragma unroll
-                        for (int dt = 0; dt < N; ++dt) dq[dt] = mma32<D>(ck[u][dt], rest, dq[dt]);
+                    for (int dt = 0; dt < N; ++dt) {
+                        const AFrag<D> k = Tile::columns(by_col, at + 16 * u, 32 * dt);
+                        dq[dt] = mma32<D>(k, ds, dq[dt]);
+                        if constexpr (sizeof(D) == 2) dq[dt] = mma32<D>(k, rest, dq[dt]);
                     }
                 }
             }
         }
+        const uint32_t move = it & 1 ? -2 * kBytes : 2 * kBytes;
+        by_row += move;
+        by_col += move;
+        put_at += move;
         if (it + 1 < kt.tiles) {
-            sk.put(lds[(it + 1) & 1][0]);
-            sv.put(lds[(it + 1) & 1][1]);
+            put();
             if (it + 2 < kt.tiles) fetch(it + 2);
         }
     }
@@ -870,6 +890,11 @@ struct QueryStage {
     float lse, delta;
     bool in;
 
+    __device__ __forceinline__ void begin(const AttArgs& x)
+    {
+        q.start(x.q, x.dim_k);
+        d_o.start(x.dout, x.dim_v);
+    }
     __device__ __forceinline__ void fetch(const AttArgs& x, int64_t n, int head, int i, int end)
     {
         const int past = x.TK - x.T, count = min(kRows, end - i);
@@ -881,10 +906,11 @@ struct QueryStage {
         lse = *seq_row<float>(x.lse, n, at - past, head);
         delta = x.delta[(n * x.H + head) * x.T + at - past];
     }
-    __device__ __forceinline__ void put(char* tq, char* to, QueryRows<kRows>& rows) const
+    // at: from q.lane(); the gradients' tile lies `apart` behind the queries'.
+    __device__ __forceinline__ void put(uint32_t at, int apart, QueryRows<kRows>& rows) const
     {
-        q.put(tq);
-        d_o.put(to);
+        q.put(at);
+        d_o.put(at + apart);
         if (threadIdx.x % kThreads < kRows) {
             const int a = threadIdx.x % kRows;
             // queries behind the end have no weights
@@ -898,7 +924,7 @@ struct QueryStage {
 // (kK), of the values (kV).  bits: the rows whose queries see the lane's key; not
 // looked at where `whole`.
 template <class D, int W, bool kWide, bool kK, bool kV, class Rows>
-__device__ __forceinline__ void add_queries(const AttArgs& x, const char* tq, const char* to, const Rows& row, int at,
+__device__ __forceinline__ void add_queries(const AttArgs& x, uint32_t by_row, uint32_t by_col, int apart, const Rows& row, int at,
                                             const OwnRows<D, W, kWide>& k, const OwnRows<D, W, kWide>& v, bool whole,
                                             uint32_t bits, int lane, f32x16 (&dk)[W / 32], f32x16 (&dv)[W / 32])
 {
@@ -907,18 +933,7 @@ __device__ __forceinline__ void add_queries(const AttArgs& x, const char* tq, co
     constexpr int N = W / 32;
     const int h = lane >> 5;
     f32x16 s = {}, dp = {};
-    row_products<D, W, kK>(tq, k, to, v, at, lane, s, dp);
-    LRS_KEEP_ORDER();
-    AFrag<D> cq[2][N], co[2][N];
-    auto load = [&](int u) {
-#pragma unroll
-        for (int dt = 0; dt < N; ++dt) {
-            if constexpr (kV) co[u][dt] = Tile::columns(to, at + 16 * u, 32 * dt, lane);
-            if constexpr (kK) cq[u][dt] = Tile::columns(tq, at + 16 * u, 32 * dt, lane);
-        }
-    };
-    load(0);
-    LRS_KEEP_ORDER();
+    row_products<D, W, kK>(by_row, k, by_row + apart, v, at, s, dp);
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
         const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&row.lse2[at + 8 * r4 + 4 * h]);
@@ -931,30 +946,22 @@ __device__ __forceinline__ void add_queries(const AttArgs& x, const char* tq, co
         }
     }
     if (!whole) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            s[r] = where_bit(bits, r, s[r], 0.0f);
-            if constexpr (kK) dp[r] = where_bit(bits, r, dp[r], 0.0f);
-        }
+        if constexpr (kV) keep_bits(bits, s, 0.0f);
+        if constexpr (kK) keep_bits(bits, dp, 0.0f);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        LRS_KEEP_ORDER();
-        if (u == 0) load(1);
-        LRS_KEEP_ORDER();
-        if constexpr (kV) {
-            const AFrag<D> p = operand<D>(s, u);
+        AFrag<D> p, ds, rest;
+        if constexpr (kV) p = operand<D>(s, u);
+        if constexpr (kK) ds = operand<D>(dp, u);
+        if constexpr (kK && sizeof(D) == 2) rest = operand_rest<D>(dp, u, ds);
 #pragma unroll
-            for (int dt = 0; dt < N; ++dt) dv[dt] = mma32<D>(co[u][dt], p, dv[dt]);
-        }
-        if constexpr (kK) {
-            const AFrag<D> ds = operand<D>(dp, u);
-#pragma unroll
-            for (int dt = 0; dt < N; ++dt) dk[dt] = mma32<D>(cq[u][dt], ds, dk[dt]);
-            if constexpr (sizeof(D) == 2) {
-                const AFrag<D> rest = operand_rest<D>(dp, u, ds);
-#pragma unroll
-                for (int dt = 0; dt < N; ++dt) dk[dt] = mma32<D>(cq[u][dt], rest, dk[dt]);
+        for (int dt = 0; dt < N; ++dt) {
+            if constexpr (kV) dv[dt] = mma32<D>(Tile::columns(by_col + apart, at + 16 * u, 32 * dt), p, dv[dt]);
+            if constexpr (kK) {
+                const AFrag<D> q = Tile::columns(by_col, at + 16 * u, 32 * dt);
+                dk[dt] = mma32<D>(q, ds, dk[dt]);
+                if constexpr (sizeof(D) == 2) dk[dt] = mma32<D>(q, rest, dk[dt]);
             }
         }
     }
@@ -983,7 +990,7 @@ template <class D, int W>
 #ifndef LRS_BQ
 #define LRS_BQ 32
 #endif
-constexpr int kQueryTile = W == 128 ? LRS_BQ : 64;
+constexpr int kQueryTile = W == 128 ? (sizeof(D) == 4 ? 32 : LRS_BQ) : 64;
 
 template <class D, int W>
 constexpr bool kSplitGrads = W * (int)sizeof(D) > 128;
@@ -1004,7 +1011,8 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
 {
     using Tile = AttTile<D, W>;
     constexpr int BQ = kQueryTile<D, W>;
-    __shared__ alignas(16) char lds[2][2][BQ * Tile::kRow];
+    constexpr int kBytes = BQ * Tile::kRow;
+    __shared__ alignas(1024) char lds[2][2][kBytes];
     __shared__ QueryRows<BQ> rows[2];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -1039,6 +1047,9 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
     const int tiles = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = tiles * x.group;
     if (total > 0) {
         QueryStage<D, W, kWide, BQ, 256> stage;
+        stage.begin(x);
+        uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
+        uint32_t put_at = stage.q.lane(lds_address(lds));
         int head = kvh * x.group, tile = 0, next_head = head, next = 0;
         auto fetch = [&]() {
             stage.fetch(x, n, next_head, begin + next * BQ, end);
@@ -1048,7 +1059,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
             }
         };
         fetch();
-        stage.put(lds[0][0], lds[0][1], rows[0]);
+        stage.put(put_at, kBytes, rows[0]);
         if (total > 1) fetch();
         for (int it = 0; it < total; ++it) {
             __syncthreads();
@@ -1059,7 +1070,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
                 if (i < most && mine0 <= i + 31) {
                     // whole: every query of the tile sees every key of the wave
                     const bool whole = mine0 + 31 <= i && i + 32 <= least;
-                    add_queries<D, W, kWide, kK, kV>(x, lds[it & 1][0], lds[it & 1][1], row, at, k, v, whole,
+                    add_queries<D, W, kWide, kK, kV>(x, by_row, by_col, kBytes, row, at, k, v, whole,
                                                      whole ? 0 : row_bits(j, until, i, h), lane, dk, dv);
                 }
             }
@@ -1067,8 +1078,12 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
                 tile = 0;
                 ++head;
             }
+            const uint32_t move = it & 1 ? -2 * kBytes : 2 * kBytes;
+            by_row += move;
+            by_col += move;
+            put_at += move;
             if (it + 1 < total) {
-                stage.put(lds[(it + 1) & 1][0], lds[(it + 1) & 1][1], rows[(it + 1) & 1]);
+                stage.put(put_at, kBytes, rows[(it + 1) & 1]);
                 if (it + 2 < total) fetch();
             }
         }
@@ -1116,9 +1131,10 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
     constexpr int BQ = 32, kBytes = BQ * Tile::kRow;
-    __shared__ alignas(16) char lds[4][2][kBytes];
+    __shared__ alignas(1024) char lds[4][2][kBytes];
     __shared__ QueryRows<BQ> rows[4];
-    const int lane = threadIdx.x % kWave, h = lane >> 5, wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int past = x.TK - x.T, kv = x.H / x.group, chunks = x.far_chunks, parts = (x.sinks + 31) / 32;
     int64_t id = (int64_t)blockIdx.x * 4 + wave;
     const int part = id % parts;
@@ -1143,12 +1159,15 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
     const int end = x.ends != nullptr ? min(i1, x.ends[n * x.TK + first]) : i1;
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
     QueryStage<D, W, kWide, BQ, kWave> stage;
+    stage.begin(x);
+    const uint32_t mine = lds_address(lds[wave]), by_row = mine + Tile::row_lane(lane);
+    const uint32_t by_col = mine + Tile::column_lane(lane), put_at = stage.q.lane(mine);
     for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head)
         for (int i = begin; i < end; i += BQ) {
             stage.fetch(x, n, head, i, end);
-            stage.put(lds[wave][0], lds[wave][1], rows[wave]);
+            stage.put(put_at, kBytes, rows[wave]);
             __builtin_amdgcn_wave_barrier();
-            add_queries<D, W, kWide, kK, kV>(x, lds[wave][0], lds[wave][1], rows[wave], 0, k, v, false,
+            add_queries<D, W, kWide, kK, kV>(x, by_row, by_col, kBytes, rows[wave], 0, k, v, false,
                                              valid ? row_bits(j + x.window, end, i, h) : 0, lane, dk, dv);
             __builtin_amdgcn_wave_barrier();
         }
