@@ -190,50 +190,70 @@ struct AttTile {
     }
 };
 
+// The row of a head at a step (heads are not shared within an array here).
+template <class D>
+__device__ __forceinline__ const char* att_row(const SeqView& v, int64_t n, int64_t t, int64_t h)
+{
+    return static_cast<const char*>(v.p) + (n * v.env + t * v.step + h * v.head) * (int64_t)sizeof(D);
+}
+
+// Loads through a buffer descriptor: what lies at or behind `bytes` becomes zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const char* p, int bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, bytes, 0x00020000);
+}
+
 // Rows of memory on their way into a tile of kRows rows, by a block of 256 threads
 // or by a wave.  What lies beyond the last row or the dimension becomes zeros.
 // kWide: rows are whole 16-byte units, loaded through a buffer descriptor whose
 // bounds make the zeros: one offset per lane, and no branch between the loads (where
-// branches meet each load would be waited for).
+// branches meet each load would be waited for).  place() says where the next tile
+// begins, and after fetch() the one behind it is next.
 template <class D, int W, int kRows, bool kWide, int kThreads = 256>
 struct AttStage {
     static constexpr int kUnits = kRows * (W / 8) / kThreads, kApart = kThreads / (W / 8);
     static_assert(kApart % 16 == 0 || kThreads < 256, "rows of a thread's units lie alike");
     Raw8<D> r[kUnits];
-    uint32_t off;  // kWide: of this thread's first unit, in bytes
+    const char* p;
+    int64_t step;      // bytes
+    uint32_t off;      // kWide: of this thread's first unit
+    int dim, vec;
 
     static __device__ __forceinline__ int row() { return (int)(threadIdx.x % kThreads) / (W / 8); }
     static __device__ __forceinline__ int column() { return (int)(threadIdx.x % kThreads) % (W / 8) * 8; }
 
-    __device__ __forceinline__ void start(const SeqView& v, int dim)
+    __device__ __forceinline__ void start(const SeqView& v, int dim_)
     {
+        dim = dim_;
+        vec = v.vec;
+        step = v.step * (int64_t)sizeof(D);
         // beyond every bound where the tile is wider than the rows
-        off = column() < dim ? ((uint32_t)row() * (uint32_t)v.step + column()) * (uint32_t)sizeof(D) : 0x7ffffff0u;
+        off = column() < dim ? (uint32_t)row() * (uint32_t)step + column() * (uint32_t)sizeof(D) : 0x7f000000u;
     }
-    __device__ __forceinline__ void fetch(const SeqView& v, int64_t n, int h, int64_t t0, int count, int dim)
+    __device__ __forceinline__ void place(const SeqView& v, int64_t n, int h, int64_t t)
     {
-        const D* const from = seq_row<D>(v, n, t0, h);
+        p = att_row<D>(v, n, t, h);
+    }
+    __device__ __forceinline__ void fetch(int count)
+    {
         if constexpr (kWide) {
-            const int step = (int)v.step * (int)sizeof(D);
+            const __amdgpu_buffer_rsrc_t rows = bounded(p, (count - 1) * (int)step + dim * (int)sizeof(D));
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-                const int left = count - u * kApart;  // rows from this unit's first on
-                const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
-                    (void*)(reinterpret_cast<const char*>(from) + (int64_t)u * kApart * step), (short)0,
-                    left > 0 ? (left - 1) * step + dim * (int)sizeof(D) : 0, 0x00020000);
+            for (int u = 0; u < kUnits; ++u)
 #pragma unroll
                 for (int k = 0; k < (int)sizeof(D) / 2; ++k)
-                    r[u].w[k] = __builtin_amdgcn_raw_buffer_load_b128(rows, off + 16u * k, 0, 0);
-            }
+                    r[u].w[k] = __builtin_amdgcn_raw_buffer_load_b128(
+                        rows, off + (uint32_t)(u * kApart) * (uint32_t)step + 16u * k, 0, 0);
         } else {
             const int c = column();
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 const int at = row() + u * kApart;
                 r[u] = Raw8<D>{};
-                if (at < count && c < dim) r[u] = load8<D>(from + (int64_t)at * v.step, c, dim, v.vec);
+                if (at < count && c < dim) r[u] = load8<D>(reinterpret_cast<const D*>(p + at * step), c, dim, vec);
             }
         }
+        p += kRows * step;
     }
     // Where put() puts this thread's first unit of a tile at `tile`.
     static __device__ __forceinline__ uint32_t lane(uint32_t tile)
@@ -522,7 +542,7 @@ struct OwnRows {
     __device__ __forceinline__ void load(const SeqView& v, int64_t n, int64_t t, int h, int dim, bool valid,
                                          int lane)
     {
-        const D* const row = seq_row<D>(v, n, t, h);
+        const D* const row = reinterpret_cast<const D*>(att_row<D>(v, n, t, h));
 #pragma unroll
         for (int ks = 0; ks < W / 16; ++ks) {
             const int c = 16 * ks + 8 * (lane >> 5);
@@ -673,8 +693,12 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
     auto fetch = [&](int it) {
         int j0, j1;
         kt.get(it, BK, j0, j1);
-        sk.fetch(x.k, b.n, b.kvh, j0, j1 - j0, x.dim_k);
-        sv.fetch(x.v, b.n, b.kvh, j0, j1 - j0, x.dim_v);
+        if (it == 0 || it == kt.far_tiles) {
+            sk.place(x.k, b.n, b.kvh, j0);
+            sv.place(x.v, b.n, b.kvh, j0);
+        }
+        sk.fetch(j1 - j0);
+        sv.fetch(j1 - j0);
     };
     // the lane's places in the tiles of the first buffer, moved to the other and back
     uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
@@ -794,8 +818,12 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
     auto fetch = [&](int it) {
         int j0, j1;
         kt.get(it, BK, j0, j1);
-        sk.fetch(x.k, b.n, b.kvh, j0, j1 - j0, x.dim_k);
-        sv.fetch(x.v, b.n, b.kvh, j0, j1 - j0, x.dim_v);
+        if (it == 0 || it == kt.far_tiles) {
+            sk.place(x.k, b.n, b.kvh, j0);
+            sv.place(x.v, b.n, b.kvh, j0);
+        }
+        sk.fetch(j1 - j0);
+        sv.fetch(j1 - j0);
     };
     // the lane's places in the tiles of the first buffer, moved to the other and back
     uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
@@ -882,29 +910,39 @@ struct QueryRows {
 template <class D>
 constexpr float kLessWeight = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
 
-// A tile of queries and their gradients on its way to LDS, from query step i (of the
-// keys' steps) on.
+// Tiles of queries and their gradients on their way to LDS, one behind the other.
 template <class D, int W, bool kWide, int kRows, int kThreads>
 struct QueryStage {
     AttStage<D, W, kRows, kWide, kThreads> q, d_o;
+    const char *lse_p, *delta_p;
+    int64_t lse_step;
     float lse, delta;
-    bool in;
 
-    __device__ __forceinline__ void begin(const AttArgs& x)
+    __device__ __forceinline__ void start(const AttArgs& x)
     {
         q.start(x.q, x.dim_k);
         d_o.start(x.dout, x.dim_v);
+        lse_step = x.lse.step * 4;
     }
-    __device__ __forceinline__ void fetch(const AttArgs& x, int64_t n, int head, int i, int end)
+    // The next tile begins at query t of a head.
+    __device__ __forceinline__ void place(const AttArgs& x, int64_t n, int head, int t)
     {
-        const int past = x.TK - x.T, count = min(kRows, end - i);
-        q.fetch(x.q, n, head, i - past, count, x.dim_k);
-        d_o.fetch(x.dout, n, head, i - past, count, x.dim_v);
-        // by every thread alike, and used only in put(): a use here would wait for all loads
-        const int a = (int)(threadIdx.x % kRows), at = min(i + a, end - 1);
-        in = a < count;
-        lse = *seq_row<float>(x.lse, n, at - past, head);
-        delta = x.delta[(n * x.H + head) * x.T + at - past];
+        q.place(x.q, n, head, t);
+        d_o.place(x.dout, n, head, t);
+        lse_p = att_row<float>(x.lse, n, t, head);
+        delta_p = reinterpret_cast<const char*>(x.delta + (n * x.H + head) * x.T + t);
+    }
+    // (queries behind the last one are seen by no key: what is loaded for them is not used)
+    __device__ __forceinline__ void fetch(int left)
+    {
+        const int count = min(kRows, left), a = threadIdx.x % kRows;
+        q.fetch(count);
+        d_o.fetch(count);
+        const int at = min(a, count - 1);
+        lse = *reinterpret_cast<const float*>(lse_p + at * lse_step);
+        delta = reinterpret_cast<const float*>(delta_p)[at];
+        lse_p += kRows * lse_step;
+        delta_p += kRows * 4;
     }
     // at: from q.lane(); the gradients' tile lies `apart` behind the queries'.
     __device__ __forceinline__ void put(uint32_t at, int apart, QueryRows<kRows>& rows) const
@@ -913,9 +951,8 @@ struct QueryStage {
         d_o.put(at + apart);
         if (threadIdx.x % kThreads < kRows) {
             const int a = threadIdx.x % kRows;
-            // queries behind the end have no weights
-            rows.lse2[a] = in ? fmaf(lse, kAttLog2e, -kWeightBits<D>) : INFINITY;
-            rows.delta[a] = in ? delta * kLessWeight<D> : 0.0f;
+            rows.lse2[a] = fmaf(lse, kAttLog2e, -kWeightBits<D>);
+            rows.delta[a] = delta * kLessWeight<D>;
         }
     }
 };
@@ -1047,12 +1084,13 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
     const int tiles = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = tiles * x.group;
     if (total > 0) {
         QueryStage<D, W, kWide, BQ, 256> stage;
-        stage.begin(x);
+        stage.start(x);
         uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
         uint32_t put_at = stage.q.lane(lds_address(lds));
-        int head = kvh * x.group, tile = 0, next_head = head, next = 0;
+        int tile = 0, next_head = kvh * x.group, next = 0;
         auto fetch = [&]() {
-            stage.fetch(x, n, next_head, begin + next * BQ, end);
+            if (next == 0) stage.place(x, n, next_head, begin - past);
+            stage.fetch(end - begin - next * BQ);
             if (++next == tiles) {
                 next = 0;
                 ++next_head;
@@ -1074,10 +1112,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
                                                      whole ? 0 : row_bits(j, until, i, h), lane, dk, dv);
                 }
             }
-            if (++tile == tiles) {
-                tile = 0;
-                ++head;
-            }
+            if (++tile == tiles) tile = 0;
             const uint32_t move = it & 1 ? -2 * kBytes : 2 * kBytes;
             by_row += move;
             by_col += move;
@@ -1159,18 +1194,20 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
     const int end = x.ends != nullptr ? min(i1, x.ends[n * x.TK + first]) : i1;
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
     QueryStage<D, W, kWide, BQ, kWave> stage;
-    stage.begin(x);
+    stage.start(x);
     const uint32_t mine = lds_address(lds[wave]), by_row = mine + Tile::row_lane(lane);
     const uint32_t by_col = mine + Tile::column_lane(lane), put_at = stage.q.lane(mine);
-    for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head)
+    for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head) {
+        if (begin < end) stage.place(x, n, head, begin - past);
         for (int i = begin; i < end; i += BQ) {
-            stage.fetch(x, n, head, i, end);
+            stage.fetch(end - i);
             stage.put(put_at, kBytes, rows[wave]);
             __builtin_amdgcn_wave_barrier();
             add_queries<D, W, kWide, kK, kV>(x, by_row, by_col, kBytes, rows[wave], 0, k, v, false,
                                              valid ? row_bits(j + x.window, end, i, h) : 0, lane, dk, dv);
             __builtin_amdgcn_wave_barrier();
         }
+    }
     if (s >= x.sinks) return;
     float* const to = far_sums<W>(x, row_of, c, s);
 #pragma unroll
