@@ -26,6 +26,11 @@
 
 #include "sequence.hpp"
 
+#ifndef LRS_KS
+#define LRS_KS 2
+#define LRS_GS 2
+#define LRS_GT 32
+#endif
 namespace lrs {
 
 constexpr int kMaxAttDim = 128;
@@ -209,11 +214,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const char* p, int byt
 // bounds make the zeros: one offset per lane, and no branch between the loads (where
 // branches meet each load would be waited for).  place() says where the next tile
 // begins, and after fetch() the one behind it is next.
-template <class D, int W, int kRows, bool kWide, int kThreads = 256>
+template <class D, int W, int kRows, bool kWide, int kThreads = 256, int kSets = 1>
 struct AttStage {
     static constexpr int kUnits = kRows * (W / 8) / kThreads, kApart = kThreads / (W / 8);
     static_assert(kApart % 16 == 0 || kThreads < 256, "rows of a thread's units lie alike");
-    Raw8<D> r[kUnits];
+    Raw8<D> r[kSets][kUnits];  // tiles on their way
     const char* p;
     int64_t step;      // bytes
     uint32_t off;      // kWide: of this thread's first unit
@@ -234,6 +239,7 @@ struct AttStage {
     {
         p = att_row<D>(v, n, t, h);
     }
+    template <int set = 0>
     __device__ __forceinline__ void fetch(int count)
     {
         if constexpr (kWide) {
@@ -242,15 +248,16 @@ struct AttStage {
             for (int u = 0; u < kUnits; ++u)
 #pragma unroll
                 for (int k = 0; k < (int)sizeof(D) / 2; ++k)
-                    r[u].w[k] = __builtin_amdgcn_raw_buffer_load_b128(
+                    r[set][u].w[k] = __builtin_amdgcn_raw_buffer_load_b128(
                         rows, off + (uint32_t)(u * kApart) * (uint32_t)step + 16u * k, 0, 0);
         } else {
             const int c = column();
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 const int at = row() + u * kApart;
-                r[u] = Raw8<D>{};
-                if (at < count && c < dim) r[u] = load8<D>(reinterpret_cast<const D*>(p + at * step), c, dim, vec);
+                r[set][u] = Raw8<D>{};
+                if (at < count && c < dim)
+                    r[set][u] = load8<D>(reinterpret_cast<const D*>(p + at * step), c, dim, vec);
             }
         }
         p += kRows * step;
@@ -260,6 +267,7 @@ struct AttStage {
     {
         return tile + AttTile<D, W>::at(row(), (int)sizeof(D) / 2 * (column() / 8));
     }
+    template <int set = 0>
     __device__ __forceinline__ void put(uint32_t mine) const
     {
 #pragma unroll
@@ -269,7 +277,7 @@ struct AttStage {
                 ? mine + u * kApart * AttTile<D, W>::kRow
                 : mine - lane(0) + AttTile<D, W>::at(row() + u * kApart, (int)sizeof(D) / 2 * (column() / 8));
 #pragma unroll
-            for (int k = 0; k < (int)sizeof(D) / 2; ++k) lds_store(at ^ (16u * k), r[u].w[k]);
+            for (int k = 0; k < (int)sizeof(D) / 2; ++k) lds_store(at ^ (16u * k), r[set][u].w[k]);
         }
     }
 };
@@ -595,16 +603,27 @@ __device__ __forceinline__ float own_dot(const SeqView& v, int64_t n, int64_t t,
 }
 
 // The products of 32 rows of tile `ta` (and of `tb`) with the wave's own rows, over
-// all W elements.
-template <class D, int W, bool kTwo, bool kWide>
+// all W elements.  Fragments are read kAhead products before they are used: left to
+// itself the compiler reads one, waits for it, and multiplies.
+template <class D, int W, bool kTwo, int kAhead, bool kWide>
 __device__ __forceinline__ void row_products(uint32_t ta, const OwnRows<D, W, kWide>& a, uint32_t tb,
                                              const OwnRows<D, W, kWide>& b, int row, f32x16& s, f32x16& t)
 {
     using Tile = AttTile<D, W>;
+    constexpr int N = W / 16;
+    AFrag<D> fa[N], fb[N];
 #pragma unroll
-    for (int ks = 0; ks < W / 16; ++ks) {
-        s = mma32<D>(Tile::rows(ta, row, ks), a.f[ks], s);
-        if constexpr (kTwo) t = mma32<D>(Tile::rows(tb, row, ks), b.f[ks], t);
+    for (int ks = 0; ks < N + kAhead; ++ks) {
+        if (ks < N) {
+            fa[ks] = Tile::rows(ta, row, ks);
+            if constexpr (kTwo) fb[ks] = Tile::rows(tb, row, ks);
+        }
+        if constexpr (kAhead > 0) __builtin_amdgcn_sched_barrier(0);
+        const int at = ks - kAhead;
+        if (at >= 0) {
+            s = mma32<D>(fa[at], a.f[at], s);
+            if constexpr (kTwo) t = mma32<D>(fb[at], b.f[at], t);
+        }
     }
 }
 
@@ -649,7 +668,11 @@ __device__ __forceinline__ bool finite(const f32x16 (&acc)[kTiles])
 template <class D, int W>
 constexpr int kKeyTile = sizeof(D) == 4 ? 32 : 64;
 template <class D, int W>
-constexpr int kGradTile = sizeof(D) == 4 && W == 128 ? 32 : 64;
+constexpr int kGradTile = W == 128 ? (sizeof(D) == 4 ? 32 : LRS_GT) : 64;
+template <class D, int W>
+constexpr int kKeySets = sizeof(D) == 4 ? 1 : LRS_KS;
+template <class D, int W>
+constexpr int kGradSets = sizeof(D) == 4 ? 1 : LRS_GS;
 template <class D, int W>
 constexpr int kAttBlocks = sizeof(D) == 4 && W == 128 ? 1 : 2;  // blocks per CU
 
@@ -673,6 +696,66 @@ struct AttBlock {
     }
 };
 
+// Goes over the tiles of keys and values that a block's queries see: compute(by_row,
+// by_col, is_far, j0, j1) for each, with a lane's places in the keys' tile (the values'
+// lies kBytes behind).  kSets: how many tiles are on their way from memory.
+template <class D, int W, int BK, bool kWide, int kSets, class Compute>
+__device__ __forceinline__ void over_keys(const AttArgs& x, const AttBlock& b, const KeyTiles& kt, char* lds, int lane,
+                                          Compute compute)
+{
+    using Tile = AttTile<D, W>;
+    constexpr int kBytes = BK * Tile::kRow;
+    AttStage<D, W, BK, kWide, 256, kSets> sk, sv;
+    sk.start(x.k, x.dim_k);
+    sv.start(x.v, x.dim_v);
+    int fetched = 0;
+    auto fetch = [&](auto set) {
+        constexpr int s = decltype(set)::value;
+        if (fetched == kt.tiles) return;
+        int j0, j1;
+        kt.get(fetched, BK, j0, j1);
+        if (fetched == 0 || fetched == kt.far_tiles) {
+            sk.place(x.k, b.n, b.kvh, j0);
+            sv.place(x.v, b.n, b.kvh, j0);
+        }
+        sk.template fetch<s>(j1 - j0);
+        sv.template fetch<s>(j1 - j0);
+        ++fetched;
+    };
+    // the lane's places in the tiles of the first buffer, moved to the other and back
+    uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
+    uint32_t put_at = sk.lane(lds_address(lds));
+    auto put = [&](auto set) {
+        sk.template put<decltype(set)::value>(put_at);
+        sv.template put<decltype(set)::value>(put_at + kBytes);
+    };
+    // Tile `it`, with the one behind it put down from `set` and another fetched into that.
+    auto step = [&](int it, auto set) {
+        __syncthreads();
+        int j0, j1;
+        kt.get(it, BK, j0, j1);
+        compute(by_row, by_col, it < kt.far_tiles, j0, j1);
+        const uint32_t move = it & 1 ? -2 * kBytes : 2 * kBytes;
+        by_row += move;
+        by_col += move;
+        put_at += move;
+        if (it + 1 < kt.tiles) {
+            put(set);
+            fetch(set);
+        }
+    };
+    constexpr std::integral_constant<int, 0> s0{};
+    constexpr std::integral_constant<int, kSets - 1> s1{};
+    fetch(s0);
+    put(s0);
+    fetch(s1);
+    if constexpr (kSets == 2) fetch(s0);
+    for (int it = 0; it < kt.tiles; it += 2) {
+        step(it, s1);
+        if (it + 1 < kt.tiles) step(it + 1, s0);
+    }
+}
+
 template <class D, int W, bool kWide>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const AttArgs x)
 {
@@ -687,91 +770,55 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
     q.load(x.q, b.n, wq.i - (x.TK - x.T), b.head, x.dim_k, wq.valid, lane);
     q.signs(x.scale < 0.0f);
 
-    AttStage<D, W, BK, kWide> sk, sv;
-    sk.start(x.k, x.dim_k);
-    sv.start(x.v, x.dim_v);
-    auto fetch = [&](int it) {
-        int j0, j1;
-        kt.get(it, BK, j0, j1);
-        if (it == 0 || it == kt.far_tiles) {
-            sk.place(x.k, b.n, b.kvh, j0);
-            sv.place(x.v, b.n, b.kvh, j0);
-        }
-        sk.fetch(j1 - j0);
-        sv.fetch(j1 - j0);
-    };
-    // the lane's places in the tiles of the first buffer, moved to the other and back
-    uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
-    uint32_t put_at = sk.lane(lds_address(lds));
-    auto put = [&]() {
-        sk.put(put_at);
-        sv.put(put_at + kBytes);
-    };
-    fetch(0);
-    put();
-    if (kt.tiles > 1) fetch(1);
-
     f32x16 o[W / 32] = {};
     float m = -INFINITY, l = 0.0f;  // m: the largest score; l: this half's sum
-    for (int it = 0; it < kt.tiles; ++it) {
-        __syncthreads();
-        int j0, j1;
-        kt.get(it, BK, j0, j1);
-        const bool is_far = it < kt.far_tiles;
-        if (wq.touches(kt, is_far, j0, j1)) {
-            f32x16 s[S] = {};
+    over_keys<D, W, BK, kWide, kKeySets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
+                                                                              bool is_far, int j0, int j1) {
+        if (!wq.touches(kt, is_far, j0, j1)) return;
+        f32x16 s[S] = {};
 #pragma unroll
-            for (int ks = 0; ks < W / 16; ++ks)
+        for (int ks = 0; ks < W / 16; ++ks)
 #pragma unroll
-                for (int a = 0; a < S; ++a) s[a] = mma32<D>(Tile::rows(by_row, 32 * a, ks), q.f[ks], s[a]);
-            if (!wq.whole(is_far, j0, j1, BK)) {
+            for (int a = 0; a < S; ++a) s[a] = mma32<D>(Tile::rows(by_row, 32 * a, ks), q.f[ks], s[a]);
+        if (!wq.whole(is_far, j0, j1, BK)) {
 #pragma unroll
-                for (int a = 0; a < S; ++a) keep_bits(wq.bits(is_far, j0 + 32 * a, j1, h), s[a], -INFINITY);
+            for (int a = 0; a < S; ++a) keep_bits(wq.bits(is_far, j0 + 32 * a, j1, h), s[a], -INFINITY);
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int a = 0; a < S; ++a)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[a][r]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // the sums are scaled again only when the largest score has grown by 2^8
+        if (__any((top - m) * x.c > 8.0f)) {
+            const float to = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - to) * x.c);
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[dt][r] *= f;
+        }
+        const float base = m == -INFINITY ? 0.0f : m * x.c;
+#pragma unroll
+        for (int a = 0; a < S; ++a)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[a][r] = __builtin_amdgcn_exp2f(fmaf(s[a][r], x.c, -base));
+                l += s[a][r];
             }
-            float top = s[0][0];
 #pragma unroll
-            for (int a = 0; a < S; ++a)
+        for (int a = 0; a < S; ++a)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[a][r]);
-            top = fmaxf(top, __shfl_xor(top, 32));
-            // the sums are scaled again only when the largest score has grown by 2^8
-            if (__any((top - m) * x.c > 8.0f)) {
-                const float to = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - to) * x.c);
-                m = to;
-                l *= f;
+            for (int u = 0; u < 2; ++u) {
+                const AFrag<D> p = operand<D>(s[a], u);
 #pragma unroll
                 for (int dt = 0; dt < W / 32; ++dt)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[dt][r] *= f;
+                    o[dt] = mma32<D>(Tile::columns(by_col + kBytes, 32 * a + 16 * u, 32 * dt), p, o[dt]);
             }
-            const float base = m == -INFINITY ? 0.0f : m * x.c;
-#pragma unroll
-            for (int a = 0; a < S; ++a)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[a][r] = __builtin_amdgcn_exp2f(fmaf(s[a][r], x.c, -base));
-                    l += s[a][r];
-                }
-#pragma unroll
-            for (int a = 0; a < S; ++a)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const AFrag<D> p = operand<D>(s[a], u);
-#pragma unroll
-                    for (int dt = 0; dt < W / 32; ++dt)
-                        o[dt] = mma32<D>(Tile::columns(by_col + kBytes, 32 * a + 16 * u, 32 * dt), p, o[dt]);
-                }
-        }
-        const uint32_t move = it & 1 ? -2 * kBytes : 2 * kBytes;
-        by_row += move;
-        by_col += move;
-        put_at += move;
-        if (it + 1 < kt.tiles) {
-            put();
-            if (it + 2 < kt.tiles) fetch(it + 2);
-        }
-    }
+    });
     if (!wq.any()) return;
     l += __shfl_xor(l, 32);
     const float by = 1.0f / l, lse = (m * x.c + __builtin_amdgcn_logf(l)) * kAttLn2;
@@ -812,43 +859,16 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
         if (wq.valid && h == 0) *delta_at = delta;
     }
 
-    AttStage<D, W, BK, kWide> sk, sv;
-    sk.start(x.k, x.dim_k);
-    sv.start(x.v, x.dim_v);
-    auto fetch = [&](int it) {
-        int j0, j1;
-        kt.get(it, BK, j0, j1);
-        if (it == 0 || it == kt.far_tiles) {
-            sk.place(x.k, b.n, b.kvh, j0);
-            sv.place(x.v, b.n, b.kvh, j0);
-        }
-        sk.fetch(j1 - j0);
-        sv.fetch(j1 - j0);
-    };
-    // the lane's places in the tiles of the first buffer, moved to the other and back
-    uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
-    uint32_t put_at = sk.lane(lds_address(lds));
-    auto put = [&]() {
-        sk.put(put_at);
-        sv.put(put_at + kBytes);
-    };
-    fetch(0);
-    put();
-    if (kt.tiles > 1) fetch(1);
-
     f32x16 dq[W / 32] = {};
     float sum = 0.0f;
-    for (int it = 0; it < kt.tiles; ++it) {
-        __syncthreads();
-        int j0, j1;
-        kt.get(it, BK, j0, j1);
-        const bool is_far = it < kt.far_tiles;
+    over_keys<D, W, BK, kWide, kGradSets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
+                                                                               bool is_far, int j0, int j1) {
 #pragma unroll
         for (int at = 0; at < BK; at += 32) {
             const int ja = j0 + at, jb = min(ja + 32, j1);
             if (ja >= j1 || !wq.touches(kt, is_far, ja, jb)) continue;
             f32x16 s = {}, dp = {};
-            row_products<D, W, true>(by_row, q, by_row + kBytes, d_o, at, s, dp);
+            row_products<D, W, true, 1>(by_row, q, by_row + kBytes, d_o, at, s, dp);
             constexpr int N = W / 32;
 #pragma unroll
             for (int r = 0; r < 16; ++r)
@@ -872,15 +892,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
                 }
             }
         }
-        const uint32_t move = it & 1 ? -2 * kBytes : 2 * kBytes;
-        by_row += move;
-        by_col += move;
-        put_at += move;
-        if (it + 1 < kt.tiles) {
-            put();
-            if (it + 2 < kt.tiles) fetch(it + 2);
-        }
-    }
+    });
     if constexpr (kSum) {
         sum += __shfl_xor(sum, 32);
         if (wq.valid && h == 0) *delta_at = sum;
@@ -911,12 +923,12 @@ template <class D>
 constexpr float kLessWeight = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
 
 // Tiles of queries and their gradients on their way to LDS, one behind the other.
-template <class D, int W, bool kWide, int kRows, int kThreads>
+template <class D, int W, bool kWide, int kRows, int kThreads, int kSets = 1>
 struct QueryStage {
-    AttStage<D, W, kRows, kWide, kThreads> q, d_o;
+    AttStage<D, W, kRows, kWide, kThreads, kSets> q, d_o;
     const char *lse_p, *delta_p;
     int64_t lse_step;
-    float lse, delta;
+    float lse[kSets], delta[kSets];
 
     __device__ __forceinline__ void start(const AttArgs& x)
     {
@@ -933,26 +945,28 @@ struct QueryStage {
         delta_p = reinterpret_cast<const char*>(x.delta + (n * x.H + head) * x.T + t);
     }
     // (queries behind the last one are seen by no key: what is loaded for them is not used)
+    template <int set = 0>
     __device__ __forceinline__ void fetch(int left)
     {
         const int count = min(kRows, left), a = threadIdx.x % kRows;
-        q.fetch(count);
-        d_o.fetch(count);
+        q.template fetch<set>(count);
+        d_o.template fetch<set>(count);
         const int at = min(a, count - 1);
-        lse = *reinterpret_cast<const float*>(lse_p + at * lse_step);
-        delta = reinterpret_cast<const float*>(delta_p)[at];
+        lse[set] = *reinterpret_cast<const float*>(lse_p + at * lse_step);
+        delta[set] = reinterpret_cast<const float*>(delta_p)[at];
         lse_p += kRows * lse_step;
         delta_p += kRows * 4;
     }
     // at: from q.lane(); the gradients' tile lies `apart` behind the queries'.
+    template <int set = 0>
     __device__ __forceinline__ void put(uint32_t at, int apart, QueryRows<kRows>& rows) const
     {
-        q.put(at);
-        d_o.put(at + apart);
+        q.template put<set>(at);
+        d_o.template put<set>(at + apart);
         if (threadIdx.x % kThreads < kRows) {
             const int a = threadIdx.x % kRows;
-            rows.lse2[a] = fmaf(lse, kAttLog2e, -kWeightBits<D>);
-            rows.delta[a] = delta * kLessWeight<D>;
+            rows.lse2[a] = fmaf(lse[set], kAttLog2e, -kWeightBits<D>);
+            rows.delta[a] = delta[set] * kLessWeight<D>;
         }
     }
 };
@@ -970,7 +984,7 @@ __device__ __forceinline__ void add_queries(const AttArgs& x, uint32_t by_row, u
     constexpr int N = W / 32;
     const int h = lane >> 5;
     f32x16 s = {}, dp = {};
-    row_products<D, W, kK>(by_row, k, by_row + apart, v, at, s, dp);
+    row_products<D, W, kK, 1>(by_row, k, by_row + apart, v, at, s, dp);
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
         const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&row.lse2[at + 8 * r4 + 4 * h]);
@@ -1024,10 +1038,10 @@ __device__ __forceinline__ float* far_sums(const AttArgs& x, int64_t row, int ch
 // for that of the values (kV): together they need more registers than two waves on a
 // SIMD have, and one wave alone waits through its softmax.
 template <class D, int W>
-#ifndef LRS_BQ
-#define LRS_BQ 32
-#endif
-constexpr int kQueryTile = W == 128 ? (sizeof(D) == 4 ? 32 : LRS_BQ) : 64;
+constexpr int kQueryTile = W == 128 || sizeof(D) == 2 ? 32 : 64;
+
+template <class D, int W>
+constexpr int kQuerySets = sizeof(D) == 4 ? 1 : 2;
 
 template <class D, int W>
 constexpr bool kSplitGrads = W * (int)sizeof(D) > 128;
@@ -1083,23 +1097,24 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
     const int tiles = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = tiles * x.group;
     if (total > 0) {
-        QueryStage<D, W, kWide, BQ, 256> stage;
+        // tiles are loaded two ahead: what one tile takes to compute is less than a load takes
+        QueryStage<D, W, kWide, BQ, 256, kQuerySets<D, W>> stage;
         stage.start(x);
         uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
         uint32_t put_at = stage.q.lane(lds_address(lds));
-        int tile = 0, next_head = kvh * x.group, next = 0;
-        auto fetch = [&]() {
+        int tile = 0, next_head = kvh * x.group, next = 0, fetched = 0;
+        auto fetch = [&](auto set) {
+            if (fetched == total) return;
+            ++fetched;
             if (next == 0) stage.place(x, n, next_head, begin - past);
-            stage.fetch(end - begin - next * BQ);
+            stage.template fetch<decltype(set)::value>(end - begin - next * BQ);
             if (++next == tiles) {
                 next = 0;
                 ++next_head;
             }
         };
-        fetch();
-        stage.put(put_at, kBytes, rows[0]);
-        if (total > 1) fetch();
-        for (int it = 0; it < total; ++it) {
+        // Tile `it`, with the one behind it put down from `set` and another fetched into that.
+        auto step = [&](int it, auto set) {
             __syncthreads();
             const QueryRows<BQ>& row = rows[it & 1];
 #pragma unroll
@@ -1118,9 +1133,19 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
             by_col += move;
             put_at += move;
             if (it + 1 < total) {
-                stage.put(put_at, kBytes, rows[(it + 1) & 1]);
-                if (it + 2 < total) fetch();
+                stage.template put<decltype(set)::value>(put_at, kBytes, rows[(it + 1) & 1]);
+                fetch(set);
             }
+        };
+        constexpr std::integral_constant<int, 0> s0{};
+        constexpr std::integral_constant<int, kQuerySets<D, W> - 1> s1{};
+        fetch(s0);
+        stage.template put<0>(put_at, kBytes, rows[0]);
+        fetch(s1);
+        if constexpr (kQuerySets<D, W> == 2) fetch(s0);
+        for (int it = 0; it < total; it += 2) {
+            step(it, s1);
+            if (it + 1 < total) step(it + 1, s0);
         }
     }
     constexpr float kLess = kLessWeight<D>;
