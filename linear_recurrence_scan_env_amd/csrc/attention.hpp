@@ -1020,7 +1020,7 @@ __device__ __forceinline__ void add_queries(const AttArgs& x, uint32_t by_row, u
 
 // First steps of an episode are seen by all of its queries.  Those beyond the end of
 // the chunk of kFarChunk steps that the episode begins in are left to a kernel of
-// their own (attend_far), a wave to a chunk, which keeps the sums of each chunk
+// their own (attend_far), a block to a chunk, which keeps the sums of each chunk
 // apart for attend_dkv to join: or one block would walk the whole episode.
 constexpr int kFarChunk = 256;
 constexpr int kFarSinks = 64;  // with more first steps than this attend_dkv does it all
@@ -1156,17 +1156,18 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
         const int last = valid && s < x.sinks ? (x.ends != nullptr ? x.ends[n * x.TK + j] : x.TK) - 1 : -1;
         const int c0 = max(first / kFarChunk + 1, past / kFarChunk);
         auto add = [&](f32x16(&acc)[W / 32], int from) {
+            const float* at = far_sums<W>(x, n * kv + kvh, c0, s) + from + 4 * h;
+            for (int c = c0; c <= last / kFarChunk; ++c, at += (int64_t)x.sinks * 2 * W) {
+                f32x4 v[W / 32][4];
 #pragma unroll
-            for (int dt = 0; dt < W / 32; ++dt)
+                for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int c = c0; c <= last / kFarChunk; ++c)
-                        sum += *reinterpret_cast<const f32x4*>(far_sums<W>(x, n * kv + kvh, c, s) + from + 32 * dt +
-                                                               8 * r4 + 4 * h);
+                    for (int r4 = 0; r4 < 4; ++r4) v[dt][r4] = *reinterpret_cast<const f32x4*>(at + 32 * dt + 8 * r4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[dt][4 * r4 + e] += sum[e];
-                }
+                for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[dt][r] += v[dt][r / 4][r % 4];
+            }
         };
         if constexpr (kK) add(dk, 0);
         if constexpr (kV) add(dv, W);
@@ -1183,47 +1184,46 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
         careful_dkv<D, kK, kV>(x, n, kvh, mine0 + __builtin_ctzll(again), lane);
 }
 
-// What the queries of one chunk beyond its window give to the first steps of the
+// What the queries of one chunk beyond its window give to 32 first steps of the
 // episode that the chunk begins in the middle of, summed over the heads that share
-// them: a wave to 32 of those steps.
+// them: a quarter of the chunk to each wave, joined through LDS.
 template <class D, int W, bool kWide, bool kK, bool kV>
 __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
-    constexpr int BQ = 32, kBytes = BQ * Tile::kRow;
-    __shared__ alignas(1024) char lds[4][2][kBytes];
+    constexpr int BQ = 32, kBytes = BQ * Tile::kRow, kPart = kFarChunk / 4;
+    // a wave's two tiles, and after them its sums (W x 32 values)
+    constexpr int kRegion = 2 * kBytes > W * 128 ? 2 * kBytes : W * 128;
+    __shared__ alignas(1024) char lds[4][kRegion];
     __shared__ QueryRows<BQ> rows[4];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int past = x.TK - x.T, kv = x.H / x.group, chunks = x.far_chunks, parts = (x.sinks + 31) / 32;
-    int64_t id = (int64_t)blockIdx.x * 4 + wave;
+    uint32_t id = blockIdx.x;
     const int part = id % parts;
     id /= parts;
-    const int c = (int)(id % chunks);
+    const int c = id % chunks;
     id /= chunks;
-    if (id >= x.N * kv) return;  // (waves are on their own: there is no barrier)
-    const int64_t row_of = id;
-    const int kvh = (int)(id % kv);
+    const int kvh = id % kv;
     const int64_t n = id / kv;
     const int i0 = c * kFarChunk, i1 = min(i0 + kFarChunk, x.TK);
-    if (i1 <= past) return;
     const int first = episode_start(x, n, i0);
+    if (i1 <= past || first / kFarChunk == c) return;  // (the whole block)
     const int s = 32 * part + (lane & 31), j = first + s;
-    if (first / kFarChunk == c) return;
     const bool valid = s < x.sinks && j < x.TK;
     OwnRows<D, W, kWide> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
     k.signs(x.scale < 0.0f);
     if constexpr (kK) v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
-    const int begin = max(max(i0, past), first + 32 * part + x.window);
-    const int end = x.ends != nullptr ? min(i1, x.ends[n * x.TK + first]) : i1;
+    const int begin = max(max(i0 + wave * kPart, past), first + 32 * part + x.window);
+    const int end = min(min(i1, i0 + (wave + 1) * kPart), x.ends != nullptr ? x.ends[n * x.TK + first] : x.TK);
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
     QueryStage<D, W, kWide, BQ, kWave> stage;
     stage.start(x);
     const uint32_t mine = lds_address(lds[wave]), by_row = mine + Tile::row_lane(lane);
     const uint32_t by_col = mine + Tile::column_lane(lane), put_at = stage.q.lane(mine);
-    for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head) {
-        if (begin < end) stage.place(x, n, head, begin - past);
+    for (int head = kvh * x.group; begin < end && head < (kvh + 1) * x.group; ++head) {
+        stage.place(x, n, head, begin - past);
         for (int i = begin; i < end; i += BQ) {
             stage.fetch(end - i);
             stage.put(put_at, kBytes, rows[wave]);
@@ -1233,16 +1233,30 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
             __builtin_amdgcn_wave_barrier();
         }
     }
-    if (s >= x.sinks) return;
-    float* const to = far_sums<W>(x, row_of, c, s);
+    float* const to = far_sums<W>(x, n * kv + kvh, c, s);
+    auto join = [&](const f32x16(&acc)[W / 32], int from) {
+        __syncthreads();
+        float* const own = reinterpret_cast<float*>(lds[wave]);
 #pragma unroll
-    for (int dt = 0; dt < W / 32; ++dt)
+        for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-            const int at = 32 * dt + 8 * r4 + 4 * h;
-            if constexpr (kK) *reinterpret_cast<f32x4*>(to + at) = f32x4{dk[dt][4 * r4], dk[dt][4 * r4 + 1], dk[dt][4 * r4 + 2], dk[dt][4 * r4 + 3]};
-            if constexpr (kV) *reinterpret_cast<f32x4*>(to + W + at) = f32x4{dv[dt][4 * r4], dv[dt][4 * r4 + 1], dv[dt][4 * r4 + 2], dv[dt][4 * r4 + 3]};
+            for (int r = 0; r < 16; ++r) own[(16 * dt + r) * kWave + lane] = acc[dt][r];
+        __syncthreads();
+        // a quarter of the values to each wave: registers 4 wave .. 4 wave + 3 of each tile
+        if (s >= x.sinks) return;
+#pragma unroll
+        for (int dt = 0; dt < W / 32; ++dt) {
+            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sum[e] += reinterpret_cast<const float*>(lds[w])[(16 * dt + 4 * wave + e) * kWave + lane];
+            *reinterpret_cast<f32x4*>(to + from + 32 * dt + 8 * wave + 4 * h) = sum;
         }
+    };
+    if constexpr (kK) join(dk, 0);
+    if constexpr (kV) join(dv, W);
 }
 
 // The first step of each step's episode and the step behind its last, [N, TK]: a
@@ -1681,8 +1695,8 @@ template <class D, int W, bool kWide, bool kK, bool kV>
 lrs_status launch_dkv(const char* nm, AttArgs x, hipStream_t stream)
 {
     if (x.far_part != nullptr) {
-        const int64_t waves = x.N * (x.H / x.group) * x.far_chunks * ((x.sinks + 31) / 32);
-        LRS_TRY(launch_seq(nm, attend_far<D, W, kWide, kK, kV>, (uint64_t)((waves + 3) / 4), 256, stream, x));
+        const int64_t blocks = x.N * (x.H / x.group) * x.far_chunks * ((x.sinks + 31) / 32);
+        LRS_TRY(launch_seq(nm, attend_far<D, W, kWide, kK, kV>, (uint64_t)blocks, 256, stream, x));
     }
     const uint64_t blocks = key_blocks(x);
     return launch_seq(nm, attend_dkv<D, W, kWide, kK, kV>, blocks, 256, stream, x);
