@@ -210,18 +210,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const char* p, int byt
 
 // Rows of memory on their way into a tile of kRows rows, by a block of 256 threads
 // or by a wave.  What lies beyond the last row or the dimension becomes zeros.
-// kWide: rows are whole 16-byte units, loaded through a buffer descriptor whose
-// bounds make the zeros: one offset per lane, and no branch between the loads (where
-// branches meet each load would be waited for).  place() says where the next tile
+// kBy: rows are taken by 8 elements (16-bit types), by 4 (dims of whole fours, rows on
+// as many), or 0: by the element with branches.  The first two load through a buffer
+// descriptor whose bounds make the zeros, and have no branch between the loads: where
+// branches meet each load would be waited for.  place() says where the next tile
 // begins, and after fetch() the one behind it is next.
-template <class D, int W, int kRows, bool kWide, int kThreads = 256, int kSets = 1>
+template <class D, int W, int kRows, int kBy, int kThreads = 256, int kSets = 1>
 struct AttStage {
     static constexpr int kUnits = kRows * (W / 8) / kThreads, kApart = kThreads / (W / 8);
     static_assert(kApart % 16 == 0 || kThreads < 256, "rows of a thread's units lie alike");
     Raw8<D> r[kSets][kUnits];  // tiles on their way
     const char* p;
     int64_t step;      // bytes
-    uint32_t off;      // kWide: of this thread's first unit
+    uint32_t off[2];   // where this thread's first unit begins, and its other half (kBy = 4)
     int dim, vec;
 
     static __device__ __forceinline__ int row() { return (int)(threadIdx.x % kThreads) / (W / 8); }
@@ -233,7 +234,9 @@ struct AttStage {
         vec = v.vec;
         step = v.step * (int64_t)sizeof(D);
         // beyond every bound where the tile is wider than the rows
-        off = column() < dim ? (uint32_t)row() * (uint32_t)step + column() * (uint32_t)sizeof(D) : 0x7f000000u;
+        for (int k = 0; k < 2; ++k)
+            off[k] = column() + 4 * k < dim
+                ? (uint32_t)row() * (uint32_t)step + (column() + 4 * k) * (uint32_t)sizeof(D) : 0x7f000000u;
     }
     __device__ __forceinline__ void place(const SeqView& v, int64_t n, int h, int64_t t)
     {
@@ -242,14 +245,23 @@ struct AttStage {
     template <int set = 0>
     __device__ __forceinline__ void fetch(int count)
     {
-        if constexpr (kWide) {
+        if constexpr (kBy > 0) {
             const __amdgpu_buffer_rsrc_t rows = bounded(p, (count - 1) * (int)step + dim * (int)sizeof(D));
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u)
+            for (int u = 0; u < kUnits; ++u) {
+                const uint32_t more = (uint32_t)(u * kApart) * (uint32_t)step;
+                if constexpr (kBy == 8) {
+                    r[set][u].w[0] = __builtin_amdgcn_raw_buffer_load_b128(rows, off[0] + more, 0, 0);
+                } else if constexpr (sizeof(D) == 4) {
 #pragma unroll
-                for (int k = 0; k < (int)sizeof(D) / 2; ++k)
-                    r[set][u].w[k] = __builtin_amdgcn_raw_buffer_load_b128(
-                        rows, off + (uint32_t)(u * kApart) * (uint32_t)step + 16u * k, 0, 0);
+                    for (int k = 0; k < 2; ++k)
+                        r[set][u].w[k] = __builtin_amdgcn_raw_buffer_load_b128(rows, off[k] + more, 0, 0);
+                } else {
+                    const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(rows, off[0] + more, 0, 0);
+                    const u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(rows, off[1] + more, 0, 0);
+                    r[set][u].w[0] = u32x4{a[0], a[1], b[0], b[1]};
+                }
+            }
         } else {
             const int c = column();
 #pragma unroll
@@ -543,7 +555,7 @@ __device__ __forceinline__ void careful_dkv(const AttArgs& x, int64_t n, int kvh
 // -------------------------------------------------------------- fast kernels
 
 // 32 rows (queries or keys, a lane's own) as operands: element 16 ks + 8 h + e.
-template <class D, int W, bool kWide>
+template <class D, int W, int kBy>
 struct OwnRows {
     AFrag<D> f[W / 16];
 
@@ -556,10 +568,16 @@ struct OwnRows {
             const int c = 16 * ks + 8 * (lane >> 5);
             f[ks] = AFrag<D>{};
             if (!valid || c >= dim) continue;
-            if constexpr (kWide) {
-#pragma unroll
-                for (int k = 0; k < (int)sizeof(D) / 2; ++k)
-                    f[ks].w[k] = *reinterpret_cast<const u32x4*>(row + c + k * (16 / (int)sizeof(D)));
+            if constexpr (kBy == 8) {
+                f[ks].w[0] = *reinterpret_cast<const u32x4*>(row + c);
+            } else if constexpr (kBy == 4 && sizeof(D) == 4) {
+                f[ks].w[0] = *reinterpret_cast<const u32x4*>(row + c);
+                if (c + 4 < dim) f[ks].w[1] = *reinterpret_cast<const u32x4*>(row + c + 4);
+            } else if constexpr (kBy == 4) {
+                const u32x2 a = *reinterpret_cast<const u32x2*>(row + c);
+                u32x2 b = {};
+                if (c + 4 < dim) b = *reinterpret_cast<const u32x2*>(row + c + 4);
+                f[ks].w[0] = u32x4{a[0], a[1], b[0], b[1]};
             } else {
                 f[ks] = load8<D>(row, c, dim, v.vec);
             }
@@ -577,11 +595,11 @@ struct OwnRows {
 };
 
 // The products of a lane's own rows with others of the same place, summed.
-template <class D, int W, bool kWide>
+template <class D, int W, int kBy>
 __device__ __forceinline__ float own_dot(const SeqView& v, int64_t n, int64_t t, int head, int dim, bool valid,
-                                         int lane, const OwnRows<D, W, kWide>& with)
+                                         int lane, const OwnRows<D, W, kBy>& with)
 {
-    OwnRows<D, W, kWide> o;
+    OwnRows<D, W, kBy> o;
     o.load(v, n, t, head, dim, valid, lane);
     float sum = 0.0f;
 #pragma unroll
@@ -605,9 +623,9 @@ __device__ __forceinline__ float own_dot(const SeqView& v, int64_t n, int64_t t,
 // The products of 32 rows of tile `ta` (and of `tb`) with the wave's own rows, over
 // all W elements.  Fragments are read kAhead products before they are used: left to
 // itself the compiler reads one, waits for it, and multiplies.
-template <class D, int W, bool kTwo, int kAhead, bool kWide>
-__device__ __forceinline__ void row_products(uint32_t ta, const OwnRows<D, W, kWide>& a, uint32_t tb,
-                                             const OwnRows<D, W, kWide>& b, int row, f32x16& s, f32x16& t)
+template <class D, int W, bool kTwo, int kAhead, int kBy>
+__device__ __forceinline__ void row_products(uint32_t ta, const OwnRows<D, W, kBy>& a, uint32_t tb,
+                                             const OwnRows<D, W, kBy>& b, int row, f32x16& s, f32x16& t)
 {
     using Tile = AttTile<D, W>;
     constexpr int N = W / 16;
@@ -629,7 +647,7 @@ __device__ __forceinline__ void row_products(uint32_t ta, const OwnRows<D, W, kW
 
 // Writes a product whose columns are the wave's rows (a lane's own: `row`) and
 // whose rows are elements; rows of memory get four elements at a time.
-template <class D, bool kWide, int kTiles>
+template <class D, int kBy, int kTiles>
 __device__ __forceinline__ void store_own(D* row, const f32x16 (&acc)[kTiles], float by, int dim, int h)
 {
 #pragma unroll
@@ -639,7 +657,7 @@ __device__ __forceinline__ void store_own(D* row, const f32x16 (&acc)[kTiles], f
             const int c = 32 * dt + 8 * r4 + 4 * h;
             const float v[4] = {acc[dt][4 * r4] * by, acc[dt][4 * r4 + 1] * by, acc[dt][4 * r4 + 2] * by,
                                 acc[dt][4 * r4 + 3] * by};
-            if (kWide) {
+            if constexpr (kBy > 0) {
                 if (c >= dim) continue;
                 if constexpr (sizeof(D) == 4)
                     *reinterpret_cast<f32x4*>(row + c) = f32x4{v[0], v[1], v[2], v[3]};
@@ -699,13 +717,13 @@ struct AttBlock {
 // Goes over the tiles of keys and values that a block's queries see: compute(by_row,
 // by_col, is_far, j0, j1) for each, with a lane's places in the keys' tile (the values'
 // lies kBytes behind).  kSets: how many tiles are on their way from memory.
-template <class D, int W, int BK, bool kWide, int kSets, class Compute>
+template <class D, int W, int BK, int kBy, int kSets, class Compute>
 __device__ __forceinline__ void over_keys(const AttArgs& x, const AttBlock& b, const KeyTiles& kt, char* lds, int lane,
                                           Compute compute)
 {
     using Tile = AttTile<D, W>;
     constexpr int kBytes = BK * Tile::kRow;
-    AttStage<D, W, BK, kWide, 256, kSets> sk, sv;
+    AttStage<D, W, BK, kBy, 256, kSets> sk, sv;
     sk.start(x.k, x.dim_k);
     sv.start(x.v, x.dim_v);
     int fetched = 0;
@@ -756,7 +774,7 @@ __device__ __forceinline__ void over_keys(const AttArgs& x, const AttBlock& b, c
     }
 }
 
-template <class D, int W, bool kWide>
+template <class D, int W, int kBy>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
@@ -766,13 +784,13 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
     const AttBlock b(x);
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
     const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
-    OwnRows<D, W, kWide> q;
+    OwnRows<D, W, kBy> q;
     q.load(x.q, b.n, wq.i - (x.TK - x.T), b.head, x.dim_k, wq.valid, lane);
     q.signs(x.scale < 0.0f);
 
     f32x16 o[W / 32] = {};
     float m = -INFINITY, l = 0.0f;  // m: the largest score; l: this half's sum
-    over_keys<D, W, BK, kWide, kKeySets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
+    over_keys<D, W, BK, kBy, kKeySets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
                                                                               bool is_far, int j0, int j1) {
         if (!wq.touches(kt, is_far, j0, j1)) return;
         f32x16 s[S] = {};
@@ -825,7 +843,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
     const int t = wq.i - (x.TK - x.T);
     const bool fine = finite(o) && by < INFINITY && fabsf(lse) < INFINITY;
     if (wq.valid) {
-        store_own<D, kWide>(seq_row_out<D>(x.o, b.n, t, b.head), o, by, x.dim_v, h);
+        store_own<D, kBy>(seq_row_out<D>(x.o, b.n, t, b.head), o, by, x.dim_v, h);
         if (h == 0 && x.lse.p != nullptr) *seq_row_out<float>(x.lse, b.n, t, b.head) = lse;
     }
     uint64_t again = __ballot(wq.valid && !fine);
@@ -834,7 +852,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
 }
 
 // kSum: the pass before, for short windows, which only sums D as sum_j p_ij do_i . v_j.
-template <class D, int W, bool kWide, bool kSum>
+template <class D, int W, int kBy, bool kSum>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
@@ -845,7 +863,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
     const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
     const int t = wq.i - (x.TK - x.T);
-    OwnRows<D, W, kWide> q, d_o;
+    OwnRows<D, W, kBy> q, d_o;
     q.load(x.q, b.n, t, b.head, x.dim_k, wq.valid, lane);
     q.signs(x.scale < 0.0f);
     d_o.load(x.dout, b.n, t, b.head, x.dim_v, wq.valid, lane);
@@ -855,13 +873,13 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
     if (x.sum_delta) {
         if (!kSum && wq.valid) delta = *delta_at;
     } else {
-        delta = own_dot<D, W, kWide>(x.o, b.n, t, b.head, x.dim_v, wq.valid, lane, d_o);
+        delta = own_dot<D, W, kBy>(x.o, b.n, t, b.head, x.dim_v, wq.valid, lane, d_o);
         if (wq.valid && h == 0) *delta_at = delta;
     }
 
     f32x16 dq[W / 32] = {};
     float sum = 0.0f;
-    over_keys<D, W, BK, kWide, kGradSets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
+    over_keys<D, W, BK, kBy, kGradSets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
                                                                                bool is_far, int j0, int j1) {
 #pragma unroll
         for (int at = 0; at < BK; at += 32) {
@@ -901,7 +919,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
     if (!wq.any()) return;
     const bool fine = finite(dq);
     if (wq.valid)
-        store_own<D, kWide>(seq_row_out<D>(x.dq, b.n, t, b.head), dq, x.scale, x.dim_k, h);
+        store_own<D, kBy>(seq_row_out<D>(x.dq, b.n, t, b.head), dq, x.scale, x.dim_k, h);
     uint64_t again = __ballot(wq.valid && !fine);
     for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
         careful_dq<D>(x, b.n, b.head, wq.first + __builtin_ctzll(again), lane);
@@ -923,9 +941,9 @@ template <class D>
 constexpr float kLessWeight = kWeightBits<D> == 0.0f ? 1.0f : 0x1p-10f;
 
 // Tiles of queries and their gradients on their way to LDS, one behind the other.
-template <class D, int W, bool kWide, int kRows, int kThreads, int kSets = 1>
+template <class D, int W, int kBy, int kRows, int kThreads, int kSets = 1>
 struct QueryStage {
-    AttStage<D, W, kRows, kWide, kThreads, kSets> q, d_o;
+    AttStage<D, W, kRows, kBy, kThreads, kSets> q, d_o;
     const char *lse_p, *delta_p;
     int64_t lse_step;
     float lse[kSets], delta[kSets];
@@ -974,9 +992,9 @@ struct QueryStage {
 // Adds what 32 queries in LDS give to the gradients of the wave's keys: of the keys
 // (kK), of the values (kV).  bits: the rows whose queries see the lane's key; not
 // looked at where `whole`.
-template <class D, int W, bool kWide, bool kK, bool kV, class Rows>
+template <class D, int W, int kBy, bool kK, bool kV, class Rows>
 __device__ __forceinline__ void add_queries(const AttArgs& x, uint32_t by_row, uint32_t by_col, int apart, const Rows& row, int at,
-                                            const OwnRows<D, W, kWide>& k, const OwnRows<D, W, kWide>& v, bool whole,
+                                            const OwnRows<D, W, kBy>& k, const OwnRows<D, W, kBy>& v, bool whole,
                                             uint32_t bits, int lane, f32x16 (&dk)[W / 32], f32x16 (&dv)[W / 32])
 {
     using Tile = AttTile<D, W>;
@@ -1057,7 +1075,7 @@ __device__ __forceinline__ int seen_until(const AttArgs& x, int64_t n, int j)
     return min(until, end);
 }
 
-template <class D, int W, bool kWide, bool kK, bool kV>
+template <class D, int W, int kBy, bool kK, bool kV>
 __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void attend_dkv(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
@@ -1074,7 +1092,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
     const int j0 = (int)(id % x.tiles) * 128, j1 = min(j0 + 128, x.TK);
     const int mine0 = j0 + 32 * wave, j = mine0 + (lane & 31);
     const bool valid = j < x.TK;
-    OwnRows<D, W, kWide> k, v;
+    OwnRows<D, W, kBy> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
     k.signs(x.scale < 0.0f);
     if constexpr (kK) v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
@@ -1098,7 +1116,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
     const int tiles = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = tiles * x.group;
     if (total > 0) {
         // tiles are loaded two ahead: what one tile takes to compute is less than a load takes
-        QueryStage<D, W, kWide, BQ, 256, kQuerySets<D, W>> stage;
+        QueryStage<D, W, kBy, BQ, 256, kQuerySets<D, W>> stage;
         stage.start(x);
         uint32_t by_row = lds_address(lds) + Tile::row_lane(lane), by_col = lds_address(lds) + Tile::column_lane(lane);
         uint32_t put_at = stage.q.lane(lds_address(lds));
@@ -1123,7 +1141,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
                 if (i < most && mine0 <= i + 31) {
                     // whole: every query of the tile sees every key of the wave
                     const bool whole = mine0 + 31 <= i && i + 32 <= least;
-                    add_queries<D, W, kWide, kK, kV>(x, by_row, by_col, kBytes, row, at, k, v, whole,
+                    add_queries<D, W, kBy, kK, kV>(x, by_row, by_col, kBytes, row, at, k, v, whole,
                                                      whole ? 0 : row_bits(j, until, i, h), lane, dk, dv);
                 }
             }
@@ -1176,8 +1194,8 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
     if constexpr (kK) fine = finite(dk);
     if constexpr (kV) fine = fine && finite(dv);
     if (valid) {
-        if constexpr (kK) store_own<D, kWide>(seq_row_out<D>(x.dk, n, j, kvh), dk, x.scale, x.dim_k, h);
-        if constexpr (kV) store_own<D, kWide>(seq_row_out<D>(x.dv, n, j, kvh), dv, kLess, x.dim_v, h);
+        if constexpr (kK) store_own<D, kBy>(seq_row_out<D>(x.dk, n, j, kvh), dk, x.scale, x.dim_k, h);
+        if constexpr (kV) store_own<D, kBy>(seq_row_out<D>(x.dv, n, j, kvh), dv, kLess, x.dim_v, h);
     }
     uint64_t again = __ballot(valid && !fine);
     for (again = (again | again >> 32) & 0xffffffffu; again != 0; again &= again - 1)
@@ -1187,7 +1205,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
 // What the queries of one chunk beyond its window give to 32 first steps of the
 // episode that the chunk begins in the middle of, summed over the heads that share
 // them: a quarter of the chunk to each wave, joined through LDS.
-template <class D, int W, bool kWide, bool kK, bool kV>
+template <class D, int W, int kBy, bool kK, bool kV>
 __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
@@ -1211,14 +1229,14 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
     if (i1 <= past || first / kFarChunk == c) return;  // (the whole block)
     const int s = 32 * part + (lane & 31), j = first + s;
     const bool valid = s < x.sinks && j < x.TK;
-    OwnRows<D, W, kWide> k, v;
+    OwnRows<D, W, kBy> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
     k.signs(x.scale < 0.0f);
     if constexpr (kK) v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
     const int begin = max(max(i0 + wave * kPart, past), first + 32 * part + x.window);
     const int end = min(min(i1, i0 + (wave + 1) * kPart), x.ends != nullptr ? x.ends[n * x.TK + first] : x.TK);
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
-    QueryStage<D, W, kWide, BQ, kWave> stage;
+    QueryStage<D, W, kBy, BQ, kWave> stage;
     stage.start(x);
     const uint32_t mine = lds_address(lds[wave]), by_row = mine + Tile::row_lane(lane);
     const uint32_t by_col = mine + Tile::column_lane(lane), put_at = stage.q.lane(mine);
@@ -1228,7 +1246,7 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
             stage.fetch(end - i);
             stage.put(put_at, kBytes, rows[wave]);
             __builtin_amdgcn_wave_barrier();
-            add_queries<D, W, kWide, kK, kV>(x, by_row, by_col, kBytes, rows[wave], 0, k, v, false,
+            add_queries<D, W, kBy, kK, kV>(x, by_row, by_col, kBytes, rows[wave], 0, k, v, false,
                                              valid ? row_bits(j + x.window, end, i, h) : 0, lane, dk, dv);
             __builtin_amdgcn_wave_barrier();
         }
@@ -1682,37 +1700,53 @@ inline uint64_t key_blocks(AttArgs& x)
     return (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.tiles;
 }
 
-// Whether the kernels may take rows by 16-byte units: dims of whole units of eight
-// elements, and a tile's rows within 32-bit offsets.
-inline bool all_wide(std::initializer_list<const SeqView*> views, int64_t dk, int64_t dv)
+// By how many elements at a time the kernels may take rows (8, 4 or 0): dims of whole
+// units, rows on as many, and a tile's rows (64) within 31-bit offsets.
+inline int rows_by(std::initializer_list<const SeqView*> views, int64_t dk, int64_t dv, int s)
 {
-    bool wide = dk % 8 == 0 && dv % 8 == 0;
-    for (const SeqView* v : views) wide = wide && v->vec == 16 && v->step < (int64_t(1) << 22);
-    return wide;
+    for (int by = s == 4 ? 4 : 8; by >= 4; by -= 4) {
+        bool ok = dk % by == 0 && dv % by == 0;
+        for (const SeqView* v : views) ok = ok && rows_on(*v, by, s) && v->step * s <= (int64_t(1) << 25);
+        if (ok) return by;
+    }
+    return 0;
 }
 
-template <class D, int W, bool kWide, bool kK, bool kV>
+// Calls f with W (64 or 128) and the rows' unit as constants.
+template <class D, class F>
+lrs_status with_sizes(int64_t dk, int64_t dv, int by, F f)
+{
+    using N = std::integral_constant<int, 64>;
+    using M = std::integral_constant<int, 128>;
+    const bool narrow = std::max(dk, dv) <= 64;
+    if constexpr (sizeof(D) == 2)
+        if (by == 8) return narrow ? f(N(), std::integral_constant<int, 8>()) : f(M(), std::integral_constant<int, 8>());
+    if (by == 4) return narrow ? f(N(), std::integral_constant<int, 4>()) : f(M(), std::integral_constant<int, 4>());
+    return narrow ? f(N(), std::integral_constant<int, 0>()) : f(M(), std::integral_constant<int, 0>());
+}
+
+template <class D, int W, int kBy, bool kK, bool kV>
 lrs_status launch_dkv(const char* nm, AttArgs x, hipStream_t stream)
 {
     if (x.far_part != nullptr) {
         const int64_t blocks = x.N * (x.H / x.group) * x.far_chunks * ((x.sinks + 31) / 32);
-        LRS_TRY(launch_seq(nm, attend_far<D, W, kWide, kK, kV>, (uint64_t)blocks, 256, stream, x));
+        LRS_TRY(launch_seq(nm, attend_far<D, W, kBy, kK, kV>, (uint64_t)blocks, 256, stream, x));
     }
     const uint64_t blocks = key_blocks(x);
-    return launch_seq(nm, attend_dkv<D, W, kWide, kK, kV>, blocks, 256, stream, x);
+    return launch_seq(nm, attend_dkv<D, W, kBy, kK, kV>, blocks, 256, stream, x);
 }
 
-template <class D, int W, bool kWide>
+template <class D, int W, int kBy>
 lrs_status launch_backward(const char* nm, AttArgs x, hipStream_t stream)
 {
     const uint64_t blocks = query_blocks(x);
-    if (x.sum_delta) LRS_TRY(launch_seq(nm, attend_dq<D, W, kWide, true>, blocks, 256, stream, x));
-    LRS_TRY(launch_seq(nm, attend_dq<D, W, kWide, false>, blocks, 256, stream, x));
+    if (x.sum_delta) LRS_TRY(launch_seq(nm, attend_dq<D, W, kBy, true>, blocks, 256, stream, x));
+    LRS_TRY(launch_seq(nm, attend_dq<D, W, kBy, false>, blocks, 256, stream, x));
     if constexpr (kSplitGrads<D, W>) {
-        LRS_TRY((launch_dkv<D, W, kWide, true, false>(nm, x, stream)));
-        return launch_dkv<D, W, kWide, false, true>(nm, x, stream);
+        LRS_TRY((launch_dkv<D, W, kBy, true, false>(nm, x, stream)));
+        return launch_dkv<D, W, kBy, false, true>(nm, x, stream);
     } else {
-        return launch_dkv<D, W, kWide, true, true>(nm, x, stream);
+        return launch_dkv<D, W, kBy, true, true>(nm, x, stream);
     }
 }
 
@@ -1749,10 +1783,9 @@ lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int
     const uint64_t blocks = query_blocks(x);
     LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N <= kMaxGrid / 2, "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[3], stream));
-    const bool narrow = std::max(dk, dv) <= 64, wide = all_wide({&x.q, &x.k, &x.v, &x.o}, dk, dv);
-    return launch_seq(nm, wide ? (narrow ? attend_forward<D, 64, true> : attend_forward<D, 128, true>)
-                               : (narrow ? attend_forward<D, 64, false> : attend_forward<D, 128, false>),
-                      blocks, 256, stream, x);
+    return with_sizes<D>(dk, dv, rows_by({&x.q, &x.k, &x.v, &x.o}, dk, dv, s), [&](auto w, auto by) {
+        return launch_seq(nm, attend_forward<D, decltype(w)::value, decltype(by)::value>, blocks, 256, stream, x);
+    });
 }
 
 template <class D>
@@ -1795,10 +1828,10 @@ lrs_status attention_backward_entry(const char* nm, int64_t N, int64_t T, int64_
     LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && (uint64_t)N <= kMaxGrid / 2,
                 "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[4], stream));
-    const bool wide = all_wide({&x.q, &x.k, &x.v, &x.o, &x.dout, &x.dq, &x.dk, &x.dv}, dk, dv);
-    if (std::max(dk, dv) <= 64)
-        return wide ? launch_backward<D, 64, true>(nm, x, stream) : launch_backward<D, 64, false>(nm, x, stream);
-    return wide ? launch_backward<D, 128, true>(nm, x, stream) : launch_backward<D, 128, false>(nm, x, stream);
+    const int unit = rows_by({&x.q, &x.k, &x.v, &x.o, &x.dout, &x.dq, &x.dk, &x.dv}, dk, dv, s);
+    return with_sizes<D>(dk, dv, unit, [&](auto w, auto by) {
+        return launch_backward<D, decltype(w)::value, decltype(by)::value>(nm, x, stream);
+    });
 }
 
 // The splits of a step's slots: as many as make four blocks for each of 256 CUs, of

@@ -205,6 +205,27 @@ struct TokenGrad {
     float from, a, b, hit;
 };
 
+// Where token `at` stands.  The host makes one row of the tokens (T = rows) where all
+// arrays allow it, and 32 bits do where there are as few: a division of 64 bits costs
+// a token of a few actions more than all of its logits do.
+struct Place {
+    int64_t n, t;
+
+    __device__ __forceinline__ Place(const PolicyArgs& x, int64_t at)
+    {
+        if (x.T == x.rows) {
+            n = 0;
+            t = at;
+        } else if (x.rows <= 0xffffffffll) {
+            n = (uint32_t)at / (uint32_t)x.T;
+            t = (uint32_t)at - (uint32_t)n * (uint32_t)x.T;
+        } else {
+            n = at / x.T;
+            t = at % x.T;
+        }
+    }
+};
+
 struct Token {
     int64_t n, t;
     int64_t action;
@@ -212,10 +233,10 @@ struct Token {
     float old_lp, adv, ref, weight;
 
     template <class D>
-    __device__ __forceinline__ void load(const PolicyArgs& x, int64_t at)
+    __device__ __forceinline__ void load(const PolicyArgs& x, const Place& at)
     {
-        n = at / x.T;
-        t = at % x.T;
+        n = at.n;
+        t = at.t;
         action = token<int64_t>(x.action, n, t);
         const bool in = (uint64_t)action < (uint64_t)x.V;
         // an action that is none makes the token NaN
@@ -319,10 +340,10 @@ __device__ __forceinline__ void clear_row(D* row, int V, int lane, int lanes)
 
 // A token that the mask leaves out: zeros for everything.
 template <class D, bool kGrad>
-__device__ __forceinline__ bool masked_out(const PolicyArgs& x, int64_t at, int lane, int lanes)
+__device__ __forceinline__ bool masked_out(const PolicyArgs& x, const Place& at, int lane, int lanes)
 {
     if (x.mask.p == nullptr) return false;
-    const int64_t n = at / x.T, t = at % x.T;
+    const int64_t n = at.n, t = at.t;
     if (token<uint8_t>(x.mask, n, t) != 0) return false;
     if (lane == 0) {
         Token k;
@@ -353,9 +374,10 @@ __global__ __launch_bounds__(L > kWave ? L : 256) void policy_rows(const PolicyA
     const int lane = threadIdx.x % L;
     const int64_t at = (int64_t)blockIdx.x * (kBlock / L) + threadIdx.x / L;
     if (at >= x.rows) return;  // L <= 64 only: nothing waits for these lanes
-    if (masked_out<D, kGrad>(x, at, lane, L)) return;
+    const Place place(x, at);
+    if (masked_out<D, kGrad>(x, place, lane, L)) return;
     Token k;
-    k.load<D>(x, at);
+    k.load<D>(x, place);
     const VocabRow<D> row(x.z, k.n, k.t, x.V);
     u32x4 w[U];
 #pragma unroll
@@ -411,9 +433,10 @@ __global__ __launch_bounds__(kStreamLanes) void policy_stream(const PolicyArgs x
     __shared__ float part[L / kWave];
     const int lane = threadIdx.x;
     const int64_t at = blockIdx.x;
-    if (masked_out<D, kGrad>(x, at, lane, L)) return;
+    const Place place(x, at);
+    if (masked_out<D, kGrad>(x, place, lane, L)) return;
     Token k;
-    k.load<D>(x, at);
+    k.load<D>(x, place);
     const VocabRow<D> row(x.z, k.n, k.t, x.V);
     float most = -INFINITY;
     RowSums s(most);
@@ -460,10 +483,11 @@ __global__ __launch_bounds__(256) void policy_backward(const PolicyArgs x)
 {
     const int lane = threadIdx.x % L;
     const int64_t part = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-    const int64_t at = part / x.splits;
-    const int split = (int)(part % x.splits);
+    const int64_t at = x.splits == 1 ? part : part / x.splits;
+    const int split = (int)(part - at * x.splits);
     if (at >= x.rows) return;
-    const int64_t n = at / x.T, t = at % x.T;
+    const Place place(x, at);
+    const int64_t n = place.n, t = place.t;
     D* const out = seq_row_out<D>(x.dz, n, t, 0);
     const bool off = x.mask.p != nullptr && token<uint8_t>(x.mask, n, t) == 0;
     if (off) {
@@ -471,7 +495,7 @@ __global__ __launch_bounds__(256) void policy_backward(const PolicyArgs x)
         return;
     }
     Token k;
-    k.load<D>(x, at);
+    k.load<D>(x, place);
     const VocabRow<D> row(x.z, n, t, x.V);
     const float lse = token<float>(x.lse, n, t), H = token_or(x.entropy, n, t, 0.0f);
     // p = e^{z' - lse}: z - lse / scale in float32, and what that leaves of lse as a factor
@@ -536,9 +560,21 @@ inline int64_t row_units(const SeqView& z, int64_t V)
     return rows_on(z, E, sizeof(D)) ? (V + E - 1) / E : (V + 2 * E - 2) / E;
 }
 
-template <class D, bool kGrad>
-lrs_status launch_policy(const char* nm, const PolicyArgs& x, hipStream_t stream)
+// One row of all tokens, where their places in every array are evenly spaced.
+inline void join_rows(PolicyArgs& x)
 {
+    if (x.T == x.rows) return;
+    const SeqView* const all[] = {&x.z, &x.dz, &x.action, &x.old_lp, &x.adv, &x.ref, &x.mask, &x.weight,
+                                  &x.loss, &x.lp, &x.entropy, &x.lse, &x.d_lp, &x.d_entropy};
+    for (const SeqView* v : all)
+        if (v->p != nullptr && v->env != x.T * v->step) return;
+    x.T = x.rows;
+}
+
+template <class D, bool kGrad>
+lrs_status launch_policy(const char* nm, PolicyArgs x, hipStream_t stream)
+{
+    join_rows(x);
     const int64_t units = row_units<D>(x.z, x.V);
     void (*kernel)(PolicyArgs) = policy_stream<D, kGrad>;
     int lanes = kStreamLanes;
@@ -556,8 +592,8 @@ lrs_status launch_policy(const char* nm, const PolicyArgs& x, hipStream_t stream
     LRS_POLICY(256, 64, 4)
     LRS_POLICY(1024, 256, 4)
     LRS_POLICY(2048, 256, 8)
-    LRS_POLICY(4096, 512, 8)
-    LRS_POLICY(8192, 1024, 8)
+    LRS_POLICY(4096, 256, 16)
+    LRS_POLICY(8192, 512, 16)
     LRS_POLICY(16384, 1024, 16) {}
 #undef LRS_POLICY
     const int block = lanes > kWave ? lanes : 256;
@@ -568,6 +604,7 @@ lrs_status launch_policy(const char* nm, const PolicyArgs& x, hipStream_t stream
 template <class D>
 lrs_status launch_policy_backward(const char* nm, PolicyArgs x, hipStream_t stream)
 {
+    join_rows(x);
     const int64_t units = row_units<D>(x.z, x.V);
     void (*kernel)(PolicyArgs) = policy_backward<D, 256>;
     int lanes = 256;

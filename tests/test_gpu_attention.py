@@ -48,6 +48,9 @@ CASES = [
     (3, 65, 8, 2, 64, 64, 0, 16, 33, 0.2),    # short episodes, more first steps than they have
     (1, 520, 1, 1, 64, 64, 0, 30, 70, None),  # first steps over more than a tile
     (1, 700, 2, 1, 128, 128, 3, 129, 4, 0.004),
+    (1, 150, 2, 1, 100, 100, 0, 60, 2, 0.02), # dims of whole fours
+    (2, 140, 1, 1, 12, 20, 5, 30, 0, None),
+    (1, 100, 3, 1, 68, 4, 0, 33, 1, 0.05),
     # first steps whose queries go on over chunks of 256 steps, with episodes across their borders
     (1, 1300, 2, 1, 64, 64, 0, 20, 4, 0.003),
     (2, 900, 1, 1, 32, 16, 300, 10, 64, 0.004),
