@@ -14,6 +14,8 @@ autograd.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import api as _api
@@ -98,6 +100,12 @@ def compute_windowed_attention_backward(grad_out, q, k, v, out, lse, *, window, 
     return dq.t, dk.t, dv.t
 
 
+@functools.lru_cache(maxsize=256)
+def _step_workspace(*sizes):
+    """Bytes of a step's workspace, which go by its sizes alone."""
+    return _api.load().lrs_windowed_attention_step_workspace_bytes(*sizes)
+
+
 def _cache(x, name, dtype, shape, device):
     x = _api._checked(x, name, dtype, shape, device)
     if not _in_place(x, (0, 1, 2)):
@@ -136,8 +144,7 @@ def compute_windowed_attention_step(q, k, v, key_cache, value_cache, positions, 
     vc = _cache(value_cache, "value_cache", dt, (n, slots, kv, dv), dev)
     pos = _positions(positions, (n,), dev)
     o = _seq_out(out, "out", dt, (n, h, dv), dev, axes)
-    ws = _workspace(_api.load().lrs_windowed_attention_step_workspace_bytes(n, h, kv, slots, int(sinks), dk, dv),
-                    dev)
+    ws = _workspace(_step_workspace(n, h, kv, slots, int(sinks), dk, dv), dev)
     _call("windowed_attention_step", sfx, dev, "compute_windowed_attention_step", n, h, kv, slots, int(sinks),
           dk, dv, _ptr(qs), _ptr(ks), _ptr(vs), _ptr(kc), _ptr(vc), _ptr(pos),
           float(dk) ** -0.5 if scale is None else float(scale), _ptr(o), _strides(qs, ks, vs, kc, vc, None, o),

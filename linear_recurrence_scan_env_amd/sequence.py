@@ -123,8 +123,9 @@ def _call(stem, sfx, device, what, *args):
     fn = _entries.get((stem, sfx))
     if fn is None:
         fn = _entries[stem, sfx] = getattr(_api.load(), f"lrs_{stem}_{sfx}")
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
+    # (torch.cuda.current_stream makes an object of what is one number: 2 us of a call's 15)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch._C._cuda_getDevice():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
