@@ -26,11 +26,6 @@
 
 #include "sequence.hpp"
 
-#ifndef LRS_KS
-#define LRS_KS 2
-#define LRS_GS 2
-#define LRS_GT 32
-#endif
 namespace lrs {
 
 constexpr int kMaxAttDim = 128;
@@ -686,21 +681,36 @@ __device__ __forceinline__ bool finite(const f32x16 (&acc)[kTiles])
 template <class D, int W>
 constexpr int kKeyTile = sizeof(D) == 4 ? 32 : 64;
 template <class D, int W>
-constexpr int kGradTile = W == 128 ? (sizeof(D) == 4 ? 32 : LRS_GT) : 64;
+constexpr int kGradTile = W == 128 ? 32 : 64;
 template <class D, int W>
-constexpr int kKeySets = sizeof(D) == 4 ? 1 : LRS_KS;
+constexpr int kKeySets = sizeof(D) == 4 ? 1 : 2;
 template <class D, int W>
-constexpr int kGradSets = sizeof(D) == 4 ? 1 : LRS_GS;
+constexpr int kGradSets = sizeof(D) == 4 ? 1 : 2;
 template <class D, int W>
 constexpr int kAttBlocks = sizeof(D) == 4 && W == 128 ? 1 : 2;  // blocks per CU
 
-// A block's place: its heads, and the steps of its four waves.
+// A block's place: its heads, and the steps of its four waves.  Alone: each wave has a
+// head and tiles of its own (rows of up to 32 steps, of which a block would use one
+// wave: 2930 x 2 steps of 9 heads, bf16, forward 258 us with blocks and 75 alone).
 struct AttBlock {
     int64_t n;
     int head, step0, first, last, kvh;
+    bool any;
 
-    __device__ __forceinline__ AttBlock(const AttArgs& x)
+    __device__ __forceinline__ AttBlock(const AttArgs& x, bool alone)
     {
+        any = true;
+        if (alone) {
+            const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+            any = id < x.N * x.H;
+            n = id / x.H;
+            head = (int)(id - n * x.H);
+            kvh = head / x.group;
+            step0 = 0;
+            first = x.TK - x.T;
+            last = x.TK - 1;
+            return;
+        }
         const uint32_t id = by_xcd(blockIdx.x, gridDim.x);
         const int hblocks = x.H / x.hpb, rows = 4 / x.hpb * 32;
         const uint32_t tile = id % x.tiles, hb = id / x.tiles % hblocks;
@@ -717,6 +727,32 @@ struct AttBlock {
 // Goes over the tiles of keys and values that a block's queries see: compute(by_row,
 // by_col, is_far, j0, j1) for each, with a lane's places in the keys' tile (the values'
 // lies kBytes behind).  kSets: how many tiles are on their way from memory.
+template <class D, int W, int BK, int kBy, class Compute>
+__device__ __forceinline__ void over_keys_alone(const AttArgs& x, const AttBlock& b, const KeyTiles& kt, char* lds,
+                                                int lane, Compute compute)
+{
+    using Tile = AttTile<D, W>;
+    AttStage<D, W, BK, kBy, kWave> sk, sv;
+    sk.start(x.k, x.dim_k);
+    sv.start(x.v, x.dim_v);
+    const uint32_t at = lds_address(lds), put_at = sk.lane(at);
+    for (int it = 0; it < kt.tiles; ++it) {
+        int j0, j1;
+        kt.get(it, BK, j0, j1);
+        if (it == 0 || it == kt.far_tiles) {
+            sk.place(x.k, b.n, b.kvh, j0);
+            sv.place(x.v, b.n, b.kvh, j0);
+        }
+        sk.fetch(j1 - j0);
+        sv.fetch(j1 - j0);
+        sk.put(put_at);
+        sv.put(put_at + BK * Tile::kRow);
+        __builtin_amdgcn_wave_barrier();
+        compute(at + Tile::row_lane(lane), at + Tile::column_lane(lane), it < kt.far_tiles, j0, j1);
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 template <class D, int W, int BK, int kBy, int kSets, class Compute>
 __device__ __forceinline__ void over_keys(const AttArgs& x, const AttBlock& b, const KeyTiles& kt, char* lds, int lane,
                                           Compute compute)
@@ -774,14 +810,15 @@ __device__ __forceinline__ void over_keys(const AttArgs& x, const AttBlock& b, c
     }
 }
 
-template <class D, int W, int kBy>
+template <class D, int W, int kBy, bool kAlone>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
-    constexpr int BK = kKeyTile<D, W>, kBytes = BK * Tile::kRow, S = BK / 32;
-    __shared__ alignas(1024) char lds[2][2][kBytes];
+    constexpr int BK = kAlone ? 32 : kKeyTile<D, W>, kBytes = BK * Tile::kRow, S = BK / 32;
+    __shared__ alignas(1024) char lds[kAlone ? 4 : 2][2][kBytes];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
-    const AttBlock b(x);
+    const AttBlock b(x, kAlone);
+    if (kAlone && !b.any) return;
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
     const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
     OwnRows<D, W, kBy> q;
@@ -790,8 +827,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
 
     f32x16 o[W / 32] = {};
     float m = -INFINITY, l = 0.0f;  // m: the largest score; l: this half's sum
-    over_keys<D, W, BK, kBy, kKeySets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
-                                                                              bool is_far, int j0, int j1) {
+    auto compute = [&](uint32_t by_row, uint32_t by_col, bool is_far, int j0, int j1) {
         if (!wq.touches(kt, is_far, j0, j1)) return;
         f32x16 s[S] = {};
 #pragma unroll
@@ -836,7 +872,11 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
                 for (int dt = 0; dt < W / 32; ++dt)
                     o[dt] = mma32<D>(Tile::columns(by_col + kBytes, 32 * a + 16 * u, 32 * dt), p, o[dt]);
             }
-    });
+    };
+    if constexpr (kAlone)
+        over_keys_alone<D, W, BK, kBy>(x, b, kt, lds[__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)][0], lane,
+                                       compute);
+    else over_keys<D, W, BK, kBy, kKeySets<D, W>>(x, b, kt, lds[0][0], lane, compute);
     if (!wq.any()) return;
     l += __shfl_xor(l, 32);
     const float by = 1.0f / l, lse = (m * x.c + __builtin_amdgcn_logf(l)) * kAttLn2;
@@ -852,14 +892,15 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
 }
 
 // kSum: the pass before, for short windows, which only sums D as sum_j p_ij do_i . v_j.
-template <class D, int W, int kBy, bool kSum>
+template <class D, int W, int kBy, bool kSum, bool kAlone>
 __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
-    constexpr int BK = kGradTile<D, W>, kBytes = BK * Tile::kRow;
-    __shared__ alignas(1024) char lds[2][2][kBytes];
+    constexpr int BK = kAlone ? 32 : kGradTile<D, W>, kBytes = BK * Tile::kRow;
+    __shared__ alignas(1024) char lds[kAlone ? 4 : 2][2][kBytes];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
-    const AttBlock b(x);
+    const AttBlock b(x, kAlone);
+    if (kAlone && !b.any) return;
     const KeyTiles kt(x, b.n, b.first, b.last, BK);
     const WaveQueries wq(x, b.n, b.step0, kt.near, lane);
     const int t = wq.i - (x.TK - x.T);
@@ -879,8 +920,7 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
 
     f32x16 dq[W / 32] = {};
     float sum = 0.0f;
-    over_keys<D, W, BK, kBy, kGradSets<D, W>>(x, b, kt, lds[0][0], lane, [&](uint32_t by_row, uint32_t by_col,
-                                                                               bool is_far, int j0, int j1) {
+    auto compute = [&](uint32_t by_row, uint32_t by_col, bool is_far, int j0, int j1) {
 #pragma unroll
         for (int at = 0; at < BK; at += 32) {
             const int ja = j0 + at, jb = min(ja + 32, j1);
@@ -910,7 +950,11 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
                 }
             }
         }
-    });
+    };
+    if constexpr (kAlone)
+        over_keys_alone<D, W, BK, kBy>(x, b, kt, lds[__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)][0], lane,
+                                       compute);
+    else over_keys<D, W, BK, kBy, kGradSets<D, W>>(x, b, kt, lds[0][0], lane, compute);
     if constexpr (kSum) {
         sum += __shfl_xor(sum, 32);
         if (wq.valid && h == 0) *delta_at = sum;
@@ -1075,22 +1119,24 @@ __device__ __forceinline__ int seen_until(const AttArgs& x, int64_t n, int j)
     return min(until, end);
 }
 
-template <class D, int W, int kBy, bool kK, bool kV>
+// Alone: rows of up to 32 keys, each wave with a head of its own.
+template <class D, int W, int kBy, bool kK, bool kV, bool kAlone>
 __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void attend_dkv(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
-    constexpr int BQ = kQueryTile<D, W>;
+    constexpr int BQ = kAlone ? 32 : kQueryTile<D, W>;
     constexpr int kBytes = BQ * Tile::kRow;
-    __shared__ alignas(1024) char lds[2][2][kBytes];
-    __shared__ QueryRows<BQ> rows[2];
+    __shared__ alignas(1024) char lds[kAlone ? 4 : 2][2][kBytes];
+    __shared__ QueryRows<BQ> rows[kAlone ? 4 : 2];
     const int lane = threadIdx.x % kWave, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int past = x.TK - x.T, kv = x.H / x.group;
-    const uint32_t id = by_xcd(blockIdx.x, gridDim.x);
-    const int kvh = id / x.tiles % kv;
-    const int64_t n = id / x.tiles / kv;
-    const int j0 = (int)(id % x.tiles) * 128, j1 = min(j0 + 128, x.TK);
-    const int mine0 = j0 + 32 * wave, j = mine0 + (lane & 31);
+    const int64_t id = kAlone ? (int64_t)blockIdx.x * 4 + wave : (int64_t)by_xcd(blockIdx.x, gridDim.x);
+    const int64_t row_of = kAlone ? id : id / x.tiles, n = row_of / kv;
+    const int kvh = (int)(row_of - n * kv);
+    if (kAlone && n >= x.N) return;
+    const int j0 = kAlone ? 0 : (int)(id - row_of * x.tiles) * 128, j1 = min(j0 + 128, x.TK);
+    const int mine0 = kAlone ? 0 : j0 + 32 * wave, j = mine0 + (lane & 31);
     const bool valid = j < x.TK;
     OwnRows<D, W, kBy> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
@@ -1114,7 +1160,22 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
 
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
     const int tiles = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = tiles * x.group;
-    if (total > 0) {
+    if constexpr (kAlone) {
+        QueryStage<D, W, kBy, BQ, kWave> stage;
+        stage.start(x);
+        const uint32_t at = lds_address(lds[wave]), put_at = stage.q.lane(at);
+        for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head) {
+            if (begin < end) stage.place(x, n, head, begin - past);
+            for (int i = begin; i < end; i += BQ) {
+                stage.fetch(end - i);
+                stage.put(put_at, kBytes, rows[wave]);
+                __builtin_amdgcn_wave_barrier();
+                add_queries<D, W, kBy, kK, kV>(x, at + Tile::row_lane(lane), at + Tile::column_lane(lane), kBytes,
+                                               rows[wave], 0, k, v, false, row_bits(j, until, i, h), lane, dk, dv);
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    } else if (total > 0) {
         // tiles are loaded two ahead: what one tile takes to compute is less than a load takes
         QueryStage<D, W, kBy, BQ, 256, kQuerySets<D, W>> stage;
         stage.start(x);
@@ -1687,15 +1748,21 @@ inline lrs_status launch_starts(const char* nm, const AttArgs& x, const SeqView&
 
 constexpr uint64_t kMaxGrid = 0x7fffffffull;
 
+// Whether there are waves enough for the chip with a head to each.
+inline bool queries_alone(const AttArgs& x) { return x.T <= 32 && x.hpb < 4 && x.N * x.H >= 2048; }
+inline bool keys_alone(const AttArgs& x) { return x.TK <= 32 && x.N * (x.H / x.group) >= 2048; }
+
 // Blocks of the forward and of dq: 128 queries of hpb heads.
 inline uint64_t query_blocks(AttArgs& x)
 {
+    if (queries_alone(x)) return ((uint64_t)x.N * (uint64_t)x.H + 3) / 4;
     const int rows = 4 / x.hpb * 32;
     x.tiles = (x.T + rows - 1) / rows;
     return (uint64_t)x.N * (uint64_t)(x.H / x.hpb) * (uint64_t)x.tiles;
 }
 inline uint64_t key_blocks(AttArgs& x)
 {
+    if (keys_alone(x)) return ((uint64_t)x.N * (uint64_t)(x.H / x.group) + 3) / 4;
     x.tiles = (x.TK + 127) / 128;
     return (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.tiles;
 }
@@ -1733,15 +1800,20 @@ lrs_status launch_dkv(const char* nm, AttArgs x, hipStream_t stream)
         LRS_TRY(launch_seq(nm, attend_far<D, W, kBy, kK, kV>, (uint64_t)blocks, 256, stream, x));
     }
     const uint64_t blocks = key_blocks(x);
-    return launch_seq(nm, attend_dkv<D, W, kBy, kK, kV>, blocks, 256, stream, x);
+    return launch_seq(nm, keys_alone(x) ? attend_dkv<D, W, kBy, kK, kV, true> : attend_dkv<D, W, kBy, kK, kV, false>,
+                      blocks, 256, stream, x);
 }
 
 template <class D, int W, int kBy>
 lrs_status launch_backward(const char* nm, AttArgs x, hipStream_t stream)
 {
     const uint64_t blocks = query_blocks(x);
-    if (x.sum_delta) LRS_TRY(launch_seq(nm, attend_dq<D, W, kBy, true>, blocks, 256, stream, x));
-    LRS_TRY(launch_seq(nm, attend_dq<D, W, kBy, false>, blocks, 256, stream, x));
+    const bool alone = queries_alone(x);
+    if (x.sum_delta)
+        LRS_TRY(launch_seq(nm, alone ? attend_dq<D, W, kBy, true, true> : attend_dq<D, W, kBy, true, false>, blocks, 256,
+                           stream, x));
+    LRS_TRY(launch_seq(nm, alone ? attend_dq<D, W, kBy, false, true> : attend_dq<D, W, kBy, false, false>, blocks, 256,
+                       stream, x));
     if constexpr (kSplitGrads<D, W>) {
         LRS_TRY((launch_dkv<D, W, kBy, true, false>(nm, x, stream)));
         return launch_dkv<D, W, kBy, false, true>(nm, x, stream);
@@ -1784,7 +1856,9 @@ lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int
     LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N <= kMaxGrid / 2, "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[3], stream));
     return with_sizes<D>(dk, dv, rows_by({&x.q, &x.k, &x.v, &x.o}, dk, dv, s), [&](auto w, auto by) {
-        return launch_seq(nm, attend_forward<D, decltype(w)::value, decltype(by)::value>, blocks, 256, stream, x);
+        constexpr int W = decltype(w)::value, B = decltype(by)::value;
+        return launch_seq(nm, queries_alone(x) ? attend_forward<D, W, B, true> : attend_forward<D, W, B, false>, blocks,
+                          256, stream, x);
     });
 }
 

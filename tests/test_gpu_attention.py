@@ -68,6 +68,17 @@ def test_against_definition(dt, case):
     compare(got, ref.attention(q, k, v, window, sinks, reset, do=do))
 
 
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("case", [(2100, 1, 1, 1, 16, 16, 0, 5, 0, None), (700, 2, 3, 3, 64, 64, 0, 2, 1, 0.3),
+                                  (350, 32, 6, 2, 32, 64, 0, 7, 2, 0.1), (1030, 3, 2, 1, 100, 72, 30, 20, 3, 0.05),
+                                  (2049, 31, 1, 1, 128, 96, 0, 31, 40, 0.02)], ids=lambda c: "-".join(map(str, c)))
+def test_many_short_rows(dt, case):
+    n, t, heads, kv, dk, dv, past, window, sinks, reset_p = case
+    q, k, v, do, reset = inputs(15, dt, n, t, heads, kv, dk, dv, past, reset_p)
+    got = run_all(q, k, v, do, window=window, sinks=sinks, reset=reset)
+    compare(got, ref.attention(q, k, v, window, sinks, reset, do=do))
+
+
 @pytest.mark.parametrize("begins", [[250, 330], [255], [256], [257, 511, 512], [200, 300], [192, 700]])
 @pytest.mark.parametrize("window,sinks", [(7, 33), (100, 64), (300, 3)])
 def test_first_steps_around_chunks(begins, window, sinks):
