@@ -834,12 +834,21 @@ lrs_status lrs_qk_norm_rotation_backward_f16(int64_t num_envs, int64_t seq_len, 
  *     stride is ignored; lse's elements are rows of one).  Strides, bases and
  *     dims that keep every row on 16 bytes are fastest.
  *   - key_dim and value_dim 1 to 128; heads a multiple of kv_heads, at most
- *     65536; window at least 1, sinks 0 or more, any size; scale finite, not 0.
+ *     65536; key_steps and slots at most 2^29; window at least 1, sinks 0 or
+ *     more, any size; scale finite, not 0.  A call works on fewer than 2^24
+ *     blocks, of 128 query steps (128 / heads per block for shared key heads) or
+ *     128 key steps of a head each, or of four heads with up to 32 steps; more is
+ *     refused, and so are resets of more than 2^23 - 1 environments.
  *   - What a query does not see has no part in its result, NaN and infinities
  *     included; what it sees is computed as written.
- *   - Softmax sums are fp32.  In the 16-bit variants weights and their
- *     gradients are rounded to the type before they multiply rows.  A call gives
- *     the same bits every time.
+ *   - Softmax sums are fp32.  In the 16-bit variants weights are rounded to the
+ *     type before they multiply rows, and the gradients of scores go into their
+ *     products as two values of it, the second what the first left.  In float16
+ *     those below 2^-14 keep fewer bits (steps of 2^-24), as everything of that
+ *     type: gradients that small want a loss scale.  A call gives the same bits
+ *     every time.
+ *   - A result that comes out as infinity or NaN is computed again one key at a
+ *     time, to leave out what is not seen: slow where there are many.
  *   - workspace: lrs_windowed_attention_workspace_bytes(...) bytes, 16-byte
  *     aligned, any contents; NULL with 0 bytes where that is 0.  Nothing in it
  *     outlives the call's kernels.

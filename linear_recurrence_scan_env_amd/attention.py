@@ -163,9 +163,8 @@ def compute_windowed_attention_fill(k, v, key_cache, value_cache, positions, *, 
     last step's position says: that step and those before it, as many as there
     are, go into their slots.  Slots whose steps lie before the row stay as they
     are, and so do all of a row whose last position is negative."""
-    _need_tensor(k, "k", 4)
-    _need_tensor(v, "v", 4)
-    _need_tensor(key_cache, "key_cache", 4)
+    for x, name in ((k, "k"), (v, "v"), (key_cache, "key_cache"), (value_cache, "value_cache")):
+        _need_tensor(x, name, 4)
     env, step = (1, 0) if time_major else (0, 1)
     sfx, dt, dev = _api._suffix(k, "k"), k.dtype, _gpu(k, "k")
     lead, n, t = tuple(k.shape[:2]), k.shape[env], k.shape[step]
@@ -201,6 +200,8 @@ class _WindowedAttention(torch.autograd.Function):
 
 def windowed_attention(q, k, v, *, window, sinks=0, reset=None, scale=None, time_major=False):
     """compute_windowed_attention for autograd: differentiable in q, k and v;
-    returns out."""
+    returns out.  To capture both directions into a graph, call the compute_
+    functions, or first drop every eager result of the same leaves: torch does
+    not capture a backward pass beside those."""
     return _WindowedAttention.apply(q, k, v, reset, dict(window=window, sinks=sinks, scale=scale,
                                                          time_major=time_major))

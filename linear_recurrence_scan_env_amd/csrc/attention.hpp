@@ -29,6 +29,7 @@
 namespace lrs {
 
 constexpr int kMaxAttDim = 128;
+constexpr int64_t kMaxKeySteps = int64_t(1) << 29;  // a step and a window, or a slot and a block's, in 32 bits
 constexpr float kAttLog2e = 1.44269504088896341f;
 constexpr float kAttLn2 = 0.693147180559945309f;
 
@@ -82,7 +83,7 @@ __device__ __forceinline__ f32x16 mma32(const AFrag<D>& a, const AFrag<D>& b, f3
 __device__ __forceinline__ constexpr int acc_row(int r, int h) { return 8 * (r / 4) + 4 * h + r % 4; }
 
 // Registers 8u .. 8u + 7 as an operand: 16-bit types round the weights here, once
-// (to 2^-9 or 2^-12 of each; they are summed in float32 before that).
+// (by 2^-8 or 2^-11 of each at most; they are summed in float32 before that).
 template <class D>
 __device__ __forceinline__ AFrag<D> operand(const f32x16& v, int u)
 {
@@ -1094,17 +1095,15 @@ __device__ __forceinline__ float* far_sums(const AttArgs& x, int64_t row, int ch
     return x.far_part + ((row * x.far_chunks + chunk) * x.sinks + s) * (2 * W);
 }
 
-// Keys are the columns: a wave holds 32 of them and their values, a block 128;
-// queries and their gradients come in tiles of 32, head after head of the group.
-// Rows of more than 128 bytes take a kernel for the gradient of the keys (kK) and one
-// for that of the values (kV): together they need more registers than two waves on a
-// SIMD have, and one wave alone waits through its softmax.
+// Queries in a tile of attend_dkv, and tiles on their way from memory.
 template <class D, int W>
 constexpr int kQueryTile = W == 128 || sizeof(D) == 2 ? 32 : 64;
-
 template <class D, int W>
 constexpr int kQuerySets = sizeof(D) == 4 ? 1 : 2;
 
+// Rows of more than 128 bytes take a kernel for the gradient of the keys (kK) and one
+// for that of the values (kV): together they need more registers than two waves on a
+// SIMD have, and one wave alone waits through its softmax.
 template <class D, int W>
 constexpr bool kSplitGrads = W * (int)sizeof(D) > 128;
 
@@ -1119,7 +1118,9 @@ __device__ __forceinline__ int seen_until(const AttArgs& x, int64_t n, int j)
     return min(until, end);
 }
 
-// Alone: rows of up to 32 keys, each wave with a head of its own.
+// Keys are the columns: a wave holds 32 of them and their values, a block 128;
+// queries and their gradients come in tiles, head after head of the group.  Alone:
+// rows of up to 32 keys, each wave with a head of its own.
 template <class D, int W, int kBy, bool kK, bool kV, bool kAlone>
 __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void attend_dkv(const AttArgs x)
 {
@@ -1629,25 +1630,25 @@ struct AttFillArgs {
 template <class D>
 __global__ __launch_bounds__(256) void fill_slots(const AttFillArgs x, const uint32_t wide)
 {
-    const int slots = x.sinks + x.window, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const int64_t at = (int64_t)blockIdx.x * 4 + wave;
-    if (at >= x.N * slots) return;
-    const int64_t n = at / slots;
-    const int slot = (int)(at % slots);
-    const int64_t last = *seq_row<int32_t>(x.positions, n, x.T - 1, 0);
-    int64_t p = slot;
-    if (slot >= x.sinks && last >= slot) p = slot + (last - slot) / x.window * x.window;
-    const int64_t t = x.T - 1 - (last - p);
-    if (p > last || t < 0) return;
     constexpr int E = 16 / (int)sizeof(D);
+    const int slots = x.sinks + x.window, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int uk = (x.dim_k + E - 1) / E, uv = (x.dim_v + E - 1) / E;
-    for (int a = lane; a < x.KV * (uk + uv); a += kWave) {
-        const bool key = a < x.KV * uk;
-        const int b = key ? a : a - x.KV * uk, u = key ? uk : uv, h = b / u, c = b % u * E;
-        const int dim = key ? x.dim_k : x.dim_v;
-        const SeqView &from = key ? x.k : x.v, &to = key ? x.kc : x.vc;
-        store_row_unit<D>(seq_row_out<D>(to, n, slot, h), c, dim, wide,
-                          load_unit<D>(seq_row<D>(from, n, t, h), c, dim, wide));
+    for (int64_t at = (int64_t)blockIdx.x * 4 + wave; at < x.N * slots; at += (int64_t)gridDim.x * 4) {
+        const int64_t n = at / slots;
+        const int slot = (int)(at % slots);
+        const int64_t last = *seq_row<int32_t>(x.positions, n, x.T - 1, 0);
+        int64_t p = slot;
+        if (slot >= x.sinks && last >= slot) p = slot + (last - slot) / x.window * x.window;
+        const int64_t t = x.T - 1 - (last - p);
+        if (p > last || t < 0) continue;
+        for (int a = lane; a < x.KV * (uk + uv); a += kWave) {
+            const bool key = a < x.KV * uk;
+            const int b = key ? a : a - x.KV * uk, u = key ? uk : uv, h = b / u, c = b % u * E;
+            const int dim = key ? x.dim_k : x.dim_v;
+            const SeqView &from = key ? x.k : x.v, &to = key ? x.kc : x.vc;
+            store_row_unit<D>(seq_row_out<D>(to, n, slot, h), c, dim, wide,
+                              load_unit<D>(seq_row<D>(from, n, t, h), c, dim, wide));
+        }
     }
 }
 
@@ -1663,7 +1664,8 @@ inline lrs_status check_attention(const char* nm, int64_t N, int64_t T, int64_t 
                                   int64_t dk, int64_t dv, int64_t window, int64_t sinks, float scale)
 {
     LRS_TRY(check_common(nm, N, T));
-    LRS_REQUIRE(TK >= T && valid_sizes(N, TK), "%s: key_steps must be at least query_steps, and within their limits", nm);
+    LRS_REQUIRE(TK >= T && TK <= kMaxKeySteps && valid_sizes(N, TK),
+                "%s: key_steps must be at least query_steps and at most 2^29, and num_envs * key_steps < 2^34", nm);
     LRS_REQUIRE(KV >= 1 && H >= 1 && H <= 65536 && H % KV == 0,
                 "%s: heads must be a multiple of kv_heads and 1 to 65536 (got %lld and %lld)", nm, (long long)H,
                 (long long)KV);
@@ -1746,7 +1748,8 @@ inline lrs_status launch_starts(const char* nm, const AttArgs& x, const SeqView&
                       const_cast<int32_t*>(x.starts), const_cast<int32_t*>(x.ends));
 }
 
-constexpr uint64_t kMaxGrid = 0x7fffffffull;
+// Blocks of 256 threads: a grid holds fewer than 2^32.
+constexpr uint64_t kMaxGrid = 0xffffff;
 
 // Whether there are waves enough for the chip with a head to each.
 inline bool queries_alone(const AttArgs& x) { return x.T <= 32 && x.hpb < 4 && x.N * x.H >= 2048; }
@@ -1765,6 +1768,12 @@ inline uint64_t key_blocks(AttArgs& x)
     if (keys_alone(x)) return ((uint64_t)x.N * (uint64_t)(x.H / x.group) + 3) / 4;
     x.tiles = (x.TK + 127) / 128;
     return (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.tiles;
+}
+
+// Blocks of attend_far.
+inline uint64_t far_blocks(const AttArgs& x)
+{
+    return (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.far_chunks * (uint64_t)((x.sinks + 31) / 32);
 }
 
 // By how many elements at a time the kernels may take rows (8, 4 or 0): dims of whole
@@ -1795,10 +1804,8 @@ lrs_status with_sizes(int64_t dk, int64_t dv, int by, F f)
 template <class D, int W, int kBy, bool kK, bool kV>
 lrs_status launch_dkv(const char* nm, AttArgs x, hipStream_t stream)
 {
-    if (x.far_part != nullptr) {
-        const int64_t blocks = x.N * (x.H / x.group) * x.far_chunks * ((x.sinks + 31) / 32);
-        LRS_TRY(launch_seq(nm, attend_far<D, W, kBy, kK, kV>, (uint64_t)blocks, 256, stream, x));
-    }
+    if (x.far_part != nullptr)
+        LRS_TRY(launch_seq(nm, attend_far<D, W, kBy, kK, kV>, far_blocks(x), 256, stream, x));
     const uint64_t blocks = key_blocks(x);
     return launch_seq(nm, keys_alone(x) ? attend_dkv<D, W, kBy, kK, kV, true> : attend_dkv<D, W, kBy, kK, kV, false>,
                       blocks, 256, stream, x);
@@ -1853,7 +1860,7 @@ lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int
     set_vec(x.v, dv, s);
     set_vec(x.o, dv, s);
     const uint64_t blocks = query_blocks(x);
-    LRS_REQUIRE(blocks <= kMaxGrid && (uint64_t)N <= kMaxGrid / 2, "%s: num_envs * heads * steps is too large", nm);
+    LRS_REQUIRE(blocks <= kMaxGrid && (reset == nullptr || (uint64_t)N <= kMaxGrid), "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[3], stream));
     return with_sizes<D>(dk, dv, rows_by({&x.q, &x.k, &x.v, &x.o}, dk, dv, s), [&](auto w, auto by) {
         constexpr int W = decltype(w)::value, B = decltype(by)::value;
@@ -1899,7 +1906,8 @@ lrs_status attention_backward_entry(const char* nm, int64_t N, int64_t T, int64_
     x.dv = a[9];
     for (SeqView* w : {&x.q, &x.k, &x.dq, &x.dk}) set_vec(*w, dk, s);
     for (SeqView* w : {&x.v, &x.o, &x.dout, &x.dv}) set_vec(*w, dv, s);
-    LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && (uint64_t)N <= kMaxGrid / 2,
+    LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && far_blocks(x) <= kMaxGrid &&
+                    (reset == nullptr || (uint64_t)N <= kMaxGrid / 2),
                 "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[4], stream));
     const int unit = rows_by({&x.q, &x.k, &x.v, &x.o, &x.dout, &x.dq, &x.dk, &x.dv}, dk, dv, s);
@@ -1926,7 +1934,7 @@ inline bool fill_step(AttStepArgs& x, int64_t N, int64_t H, int64_t KV, int64_t 
                       int64_t dv)
 {
     if (N < 1 || N > (int64_t(1) << 31) || !att_sizes_ok(H, KV, dk, dv) || sinks < 0 || slots <= sinks ||
-        slots >= (int64_t(1) << 31))
+        slots > kMaxKeySteps)
         return false;
     x.KV = (int32_t)KV;
     x.group = (int32_t)(H / KV);
@@ -1962,7 +1970,7 @@ lrs_status attention_step_entry(const char* nm, int64_t N, int64_t H, int64_t KV
                                 D* value_cache, const int32_t* positions, float scale, D* out,
                                 const int64_t* strides, void* ws, size_t ws_bytes, hipStream_t stream)
 {
-    LRS_REQUIRE(slots >= 1 && slots < (int64_t(1) << 31), "%s: slots must be 1 to 2^31 - 1 (got %lld)", nm,
+    LRS_REQUIRE(slots >= 1 && slots <= kMaxKeySteps, "%s: slots must be 1 to 2^29 (got %lld)", nm,
                 (long long)slots);
     LRS_TRY(check_attention(nm, N, 1, 1, H, KV, dk, dv, slots - sinks, sinks, scale));
     constexpr int s = sizeof(D);
@@ -2006,7 +2014,7 @@ lrs_status attention_fill_entry(const char* nm, int64_t N, int64_t T, int64_t KV
                                 int64_t dk, int64_t dv, const D* k, const D* v, const int32_t* positions,
                                 D* key_cache, D* value_cache, const int64_t* strides, hipStream_t stream)
 {
-    LRS_REQUIRE(slots >= 1 && slots < (int64_t(1) << 31), "%s: slots must be 1 to 2^31 - 1 (got %lld)", nm,
+    LRS_REQUIRE(slots >= 1 && slots <= kMaxKeySteps, "%s: slots must be 1 to 2^29 (got %lld)", nm,
                 (long long)slots);
     LRS_TRY(check_attention(nm, N, T, T, KV, KV, dk, dv, slots - sinks, sinks, 1.0f));
     constexpr int s = sizeof(D);
@@ -2022,8 +2030,8 @@ lrs_status attention_fill_entry(const char* nm, int64_t N, int64_t T, int64_t KV
     constexpr int E = 16 / s;
     const bool wide = dk % E == 0 && dv % E == 0 && rows_on(a[0], E, s) && rows_on(a[1], E, s) &&
                       rows_on(a[3], E, s) && rows_on(a[4], E, s);
-    const uint64_t blocks = ((uint64_t)N * slots + 3) / 4;
-    LRS_REQUIRE(blocks <= kMaxGrid, "%s: num_envs * slots is too large", nm);
+    LRS_REQUIRE((uint64_t)N < (uint64_t(1) << 62) / slots, "%s: num_envs * slots is too large", nm);
+    const uint64_t blocks = std::min<uint64_t>(((uint64_t)N * slots + 3) / 4, kMaxGrid);
     return launch_seq(nm, fill_slots<D>, blocks, 256, stream, x, (uint32_t)wide);
 }
 

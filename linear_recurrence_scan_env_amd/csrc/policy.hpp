@@ -307,6 +307,19 @@ __device__ __forceinline__ void grad_unit(const PolicyArgs& x, const u32x4& w, i
 
 // ------------------------------------------------------------------- kernels
 
+// Blocks lie in rows of kGridRow: a grid's axis holds fewer than 2^32 threads, which
+// 2^30 tokens of a few actions exceed.
+constexpr uint64_t kGridRow = uint64_t(1) << 20;
+__device__ __forceinline__ int64_t grid_block() { return (int64_t)blockIdx.y * kGridRow + blockIdx.x; }
+
+inline lrs_status launch_tokens(const char* nm, void (*kernel)(PolicyArgs), uint64_t blocks, int threads,
+                                hipStream_t stream, PolicyArgs x)
+{
+    const uint64_t rows = (blocks + kGridRow - 1) / kGridRow;
+    LRS_REQUIRE(rows <= 65535, "%s: tokens * actions is too large", nm);
+    return launch_seq(nm, kernel, dim3((uint32_t)std::min(blocks, kGridRow), (uint32_t)rows), threads, stream, x);
+}
+
 __device__ __forceinline__ void put_token(const SeqView& v, const Token& k, float value)
 {
     if (v.p != nullptr) *seq_row_out<float>(v, k.n, k.t, 0) = value;
@@ -372,8 +385,8 @@ __global__ __launch_bounds__(L > kWave ? L : 256) void policy_rows(const PolicyA
     constexpr int kBlock = L > kWave ? L : 256;
     __shared__ float part[L > kWave ? L / kWave : 1];
     const int lane = threadIdx.x % L;
-    const int64_t at = (int64_t)blockIdx.x * (kBlock / L) + threadIdx.x / L;
-    if (at >= x.rows) return;  // L <= 64 only: nothing waits for these lanes
+    const int64_t at = grid_block() * (kBlock / L) + threadIdx.x / L;
+    if (at >= x.rows) return;  // whole blocks, or (L <= 64) lanes that nothing waits for
     const Place place(x, at);
     if (masked_out<D, kGrad>(x, place, lane, L)) return;
     Token k;
@@ -432,7 +445,8 @@ __global__ __launch_bounds__(kStreamLanes) void policy_stream(const PolicyArgs x
     constexpr int L = kStreamLanes, U = 4, E = kUnitElems<D>;
     __shared__ float part[L / kWave];
     const int lane = threadIdx.x;
-    const int64_t at = blockIdx.x;
+    const int64_t at = grid_block();
+    if (at >= x.rows) return;
     const Place place(x, at);
     if (masked_out<D, kGrad>(x, place, lane, L)) return;
     Token k;
@@ -482,7 +496,7 @@ template <class D, int L>
 __global__ __launch_bounds__(256) void policy_backward(const PolicyArgs x)
 {
     const int lane = threadIdx.x % L;
-    const int64_t part = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int64_t part = grid_block() * (256 / L) + threadIdx.x / L;
     const int64_t at = x.splits == 1 ? part : part / x.splits;
     const int split = (int)(part - at * x.splits);
     if (at >= x.rows) return;
@@ -598,7 +612,7 @@ lrs_status launch_policy(const char* nm, PolicyArgs x, hipStream_t stream)
 #undef LRS_POLICY
     const int block = lanes > kWave ? lanes : 256;
     const int64_t per = block / lanes;
-    return launch_seq(nm, kernel, (uint64_t)((x.rows + per - 1) / per), block, stream, x);
+    return launch_tokens(nm, kernel, (uint64_t)((x.rows + per - 1) / per), block, stream, x);
 }
 
 template <class D>
@@ -614,7 +628,7 @@ lrs_status launch_policy_backward(const char* nm, PolicyArgs x, hipStream_t stre
     // four units to a lane
     x.splits = lanes < 256 ? 1 : (int32_t)((units + 1023) / 1024);
     const int64_t per = 256 / lanes;
-    return launch_seq(nm, kernel, (uint64_t)((x.rows * x.splits + per - 1) / per), 256, stream, x);
+    return launch_tokens(nm, kernel, (uint64_t)((x.rows * x.splits + per - 1) / per), 256, stream, x);
 }
 
 // What the calls share: sizes and coefficients checked, and put where the kernels read them.

@@ -156,16 +156,21 @@ inline bool rows_on(const SeqView& v, int unit, int elem_bytes)
 
 // Launches `kernel` and returns the launch's own status.
 template <class... P>
-lrs_status launch_seq(const char* nm, void (*kernel)(P...), uint64_t blocks, int threads,
+lrs_status launch_seq(const char* nm, void (*kernel)(P...), dim3 blocks, int threads,
                       hipStream_t stream, P... params)
 {
     void* ptrs[] = {(void*)&params...};
-    const hipError_t e = hipLaunchKernel((const void*)kernel, dim3((uint32_t)blocks), dim3(threads),
-                                         ptrs, 0, stream);
+    const hipError_t e = hipLaunchKernel((const void*)kernel, blocks, dim3(threads), ptrs, 0, stream);
     if (e != hipSuccess)
         return fail(LRS_ERR_HIP, "%s: kernel launch failed: %s", nm, hipGetErrorString(e));
     g_err[0] = '\0';
     return LRS_OK;
+}
+template <class... P>
+lrs_status launch_seq(const char* nm, void (*kernel)(P...), uint64_t blocks, int threads,
+                      hipStream_t stream, P... params)
+{
+    return launch_seq(nm, kernel, dim3((uint32_t)blocks), threads, stream, params...);
 }
 
 }  // namespace lrs

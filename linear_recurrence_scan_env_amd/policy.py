@@ -170,7 +170,7 @@ class _ActionLogProbs(torch.autograd.Function):
 
 def action_log_probs(logits, actions, *, mask=None, temperature=1.0):
     """compute_action_log_probs for autograd: returns (log_probs, entropy), both
-    differentiable in the logits."""
+    differentiable in the logits.  In graphs as policy_loss is."""
     return _ActionLogProbs.apply(logits, actions, mask, temperature)
 
 
@@ -196,7 +196,10 @@ class _PolicyLoss(torch.autograd.Function):
 def policy_loss(logits, actions, old_log_probs, advantages, *, ref_log_probs=None, mask=None, clip=0.2,
                 clip_high=None, kl_coef=0.0, entropy_coef=0.0, temperature=1.0):
     """compute_policy_loss for autograd: returns (loss, log_probs, entropy), the
-    loss differentiable in the logits, the others for the record."""
+    loss differentiable in the logits, the others for the record.  To capture
+    both directions into a graph, call the compute_ functions, or first drop
+    every eager result of the same logits: torch does not capture a backward
+    pass beside those."""
     coefs = dict(clip=clip, clip_high=clip_high, kl_coef=kl_coef, entropy_coef=entropy_coef,
                  temperature=temperature)
     return _PolicyLoss.apply(logits, actions, old_log_probs, advantages, ref_log_probs, mask, coefs)

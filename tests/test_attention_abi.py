@@ -224,3 +224,12 @@ def test_reference_policy_loss_against_differences(kl, ent):
         e = e.view(z.shape)
         d = (total(z + e) - total(z - e)) / (2 * h)
         assert abs(d - float(grad.reshape(-1)[i])) <= 1e-6 * (1 + abs(d))
+
+
+def test_attention_limits(lib):
+    assert forward(lib, tk=(1 << 29) + 1) == 1 and b"2^29" in lib.lrs_last_error()
+    far = [ctypes.c_void_p(i << 40) for i in range(1, 7)]
+    many = dict(n=1 << 24, t=33, tk=33, h=1, kv=1, dk=1, dv=1, q=far[0], k=far[1], v=far[2], out=far[3], lse=far[4])
+    assert forward(lib, **many) == 1 and b"too large" in lib.lrs_last_error()
+    many.update(t=1, tk=1, reset=far[5], ws=ctypes.c_void_p(7 << 40), wsb=1 << 30, n=1 << 24)
+    assert forward(lib, **many) == 1 and b"too large" in lib.lrs_last_error()
