@@ -690,9 +690,8 @@ constexpr int kGradSets = sizeof(D) == 4 ? 1 : 2;
 template <class D, int W>
 constexpr int kAttBlocks = sizeof(D) == 4 && W == 128 ? 1 : 2;  // blocks per CU
 
-// A block's place: its heads, and the steps of its four waves.  Alone: each wave has a
-// head and tiles of its own (rows of up to 32 steps, of which a block would use one
-// wave: 2930 x 2 steps of 9 heads, bf16, forward 258 us with blocks and 75 alone).
+// A block's place: its heads, and the steps of its four waves.  Alone: each wave has 32
+// steps of a head and tiles of its own.
 struct AttBlock {
     int64_t n;
     int head, step0, first, last, kvh;
@@ -702,14 +701,15 @@ struct AttBlock {
     {
         any = true;
         if (alone) {
-            const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-            any = id < x.N * x.H;
-            n = id / x.H;
-            head = (int)(id - n * x.H);
+            const uint32_t id = by_xcd(blockIdx.x, gridDim.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+            const uint32_t row = id / x.tiles;
+            any = row < x.N * x.H;
+            n = row / x.H;
+            head = row % x.H;
             kvh = head / x.group;
-            step0 = 0;
-            first = x.TK - x.T;
-            last = x.TK - 1;
+            step0 = (id - row * x.tiles) * 32;
+            first = x.TK - x.T + step0;
+            last = min(first + 32, x.TK) - 1;
             return;
         }
         const uint32_t id = by_xcd(blockIdx.x, gridDim.x);
@@ -725,10 +725,11 @@ struct AttBlock {
     }
 };
 
-// Goes over the tiles of keys and values that a block's queries see: compute(by_row,
-// by_col, is_far, j0, j1) for each, with a lane's places in the keys' tile (the values'
-// lies kBytes behind).  kSets: how many tiles are on their way from memory.
-template <class D, int W, int BK, int kBy, class Compute>
+// Goes over the tiles of keys and values that a wave's queries see, in tiles of its own:
+// compute() as in over_keys.  kAhead: the next tile is on its way while one is computed
+// (the forward; dq and attend_dkv would spill registers: both directions of 64 x 512 f32
+// steps of 4 heads of 64 took 490 us with it, 373 with blocks).
+template <class D, int W, int BK, int kBy, bool kAhead, class Compute>
 __device__ __forceinline__ void over_keys_alone(const AttArgs& x, const AttBlock& b, const KeyTiles& kt, char* lds,
                                                 int lane, Compute compute)
 {
@@ -737,7 +738,7 @@ __device__ __forceinline__ void over_keys_alone(const AttArgs& x, const AttBlock
     sk.start(x.k, x.dim_k);
     sv.start(x.v, x.dim_v);
     const uint32_t at = lds_address(lds), put_at = sk.lane(at);
-    for (int it = 0; it < kt.tiles; ++it) {
+    auto fetch = [&](int it) {
         int j0, j1;
         kt.get(it, BK, j0, j1);
         if (it == 0 || it == kt.far_tiles) {
@@ -746,14 +747,24 @@ __device__ __forceinline__ void over_keys_alone(const AttArgs& x, const AttBlock
         }
         sk.fetch(j1 - j0);
         sv.fetch(j1 - j0);
+    };
+    if (kAhead) fetch(0);
+    for (int it = 0; it < kt.tiles; ++it) {
+        if (!kAhead) fetch(it);
         sk.put(put_at);
         sv.put(put_at + BK * Tile::kRow);
+        if (kAhead && it + 1 < kt.tiles) fetch(it + 1);
         __builtin_amdgcn_wave_barrier();
+        int j0, j1;
+        kt.get(it, BK, j0, j1);
         compute(at + Tile::row_lane(lane), at + Tile::column_lane(lane), it < kt.far_tiles, j0, j1);
         __builtin_amdgcn_wave_barrier();
     }
 }
 
+// Goes over the tiles of keys and values that a block's queries see: compute(by_row,
+// by_col, is_far, j0, j1) for each, with a lane's places in the keys' tile (the values'
+// lies kBytes behind).  kSets: how many tiles are on their way from memory.
 template <class D, int W, int BK, int kBy, int kSets, class Compute>
 __device__ __forceinline__ void over_keys(const AttArgs& x, const AttBlock& b, const KeyTiles& kt, char* lds, int lane,
                                           Compute compute)
@@ -875,8 +886,8 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_forward(const 
             }
     };
     if constexpr (kAlone)
-        over_keys_alone<D, W, BK, kBy>(x, b, kt, lds[__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)][0], lane,
-                                       compute);
+        over_keys_alone<D, W, BK, kBy, true>(x, b, kt, lds[__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)][0],
+                                              lane, compute);
     else over_keys<D, W, BK, kBy, kKeySets<D, W>>(x, b, kt, lds[0][0], lane, compute);
     if (!wq.any()) return;
     l += __shfl_xor(l, 32);
@@ -953,8 +964,8 @@ __global__ __launch_bounds__(256, (kAttBlocks<D, W>)) void attend_dq(const AttAr
         }
     };
     if constexpr (kAlone)
-        over_keys_alone<D, W, BK, kBy>(x, b, kt, lds[__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)][0], lane,
-                                       compute);
+        over_keys_alone<D, W, BK, kBy, false>(x, b, kt, lds[__builtin_amdgcn_readfirstlane(threadIdx.x / kWave)][0],
+                                              lane, compute);
     else over_keys<D, W, BK, kBy, kGradSets<D, W>>(x, b, kt, lds[0][0], lane, compute);
     if constexpr (kSum) {
         sum += __shfl_xor(sum, 32);
@@ -1120,7 +1131,7 @@ __device__ __forceinline__ int seen_until(const AttArgs& x, int64_t n, int j)
 
 // Keys are the columns: a wave holds 32 of them and their values, a block 128;
 // queries and their gradients come in tiles, head after head of the group.  Alone:
-// rows of up to 32 keys, each wave with a head of its own.
+// each wave has its own tiles.
 template <class D, int W, int kBy, bool kK, bool kV, bool kAlone>
 __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void attend_dkv(const AttArgs x)
 {
@@ -1132,12 +1143,14 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
     const int lane = threadIdx.x % kWave, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int past = x.TK - x.T, kv = x.H / x.group;
-    const int64_t id = kAlone ? (int64_t)blockIdx.x * 4 + wave : (int64_t)by_xcd(blockIdx.x, gridDim.x);
-    const int64_t row_of = kAlone ? id : id / x.tiles, n = row_of / kv;
-    const int kvh = (int)(row_of - n * kv);
+    const uint32_t block = by_xcd(blockIdx.x, gridDim.x), id = kAlone ? block * 4 + wave : block;
+    const uint32_t row_of = id / x.tiles;
+    const int64_t n = row_of / kv;
+    const int kvh = row_of % kv;
     if (kAlone && n >= x.N) return;
-    const int j0 = kAlone ? 0 : (int)(id - row_of * x.tiles) * 128, j1 = min(j0 + 128, x.TK);
-    const int mine0 = kAlone ? 0 : j0 + 32 * wave, j = mine0 + (lane & 31);
+    constexpr int kKeys = kAlone ? 32 : 128;
+    const int j0 = (int)(id - row_of * x.tiles) * kKeys, j1 = min(j0 + kKeys, x.TK);
+    const int mine0 = kAlone ? j0 : j0 + 32 * wave, j = mine0 + (lane & 31);
     const bool valid = j < x.TK;
     OwnRows<D, W, kBy> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
@@ -1165,14 +1178,16 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
         QueryStage<D, W, kBy, BQ, kWave> stage;
         stage.start(x);
         const uint32_t at = lds_address(lds[wave]), put_at = stage.q.lane(at);
-        for (int head = kvh * x.group; head < (kvh + 1) * x.group; ++head) {
-            if (begin < end) stage.place(x, n, head, begin - past);
+        for (int head = kvh * x.group; total > 0 && head < (kvh + 1) * x.group; ++head) {
+            stage.place(x, n, head, begin - past);
             for (int i = begin; i < end; i += BQ) {
                 stage.fetch(end - i);
                 stage.put(put_at, kBytes, rows[wave]);
                 __builtin_amdgcn_wave_barrier();
+                const bool whole = mine0 + 31 <= i && i + 32 <= least;
                 add_queries<D, W, kBy, kK, kV>(x, at + Tile::row_lane(lane), at + Tile::column_lane(lane), kBytes,
-                                               rows[wave], 0, k, v, false, row_bits(j, until, i, h), lane, dk, dv);
+                                               rows[wave], 0, k, v, whole, whole ? 0 : row_bits(j, until, i, h), lane,
+                                               dk, dv);
                 __builtin_amdgcn_wave_barrier();
             }
         }
@@ -1751,23 +1766,48 @@ inline lrs_status launch_starts(const char* nm, const AttArgs& x, const SeqView&
 // Blocks of 256 threads: a grid holds fewer than 2^32.
 constexpr uint64_t kMaxGrid = 0xffffff;
 
-// Whether there are waves enough for the chip with a head to each.
-inline bool queries_alone(const AttArgs& x) { return x.T <= 32 && x.hpb < 4 && x.N * x.H >= 2048; }
-inline bool keys_alone(const AttArgs& x) { return x.TK <= 32 && x.N * (x.H / x.group) >= 2048; }
-
-// Blocks of the forward and of dq: 128 queries of hpb heads.
-inline uint64_t query_blocks(AttArgs& x)
+// Whether each wave has 32 queries (or keys) and their tiles to itself.  A block of four
+// waves loads a tile once for all of them, but waits with all of them where one has none
+// of it: with rows of up to 32 steps it has work for one wave, and with windows that are
+// short beside its 128 steps each wave sits out half of the tiles.  There must be waves
+// enough for the chip.  us with blocks and alone:
+//   short rows, bf16: 2930 x 2 steps of 9 heads of 96 and 80 forward 254 and 63; both
+//   directions of 1000 x 20 of 3 heads of 128 155 and 90, of 4096 x 32 of one head of 64
+//   107 and 61, of 683 x 32 of 3 heads 63 and 38
+//   forward, 64 x 512 of 4 heads of 64, windows 32, 128 and 256: bf16 21.3 and 18.8, 23.6
+//   and 23.2, 27.5 and 28.5; f32 59 and 44, 87 and 67, 120 and 98 (512: 143 and 139)
+//   dq, of both directions at the same sizes and windows: bf16 100 and 96, 109 and 104, 127
+//   and 125; f32 339 and 316, 432 and 400, 586 and 555
+//   dk and dv, likewise: f32 317 and 313, 401 and 393, 556 and 511, with 256 x 128 queries
+//   over 192 keys (of which blocks fill three in four) 311 and 250; bf16 the same within
+//   2% at dims of 64 and 0.9 times as fast at 128
+// Rows of up to 128 steps are one block of which no wave sits out much: within 5%.
+inline bool queries_alone(const AttArgs& x, int window)
 {
-    if (queries_alone(x)) return ((uint64_t)x.N * (uint64_t)x.H + 3) / 4;
-    const int rows = 4 / x.hpb * 32;
-    x.tiles = (x.T + rows - 1) / rows;
-    return (uint64_t)x.N * (uint64_t)(x.H / x.hpb) * (uint64_t)x.tiles;
+    if (x.hpb == 4 || x.N * x.H * ((x.T + 31) / 32) < 2048) return false;
+    return x.T <= 32 || (x.TK > 128 && x.window <= window);
 }
-inline uint64_t key_blocks(AttArgs& x)
+inline bool forward_alone(const AttArgs& x, int size) { return queries_alone(x, size == 4 ? x.TK : 128); }
+inline bool dq_alone(const AttArgs& x, int size) { return queries_alone(x, size == 4 ? 256 : 128); }
+inline bool keys_alone(const AttArgs& x, int size)
 {
-    if (keys_alone(x)) return ((uint64_t)x.N * (uint64_t)(x.H / x.group) + 3) / 4;
-    x.tiles = (x.TK + 127) / 128;
-    return (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.tiles;
+    if (x.N * (x.H / x.group) * ((x.TK + 31) / 32) < 2048) return false;
+    return x.TK <= 32 || (size == 4 && x.TK > 128 && x.window <= 256 && x.sinks <= kFarSinks);
+}
+
+// Blocks of the forward and of dq: 128 queries of hpb heads, or 32 of a head for each wave.
+inline uint64_t query_blocks(AttArgs& x, bool alone)
+{
+    const int rows = alone ? 32 : 4 / x.hpb * 32;
+    x.tiles = (x.T + rows - 1) / rows;
+    return alone ? ((uint64_t)x.N * (uint64_t)x.H * (uint64_t)x.tiles + 3) / 4
+                 : (uint64_t)x.N * (uint64_t)(x.H / x.hpb) * (uint64_t)x.tiles;
+}
+inline uint64_t key_blocks(AttArgs& x, bool alone)
+{
+    x.tiles = (x.TK + (alone ? 31 : 127)) / (alone ? 32 : 128);
+    const uint64_t blocks = (uint64_t)x.N * (uint64_t)(x.H / x.group) * (uint64_t)x.tiles;
+    return alone ? (blocks + 3) / 4 : blocks;
 }
 
 // Blocks of attend_far.
@@ -1806,16 +1846,17 @@ lrs_status launch_dkv(const char* nm, AttArgs x, hipStream_t stream)
 {
     if (x.far_part != nullptr)
         LRS_TRY(launch_seq(nm, attend_far<D, W, kBy, kK, kV>, far_blocks(x), 256, stream, x));
-    const uint64_t blocks = key_blocks(x);
-    return launch_seq(nm, keys_alone(x) ? attend_dkv<D, W, kBy, kK, kV, true> : attend_dkv<D, W, kBy, kK, kV, false>,
+    const bool alone = keys_alone(x, sizeof(D));
+    const uint64_t blocks = key_blocks(x, alone);
+    return launch_seq(nm, alone ? attend_dkv<D, W, kBy, kK, kV, true> : attend_dkv<D, W, kBy, kK, kV, false>,
                       blocks, 256, stream, x);
 }
 
 template <class D, int W, int kBy>
 lrs_status launch_backward(const char* nm, AttArgs x, hipStream_t stream)
 {
-    const uint64_t blocks = query_blocks(x);
-    const bool alone = queries_alone(x);
+    const bool alone = dq_alone(x, sizeof(D));
+    const uint64_t blocks = query_blocks(x, alone);
     if (x.sum_delta)
         LRS_TRY(launch_seq(nm, alone ? attend_dq<D, W, kBy, true, true> : attend_dq<D, W, kBy, true, false>, blocks, 256,
                            stream, x));
@@ -1859,12 +1900,13 @@ lrs_status attention_entry(const char* nm, int64_t N, int64_t T, int64_t TK, int
     set_vec(x.k, dk, s);
     set_vec(x.v, dv, s);
     set_vec(x.o, dv, s);
-    const uint64_t blocks = query_blocks(x);
+    const bool alone = forward_alone(x, s);
+    const uint64_t blocks = query_blocks(x, alone);
     LRS_REQUIRE(blocks <= kMaxGrid && (reset == nullptr || (uint64_t)N <= kMaxGrid), "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[3], stream));
     return with_sizes<D>(dk, dv, rows_by({&x.q, &x.k, &x.v, &x.o}, dk, dv, s), [&](auto w, auto by) {
         constexpr int W = decltype(w)::value, B = decltype(by)::value;
-        return launch_seq(nm, queries_alone(x) ? attend_forward<D, W, B, true> : attend_forward<D, W, B, false>, blocks,
+        return launch_seq(nm, alone ? attend_forward<D, W, B, true> : attend_forward<D, W, B, false>, blocks,
                           256, stream, x);
     });
 }
@@ -1906,7 +1948,7 @@ lrs_status attention_backward_entry(const char* nm, int64_t N, int64_t T, int64_
     x.dv = a[9];
     for (SeqView* w : {&x.q, &x.k, &x.dq, &x.dk}) set_vec(*w, dk, s);
     for (SeqView* w : {&x.v, &x.o, &x.dout, &x.dv}) set_vec(*w, dv, s);
-    LRS_REQUIRE(query_blocks(x) <= kMaxGrid && key_blocks(x) <= kMaxGrid && far_blocks(x) <= kMaxGrid &&
+    LRS_REQUIRE(query_blocks(x, dq_alone(x, s)) <= kMaxGrid && key_blocks(x, keys_alone(x, s)) <= kMaxGrid && far_blocks(x) <= kMaxGrid &&
                     (reset == nullptr || (uint64_t)N <= kMaxGrid / 2),
                 "%s: num_envs * heads * steps is too large", nm);
     LRS_TRY(launch_starts(nm, x, a[4], stream));

@@ -79,6 +79,18 @@ def test_many_short_rows(dt, case):
     compare(got, ref.attention(q, k, v, window, sinks, reset, do=do))
 
 
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("case", [(420, 150, 1, 1, 16, 8, 45, 20, 3, 0.02), (150, 200, 2, 1, 64, 40, 0, 60, 2, 0.01),
+                                  (120, 300, 2, 2, 72, 72, 0, 100, 70, 0.01), (125, 520, 1, 1, 16, 128, 3, 30, 4, 0.004),
+                                  (60, 400, 3, 3, 128, 128, 0, 250, 0, 0.02), (410, 160, 1, 1, 20, 20, 0, 1000, 5, 0.03)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_many_rows_each_wave_alone(dt, case):
+    n, t, heads, kv, dk, dv, past, window, sinks, reset_p = case
+    q, k, v, do, reset = inputs(6, dt, n, t, heads, kv, dk, dv, past, reset_p)
+    got = run_all(q, k, v, do, window=window, sinks=sinks, reset=reset)
+    compare(got, ref.attention(q, k, v, window, sinks, reset, do=do))
+
+
 @pytest.mark.parametrize("begins", [[250, 330], [255], [256], [257, 511, 512], [200, 300], [192, 700]])
 @pytest.mark.parametrize("window,sinks", [(7, 33), (100, 64), (300, 3)])
 def test_first_steps_around_chunks(begins, window, sinks):
