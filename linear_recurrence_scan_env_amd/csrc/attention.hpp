@@ -1282,7 +1282,7 @@ __global__ __launch_bounds__(256, (sizeof(D) == 4 && W == 128 ? 1 : 2)) void att
 // What the queries of one chunk beyond its window give to 32 first steps of the
 // episode that the chunk begins in the middle of, summed over the heads that share
 // them: a quarter of the chunk to each wave, joined through LDS.
-template <class D, int W, int kBy, bool kK, bool kV>
+template <class D, int W, int kBy>
 __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
 {
     using Tile = AttTile<D, W>;
@@ -1309,7 +1309,7 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
     OwnRows<D, W, kBy> k, v;
     k.load(x.k, n, min(j, x.TK - 1), kvh, x.dim_k, valid, lane);
     k.signs(x.scale < 0.0f);
-    if constexpr (kK) v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
+    v.load(x.v, n, min(j, x.TK - 1), kvh, x.dim_v, valid, lane);
     const int begin = max(max(i0 + wave * kPart, past), first + 32 * part + x.window);
     const int end = min(min(i1, i0 + (wave + 1) * kPart), x.ends != nullptr ? x.ends[n * x.TK + first] : x.TK);
     f32x16 dk[W / 32] = {}, dv[W / 32] = {};
@@ -1323,7 +1323,7 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
             stage.fetch(end - i);
             stage.put(put_at, kBytes, rows[wave]);
             __builtin_amdgcn_wave_barrier();
-            add_queries<D, W, kBy, kK, kV>(x, by_row, by_col, kBytes, rows[wave], 0, k, v, false,
+            add_queries<D, W, kBy, true, true>(x, by_row, by_col, kBytes, rows[wave], 0, k, v, false,
                                              valid ? row_bits(j + x.window, end, i, h) : 0, lane, dk, dv);
             __builtin_amdgcn_wave_barrier();
         }
@@ -1350,8 +1350,8 @@ __global__ __launch_bounds__(256, 1) void attend_far(const AttArgs x)
             *reinterpret_cast<f32x4*>(to + from + 32 * dt + 8 * wave + 4 * h) = sum;
         }
     };
-    if constexpr (kK) join(dk, 0);
-    if constexpr (kV) join(dv, W);
+    join(dk, 0);
+    join(dv, W);
 }
 
 // The first step of each step's episode and the step behind its last, [N, TK]: a
@@ -1844,8 +1844,6 @@ lrs_status with_sizes(int64_t dk, int64_t dv, int by, F f)
 template <class D, int W, int kBy, bool kK, bool kV>
 lrs_status launch_dkv(const char* nm, AttArgs x, hipStream_t stream)
 {
-    if (x.far_part != nullptr)
-        LRS_TRY(launch_seq(nm, attend_far<D, W, kBy, kK, kV>, far_blocks(x), 256, stream, x));
     const bool alone = keys_alone(x, sizeof(D));
     const uint64_t blocks = key_blocks(x, alone);
     return launch_seq(nm, alone ? attend_dkv<D, W, kBy, kK, kV, true> : attend_dkv<D, W, kBy, kK, kV, false>,
@@ -1862,6 +1860,8 @@ lrs_status launch_backward(const char* nm, AttArgs x, hipStream_t stream)
                            stream, x));
     LRS_TRY(launch_seq(nm, alone ? attend_dq<D, W, kBy, false, true> : attend_dq<D, W, kBy, false, false>, blocks, 256,
                        stream, x));
+    if (x.far_part != nullptr)
+        LRS_TRY(launch_seq(nm, attend_far<D, W, kBy>, far_blocks(x), 256, stream, x));
     if constexpr (kSplitGrads<D, W>) {
         LRS_TRY((launch_dkv<D, W, kBy, true, false>(nm, x, stream)));
         return launch_dkv<D, W, kBy, false, true>(nm, x, stream);
