@@ -11,7 +11,7 @@
 //     dz_v = (c (1[v = a] - p_v) - h p_v (log p_v + H)) / temperature.
 //
 // One pass over the logits: a row of the vocabulary is held in the registers of
-// the lanes that share it (8 lanes for 18 actions, a block of 1024 for 131072 in
+// the lanes that share it (2 or 8 lanes for 18 actions, a block of 1024 for 131072 in
 // 16 bits), so that the loss and its gradient read it once; longer rows are read
 // again.  Memory is all that it should cost.
 #pragma once
@@ -585,6 +585,14 @@ inline void join_rows(PolicyArgs& x)
     x.T = x.rows;
 }
 
+// Short rows of many tokens take few lanes with more units each, so that a wave has more
+// tokens and their divisions, logarithms and sums over lanes count less.  Few tokens take
+// a lane to a unit, which ends sooner.  us of the loss and its gradient in f32, with lanes
+// for units and with few, 524288 tokens: 4 actions 19.6 and 8.5, 18 actions 38 and 23, 30
+// actions 65 and 33, 60 actions 76 and 61, 120 actions 106 and 109; 8192 tokens: 18 actions
+// 3.7 and 4.7, 60 actions 4.0 and 4.9.
+constexpr int64_t kManyTokens = 65536;
+
 template <class D, bool kGrad>
 lrs_status launch_policy(const char* nm, PolicyArgs x, hipStream_t stream)
 {
@@ -592,23 +600,27 @@ lrs_status launch_policy(const char* nm, PolicyArgs x, hipStream_t stream)
     const int64_t units = row_units<D>(x.z, x.V);
     void (*kernel)(PolicyArgs) = policy_stream<D, kGrad>;
     int lanes = kStreamLanes;
-#define LRS_POLICY(most, l, u)                 \
-    if (units <= most) {                       \
+    const bool many = x.rows >= kManyTokens;
+#define LRS_POLICY(most, l, u, when)           \
+    if (units <= most && when) {               \
         kernel = policy_rows<D, l, u, kGrad>;  \
         lanes = l;                             \
     } else
-    LRS_POLICY(4, 4, 1)
-    LRS_POLICY(8, 8, 1)
-    LRS_POLICY(16, 16, 1)
-    LRS_POLICY(32, 16, 2)
-    LRS_POLICY(64, 16, 4)
-    LRS_POLICY(128, 32, 4)
-    LRS_POLICY(256, 64, 4)
-    LRS_POLICY(1024, 256, 4)
-    LRS_POLICY(2048, 256, 8)
-    LRS_POLICY(4096, 256, 16)
-    LRS_POLICY(8192, 512, 16)
-    LRS_POLICY(16384, 1024, 16) {}
+    LRS_POLICY(4, 1, 4, many)
+    LRS_POLICY(8, 2, 4, many)
+    LRS_POLICY(16, 4, 4, many)
+    LRS_POLICY(4, 4, 1, true)
+    LRS_POLICY(8, 8, 1, true)
+    LRS_POLICY(16, 16, 1, true)
+    LRS_POLICY(32, 16, 2, true)
+    LRS_POLICY(64, 16, 4, true)
+    LRS_POLICY(128, 32, 4, true)
+    LRS_POLICY(256, 64, 4, true)
+    LRS_POLICY(1024, 256, 4, true)
+    LRS_POLICY(2048, 256, 8, true)
+    LRS_POLICY(4096, 256, 16, true)
+    LRS_POLICY(8192, 512, 16, true)
+    LRS_POLICY(16384, 1024, 16, true) {}
 #undef LRS_POLICY
     const int block = lanes > kWave ? lanes : 256;
     const int64_t per = block / lanes;
@@ -622,7 +634,11 @@ lrs_status launch_policy_backward(const char* nm, PolicyArgs x, hipStream_t stre
     const int64_t units = row_units<D>(x.z, x.V);
     void (*kernel)(PolicyArgs) = policy_backward<D, 256>;
     int lanes = 256;
-    if (units <= 8) { kernel = policy_backward<D, 8>; lanes = 8; }
+    // many tokens: as in launch_policy (loss and then gradient, as above: 18 actions 48 and 36, 30
+    // actions 81 and 47, 60 actions 87 and 73)
+    if (units <= 8 && x.rows >= kManyTokens) { kernel = policy_backward<D, 2>; lanes = 2; }
+    else if (units <= 8) { kernel = policy_backward<D, 8>; lanes = 8; }
+    else if (units <= 16 && x.rows >= kManyTokens) { kernel = policy_backward<D, 4>; lanes = 4; }
     else if (units <= 32) { kernel = policy_backward<D, 16>; lanes = 16; }
     else if (units <= 512) { kernel = policy_backward<D, 64>; lanes = 64; }
     // four units to a lane

@@ -62,6 +62,12 @@ def test_against_definition(dt, n, t, V):
 
 
 @pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("V", [1, 6, 18, 33, 55, 110])
+def test_many_tokens(dt, V):
+    check_all(inputs(2, dt, 2, 32800, V))
+
+
+@pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("kw", [dict(kl=0.0, ent=0.0), dict(kl=-0.1, ent=-0.2), dict(temperature=0.5),
                                 dict(temperature=3.0, ent=0.0), dict(mask=False)])
 def test_coefficients(dt, kw):
