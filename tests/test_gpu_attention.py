@@ -397,3 +397,30 @@ def test_step_graph():
         torch.cuda.synchronize()
         want = lrs.compute_windowed_attention_step(q, k, v, wk, wv, pos, sinks=4)
         assert torch.equal(out, want) and torch.equal(kc, wk) and torch.equal(vc, wv), i
+
+
+def test_two_graphs_at_once():
+    # each has a workspace of its own: episodes, D, sums of far queries, splits of a step
+    runs = []
+    for seed in (30, 31):
+        q, k, v, do, reset = inputs(seed, "bf16", 2, 900, 4, 2, 128, 128, reset_p=0.003)
+        kw = dict(window=50, sinks=3, reset=reset)
+        gen = torch.Generator().manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=gen).bfloat16().cuda()  # noqa: E731
+        step = (r(2, 8, 64), r(2, 2, 64), r(2, 2, 64), r(2, 3000, 2, 64), r(2, 3000, 2, 64),
+                torch.tensor([2999, 7000], dtype=torch.int32, device="cuda"))
+        call = lambda a=(q, k, v, do), kw=kw, step=step: dict(  # noqa: E731
+            run_all(*a, **kw), step=lrs.compute_windowed_attention_step(*step, sinks=4))
+        want = call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        runs.append((graph, got, want, torch.cuda.Stream(), call))  # (call holds the inputs)
+    torch.cuda.synchronize()
+    for i in range(3):
+        for graph, _, _, stream, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, got, want, _, _ in runs:
+            assert [x for x in want if not torch.equal(got[x], want[x])] == [], i
